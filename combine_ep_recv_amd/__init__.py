@@ -1,6 +1,6 @@
 """MoE token dispatch / combine on MI355X: thin Python binding over libmoe_ep.so.
 
-Every step of the path runs in the HIP kernels of ``csrc/moe_ep.hip``; this
+Every step of the path runs in the HIP kernels of ``csrc/``; this
 module only allocates outputs with torch (device memory + the current stream)
 and marshals pointers to the C ABI of ``include/moe_ep.h``. There is no CPU
 fallback: importing works without the library, but any call raises when
@@ -11,6 +11,14 @@ or ``__graft_entry__.build()``).
         x, expert_ids, ep_world, experts_per_rank, quant_mode=0)
     x_out = combine(expand_x, assist_info, ep_recv_count, expert_ids,
                     expert_scales, ep_world, experts_per_rank)
+
+Around them: ``gate`` makes expert_ids and expert_scales from a router's logits
+(``gate_backward`` its gradient), and ``quantize_mx`` / ``expert_product`` run
+the experts on microscaled rows and 4-bit weights:
+
+    expert_ids, expert_scales = gate(logits, topk)
+    rows, row_scales, assist_info, ep_recv_count = dispatch(..., quant_mode=MOE_QUANT_MX)
+    y = expert_product(rows, row_scales, weights, weight_scales, ep_recv_count)
 """
 from __future__ import annotations
 
@@ -25,13 +33,18 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_ep.s
 MOE_OK = 0
 (MOE_ERR_NULLPTR, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_QUANT, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH, MOE_ERR_SCHEDULE,
  MOE_ERR_ALIGN, MOE_ERR_MASK) = range(1, 10)
-MOE_INT32, MOE_FP16, MOE_BF16 = 0, 1, 2
+MOE_INT32, MOE_FP16, MOE_BF16, MOE_FP32 = 0, 1, 2, 3
 MOE_QUANT_NONE, MOE_QUANT_STATIC, MOE_QUANT_DYN_TOKEN, MOE_QUANT_DYN_GROUP, MOE_QUANT_MX = 0, 1, 2, 3, 4
 MOE_SCHED_TOKEN, MOE_SCHED_SEGMENT, MOE_SCHED_ADAPTIVE = 0, 1, 2
 MOE_MASK_NONE, MOE_MASK_TOKEN, MOE_MASK_PAIR = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
+MOE_MX_E2M1, MOE_MX_E4M3 = 0, 1
+MOE_ACT_NONE, MOE_ACT_SWIGLU = 0, 1
 
 EXPORTS = ("moe_dispatch_workspace_size", "moe_dispatch", "moe_dispatch_noalloc", "moe_combine_workspace_size",
-           "moe_combine", "moe_status_str")
+           "moe_combine", "moe_gate", "moe_gate_backward", "moe_mx_quantize", "moe_mx_dequantize",
+           "moe_expert_product", "moe_status_str")
 NOALLOC_SCRATCH_BYTES = 32 << 20      # MOE_NOALLOC_SCRATCH_BYTES
 
 
@@ -94,6 +107,17 @@ def library() -> ctypes.CDLL:
     lib.moe_combine.argtypes = [P, P, P, P, P, P, I, ctypes.POINTER(MoeSpecialExperts), I, I, I, I, I, I, P, P,
                                 SZ, P]
     lib.moe_combine.restype = I
+    F, L = ctypes.c_float, ctypes.c_int64
+    lib.moe_gate.argtypes = [P, P, P, I, I, I, I, I, I, I, I, I, F, P, P, P, P]
+    lib.moe_gate.restype = I
+    lib.moe_gate_backward.argtypes = [P, P, P, P, I, I, I, I, I, I, F, P, P]
+    lib.moe_gate_backward.restype = I
+    lib.moe_mx_quantize.argtypes = [P, L, I, I, I, P, P, P]
+    lib.moe_mx_quantize.restype = I
+    lib.moe_mx_dequantize.argtypes = [P, P, L, I, I, I, P, P]
+    lib.moe_mx_dequantize.restype = I
+    lib.moe_expert_product.argtypes = [P, P, I, P, P, P, I, I, I, I, I, I, I, P, P]
+    lib.moe_expert_product.restype = I
     lib.moe_status_str.argtypes = [I]
     lib.moe_status_str.restype = ctypes.c_char_p
     _lib = lib
@@ -418,3 +442,253 @@ def combine(expand_x: torch.Tensor, assist_info: torch.Tensor, ep_recv_count: to
     return combine_into(x_out, expand_x, assist_info, ep_recv_count, expert_ids, expert_scales, ep_world,
                         experts_per_rank, x_active_mask=x_active_mask, zero_experts=zero_experts,
                         copy_experts=copy_experts, ori_x=ori_x, const_experts=const_experts, const_x=const_x)
+
+
+# ---- the gate ----
+
+def _launch(name: str, device, *args):
+    """Call the library with `device` current (a launch on a device's default stream goes to the current
+    device) and raise on an error status."""
+    f = getattr(library(), name)
+    if device.index is None or device.index == torch.cuda.current_device():
+        rc = f(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args)
+    _check(name, rc)
+
+
+def _float_code(name, dt: torch.dtype) -> int:
+    """moe_dtype of a floating tensor."""
+    if dt == torch.float32:
+        return MOE_FP32
+    if dt == torch.bfloat16:
+        return MOE_BF16
+    if dt == torch.float16:
+        return MOE_FP16
+    raise MoeError(name, MOE_ERR_DTYPE, "unsupported dtype %s" % dt)
+
+
+def _gate_shape(fn, logits, ids):
+    """(tokens, experts, topk, device) of a gate call."""
+    dev = _gpu_device("logits", logits)
+    if logits.dim() != 2 or not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise MoeError(fn, MOE_ERR_SHAPE, "logits and expert_ids must be 2-D")
+    N, E = logits.shape
+    _check_tensor("logits", logits, logits.dtype, (N, E), dev)
+    _check_tensor("expert_ids", ids, torch.int32, (N, ids.shape[1]), dev)
+    return N, E, ids.shape[1], dev
+
+
+def _byte_mask(name, mask, shape, device):
+    if (not isinstance(mask, torch.Tensor) or mask.dtype not in (torch.bool, torch.uint8) or mask.shape != shape
+            or mask.device != device or not mask.is_contiguous()):
+        raise MoeError(name, MOE_ERR_MASK, "%s must be a contiguous bool or uint8 tensor of shape %s on %s"
+                       % (name, tuple(shape), device))
+    return _ptr(mask)
+
+
+def gate_into(expert_ids: torch.Tensor, expert_scales: torch.Tensor, logits: torch.Tensor,
+              score: int = MOE_SCORE_SOFTMAX, bias: Optional[torch.Tensor] = None, groups: int = 1,
+              topk_groups: int = 1, group_score: int = MOE_GROUP_MAX, renormalize: bool = True, scale: float = 1.0,
+              token_mask: Optional[torch.Tensor] = None, pair_mask: Optional[torch.Tensor] = None):
+    """moe_gate into preallocated expert_ids [N, topk] int32, expert_scales [N, topk] fp32 and, when given,
+    pair_mask [N, topk] bool or uint8, on the current stream. See gate for the rest."""
+    N, E, K, dev = _gate_shape("moe_gate", logits, expert_ids)
+    dt = _float_code("moe_gate", logits.dtype)
+    _check_tensor("expert_scales", expert_scales, torch.float32, (N, K), dev)
+    if bias is not None:
+        _check_tensor("bias", bias, torch.float32, (E,), dev)
+    mp = None if token_mask is None else _byte_mask("token_mask", token_mask, (N,), dev)
+    pp = None if pair_mask is None else _byte_mask("pair_mask", pair_mask, (N, K), dev)
+    _launch("moe_gate", dev, _ptr(logits), _ptr(bias), mp, N, E, K, dt, int(score), int(groups), int(topk_groups),
+            int(group_score), int(bool(renormalize)), float(scale), _ptr(expert_ids), _ptr(expert_scales), pp,
+            _stream_ptr(dev))
+    return expert_ids, expert_scales
+
+
+def gate(logits: torch.Tensor, topk: int, score: int = MOE_SCORE_SOFTMAX, bias: Optional[torch.Tensor] = None,
+         groups: int = 1, topk_groups: int = 1, group_score: int = MOE_GROUP_MAX, renormalize: bool = True,
+         scale: float = 1.0, token_mask: Optional[torch.Tensor] = None, with_pair_mask: bool = False):
+    """Choose each token's experts and weights from a router's logits [N, E] (fp16, bf16 or fp32).
+
+    score: MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID. bias: fp32 [E], added to the scores for the choice
+    alone. groups > 1: only the experts of the topk_groups best groups can be chosen, a group being
+    worth its best expert (MOE_GROUP_MAX) or the sum of its two best (MOE_GROUP_TOP2). The weights are
+    the chosen scores, divided by their sum if renormalize, times scale.
+    Returns (expert_ids int32 [N, topk], expert_scales fp32 [N, topk]) and, with_pair_mask, a bool
+    [N, topk] that is False where there was no expert to choose (logits of -inf or NaN) or the token is
+    not in token_mask (bool or uint8 [N]); such pairs have id -1 and weight 0, and dispatch and combine
+    take the mask as x_active_mask. The outputs carry no autograd graph: gate_backward gives the
+    gradient of the logits.
+    """
+    dev = _gpu_device("logits", logits)
+    if logits.dim() != 2 or topk < 1:
+        raise MoeError("moe_gate", MOE_ERR_SHAPE, "logits must be 2-D and topk at least 1")
+    N = logits.shape[0]
+    ids = torch.empty((N, topk), dtype=torch.int32, device=dev)
+    w = torch.empty((N, topk), dtype=torch.float32, device=dev)
+    on = torch.empty((N, topk), dtype=torch.bool, device=dev) if with_pair_mask else None
+    gate_into(ids, w, logits, score, bias, groups, topk_groups, group_score, renormalize, scale, token_mask, on)
+    return (ids, w, on) if with_pair_mask else (ids, w)
+
+
+def gate_backward_into(grad_logits: torch.Tensor, logits: torch.Tensor, expert_ids: torch.Tensor,
+                       expert_scales: torch.Tensor, grad_scales: torch.Tensor, score: int = MOE_SCORE_SOFTMAX,
+                       renormalize: bool = True, scale: float = 1.0):
+    """moe_gate_backward into a preallocated grad_logits (logits' shape and dtype; every element is
+    written) on the current stream."""
+    N, E, K, dev = _gate_shape("moe_gate_backward", logits, expert_ids)
+    dt = _float_code("moe_gate_backward", logits.dtype)
+    _check_tensor("expert_scales", expert_scales, torch.float32, (N, K), dev)
+    _check_tensor("grad_scales", grad_scales, torch.float32, (N, K), dev)
+    _check_tensor("grad_logits", grad_logits, logits.dtype, (N, E), dev)
+    _launch("moe_gate_backward", dev, _ptr(logits), _ptr(expert_ids), _ptr(expert_scales), _ptr(grad_scales), N, E,
+            K, dt, int(score), int(bool(renormalize)), float(scale), _ptr(grad_logits), _stream_ptr(dev))
+    return grad_logits
+
+
+def gate_backward(logits: torch.Tensor, expert_ids: torch.Tensor, expert_scales: torch.Tensor,
+                  grad_scales: torch.Tensor, score: int = MOE_SCORE_SOFTMAX, renormalize: bool = True,
+                  scale: float = 1.0) -> torch.Tensor:
+    """Gradient of gate's logits from grad_scales, the gradient of its expert_scales: [N, E] in the
+    logits' dtype. expert_ids and expert_scales are gate's outputs for the same score, renormalize and
+    scale; pairs with id -1 give and get nothing."""
+    _gpu_device("logits", logits)
+    return gate_backward_into(torch.empty_like(logits, memory_format=torch.contiguous_format), logits, expert_ids,
+                              expert_scales, grad_scales, score, renormalize, scale)
+
+
+# ---- microscaled rows and the experts' product ----
+
+MX_BLOCK = 32                # elements that share a scale byte
+
+
+def _mx_codes(element):
+    """(torch dtype of the codes, codes a byte): E2M1 is packed two a byte in uint8."""
+    if element == MOE_MX_E2M1:
+        return torch.uint8, 2
+    if element == MOE_MX_E4M3:
+        return torch.float8_e4m3fn, 1
+    raise MoeError("element", MOE_ERR_QUANT, "unknown microscaled element type %r" % (element,))
+
+
+def _mx_rows(name, codes):
+    """(element, rows shape) of microscaled codes: float8_e4m3fn [..., cols] or packed uint8 [..., cols / 2]."""
+    if codes.dtype == torch.float8_e4m3fn:
+        return MOE_MX_E4M3, tuple(codes.shape)
+    if codes.dtype == torch.uint8:
+        return MOE_MX_E2M1, tuple(codes.shape[:-1]) + (2 * codes.shape[-1],)
+    raise MoeError(name, MOE_ERR_DTYPE, "microscaled codes are float8_e4m3fn or packed uint8, got %s" % codes.dtype)
+
+
+def _flat(shape):
+    n = 1
+    for v in shape:
+        n *= v
+    return n
+
+
+def quantize_mx_into(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor):
+    """moe_mx_quantize of x [..., cols] into preallocated codes (float8_e4m3fn [..., cols], or uint8
+    [..., cols / 2] for packed E2M1) and scales (uint8 [..., ceil(cols / 32)]), on the current stream."""
+    dev = _gpu_device("x", x)
+    _gpu_device("codes", codes)
+    if x.dim() < 1 or codes.dim() < 1:
+        raise MoeError("moe_mx_quantize", MOE_ERR_SHAPE, "x must have at least one dimension")
+    element, shape = _mx_rows("codes", codes)
+    dt = _float_code("moe_mx_quantize", x.dtype)
+    _check_tensor("x", x, x.dtype, shape, dev)
+    _check_tensor("codes", codes, codes.dtype, codes.shape, dev)
+    _check_tensor("scales", scales, torch.uint8, shape[:-1] + (-(-shape[-1] // MX_BLOCK),), dev)
+    _launch("moe_mx_quantize", dev, _ptr(x), _flat(shape[:-1]), shape[-1], dt, element, _ptr(codes), _ptr(scales),
+            _stream_ptr(dev))
+    return codes, scales
+
+
+def quantize_mx(x: torch.Tensor, element: int = MOE_MX_E2M1):
+    """Microscaled rows of x [..., cols] (fp16, bf16 or fp32; cols a multiple of 16): (codes, scales).
+    E2M1 codes are packed two a byte (uint8 [..., cols / 2], the even element in the low nibble), E4M3
+    ones are float8_e4m3fn [..., cols]; scales are E8M0 bytes, uint8 [..., ceil(cols / 32)], each the
+    power 2^(byte - 127) of a block of 32 elements. A block with an infinity or NaN gets byte 255 (NaN)."""
+    dev = _gpu_device("x", x)
+    dt, per = _mx_codes(element)
+    if x.dim() < 1 or x.shape[-1] < 1 or x.shape[-1] % 16:
+        raise MoeError("moe_mx_quantize", MOE_ERR_SHAPE, "the last dimension must be a multiple of 16")
+    lead, cols = tuple(x.shape[:-1]), x.shape[-1]
+    codes = torch.empty(lead + (cols // per,), dtype=dt, device=dev)
+    scales = torch.empty(lead + (-(-cols // MX_BLOCK),), dtype=torch.uint8, device=dev)
+    return quantize_mx_into(codes, scales, x)
+
+
+def dequantize_mx_into(out: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
+    """moe_mx_dequantize into a preallocated out [..., cols] (fp16, bf16 or fp32) on the current stream."""
+    dev = _gpu_device("codes", codes)
+    _gpu_device("out", out)
+    if codes.dim() < 1:
+        raise MoeError("moe_mx_dequantize", MOE_ERR_SHAPE, "codes must have at least one dimension")
+    element, shape = _mx_rows("codes", codes)
+    dt = _float_code("moe_mx_dequantize", out.dtype)
+    _check_tensor("codes", codes, codes.dtype, codes.shape, dev)
+    _check_tensor("scales", scales, torch.uint8, shape[:-1] + (-(-shape[-1] // MX_BLOCK),), dev)
+    _check_tensor("out", out, out.dtype, shape, dev)
+    _launch("moe_mx_dequantize", dev, _ptr(codes), _ptr(scales), _flat(shape[:-1]), shape[-1], dt, element,
+            _ptr(out), _stream_ptr(dev))
+    return out
+
+
+def dequantize_mx(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """What microscaled codes and scales stand for, code * 2^(byte - 127), in dtype."""
+    dev = _gpu_device("codes", codes)
+    if codes.dim() < 1:
+        raise MoeError("moe_mx_dequantize", MOE_ERR_SHAPE, "codes must have at least one dimension")
+    _float_code("moe_mx_dequantize", dtype)
+    return dequantize_mx_into(torch.empty(_mx_rows("codes", codes)[1], dtype=dtype, device=dev), codes, scales)
+
+
+def expert_product_into(out: torch.Tensor, x: torch.Tensor, x_scales: torch.Tensor, weights: torch.Tensor,
+                        weight_scales: torch.Tensor, ep_recv_count: torch.Tensor, activation: int = MOE_ACT_NONE):
+    """moe_expert_product into a preallocated out [rows, n] ([rows, n / 2] with MOE_ACT_SWIGLU) in fp16
+    or bf16, on the current stream. Rows behind the last that ep_recv_count counts are left as they were."""
+    dev = _gpu_device("x", x)
+    _gpu_device("weights", weights)
+    _gpu_device("ep_recv_count", ep_recv_count)
+    _gpu_device("out", out)
+    if x.dim() != 2 or weights.dim() != 3 or ep_recv_count.dim() != 2 or out.dim() != 2:
+        raise MoeError("moe_expert_product", MOE_ERR_SHAPE,
+                       "x, weights, ep_recv_count and out must have 2, 3, 2 and 2 dimensions")
+    element, (rows, k) = _mx_rows("x", x)
+    E, n = weights.shape[:2]
+    W, nb = ep_recv_count.shape[0], -(-k // MX_BLOCK)
+    if W < 1 or E % W:
+        raise MoeError("moe_expert_product", MOE_ERR_SHAPE, "%d experts are not a multiple of %d ranks" % (E, W))
+    if out.dtype not in (torch.float16, torch.bfloat16):
+        raise MoeError("moe_expert_product", MOE_ERR_DTYPE, "out must be fp16 or bf16, got %s" % out.dtype)
+    _check_tensor("x", x, x.dtype, x.shape, dev)
+    _check_tensor("x_scales", x_scales, torch.uint8, (rows, nb), dev)
+    _check_tensor("weights", weights, torch.uint8, (E, n, k // 2), dev)
+    _check_tensor("weight_scales", weight_scales, torch.uint8, (E, n, nb), dev)
+    _check_tensor("ep_recv_count", ep_recv_count, torch.int32, (W, E), dev)
+    _check_tensor("out", out, out.dtype, (rows, n // 2 if activation == MOE_ACT_SWIGLU else n), dev)
+    _launch("moe_expert_product", dev, _ptr(x), _ptr(x_scales), element, _ptr(weights), _ptr(weight_scales),
+            _ptr(ep_recv_count), W, E // W, rows, k, n, int(activation), dtype_code(out.dtype), _ptr(out),
+            _stream_ptr(dev))
+    return out
+
+
+def expert_product(x: torch.Tensor, x_scales: torch.Tensor, weights: torch.Tensor, weight_scales: torch.Tensor,
+                   ep_recv_count: torch.Tensor, activation: int = MOE_ACT_NONE,
+                   dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """Each row of dispatch's order times its expert's weights.
+
+    x, x_scales: microscaled rows [rows, k], from dispatch under MOE_QUANT_MX or from quantize_mx;
+    weights, weight_scales: quantize_mx of [E, n, k] in E2M1; ep_recv_count: dispatch's. Returns
+    [rows, n], or with MOE_ACT_SWIGLU [rows, n / 2]: silu(first n / 2 weight rows) * the others. Rows
+    behind the last counted one are uninitialised.
+    """
+    dev = _gpu_device("x", x)
+    if x.dim() != 2 or not isinstance(weights, torch.Tensor) or weights.dim() != 3:
+        raise MoeError("moe_expert_product", MOE_ERR_SHAPE, "x must be 2-D and weights 3-D")
+    n = weights.shape[1]
+    out = torch.empty((x.shape[0], n // 2 if activation == MOE_ACT_SWIGLU else n), dtype=dtype, device=dev)
+    return expert_product_into(out, x, x_scales, weights, weight_scales, ep_recv_count, activation)

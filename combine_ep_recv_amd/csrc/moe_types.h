@@ -1,0 +1,97 @@
+// moe_types.h -- element types, wavefront reductions and pointer checks shared by the gate and the
+// microscaled kernels (gfx950, wave64).
+#ifndef MOE_TYPES_H
+#define MOE_TYPES_H
+
+#include <hip/hip_runtime.h>
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "moe_ep.h"
+
+namespace moe_detail {
+
+constexpr int kWave = 64;
+
+// 16- and 32-bit element types: their raw bits, and conversion to and from fp32 (round to nearest, ties to even)
+struct F16 {
+    using raw = uint16_t;
+    static __device__ __forceinline__ float load(raw b) { return (float)__builtin_bit_cast(_Float16, b); }
+    static __device__ __forceinline__ raw store(float f) { return __builtin_bit_cast(uint16_t, (_Float16)f); }
+};
+struct BF16 {
+    using raw = uint16_t;
+    static __device__ __forceinline__ float load(raw b) { return __uint_as_float((uint32_t)b << 16); }
+    static __device__ __forceinline__ raw store(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+};
+struct F32 {
+    using raw = uint32_t;
+    static __device__ __forceinline__ float load(raw b) { return __uint_as_float(b); }
+    static __device__ __forceinline__ raw store(float f) { return __float_as_uint(f); }
+};
+
+// One DPP move (row shift or broadcast); lanes without a source keep v, which max and the masked sum ignore.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float old, float v)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL, ROWS, 0xf, false));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double old, double v)
+{
+    const int lo = __builtin_amdgcn_update_dpp(__double2loint(old), __double2loint(v), CTRL, ROWS, 0xf, false);
+    const int hi = __builtin_amdgcn_update_dpp(__double2hiint(old), __double2hiint(v), CTRL, ROWS, 0xf, false);
+    return __hiloint2double(hi, lo);
+}
+__device__ __forceinline__ float lane_value(float v, int lane)
+{
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+__device__ __forceinline__ double lane_value(double v, int lane)
+{
+    return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), lane),
+                            __builtin_amdgcn_readlane(__double2loint(v), lane));
+}
+__device__ __forceinline__ float max_of(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double max_of(double a, double b) { return fmax(a, b); }
+
+// Maximum and sum over the 64 lanes, the same value in every lane: row shifts by 1, 2, 4 and 8, then the last
+// lane of a row to the rows above. Every lane of the wavefront is active. The order of the sum is fixed.
+template <class T>
+__device__ __forceinline__ T wave_max(T v)
+{
+    v = max_of(v, dpp<0x111, 0xf>(v, v));
+    v = max_of(v, dpp<0x112, 0xf>(v, v));
+    v = max_of(v, dpp<0x114, 0xf>(v, v));
+    v = max_of(v, dpp<0x118, 0xf>(v, v));
+    v = max_of(v, dpp<0x142, 0xa>(v, v));
+    v = max_of(v, dpp<0x143, 0xc>(v, v));
+    return lane_value(v, 63);
+}
+template <class T>
+__device__ __forceinline__ T wave_sum(T v)
+{
+    const T z = 0;
+    v += dpp<0x111, 0xf>(z, v);
+    v += dpp<0x112, 0xf>(z, v);
+    v += dpp<0x114, 0xf>(z, v);
+    v += dpp<0x118, 0xf>(z, v);
+    v += dpp<0x142, 0xa>(z, v);
+    v += dpp<0x143, 0xc>(z, v);
+    return lane_value(v, 63);
+}
+
+// Orders a wavefront's own LDS writes before its reads of other lanes' words.
+__device__ __forceinline__ void wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+inline bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+inline int launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH; }
+
+}  // namespace moe_detail
+
+#endif  // MOE_TYPES_H

@@ -1,5 +1,6 @@
 /*
- * moe_ep.h -- MoE token dispatch and combine on one MI355X (gfx950).
+ * moe_ep.h -- MoE token dispatch and combine on one MI355X (gfx950), with the gate
+ * that routes the tokens and the experts' product on microscaled rows.
  *
  * C ABI. Every tensor argument is a plain DEVICE pointer to row-major,
  * densely packed memory that the caller allocated and owns; sizes are plain
@@ -66,8 +67,8 @@ enum moe_status {
     MOE_ERR_MASK = 9       /* unknown mask kind, or a mask pointer that does not match it */
 };
 
-/* Token element types. */
-enum moe_dtype { MOE_INT32 = 0, MOE_FP16 = 1, MOE_BF16 = 2 };
+/* Token element types. MOE_FP32 is taken by the gate and by microscaled quantisation, not by dispatch or combine. */
+enum moe_dtype { MOE_INT32 = 0, MOE_FP16 = 1, MOE_BF16 = 2, MOE_FP32 = 3 };
 
 /* Quantisation modes; the numbering follows quantMode of
  * aclnnMoeDistributeDispatchV4 (0 = none, 1 = static, 2 = per-token dynamic,
@@ -321,6 +322,105 @@ int moe_combine(const void *expand_x, const int32_t *assist_info, const int32_t 
                 int ep_world, int bs,
                 int experts_per_rank, int h, int topk, int dtype, void *x_out,
                 void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- the gate: the routing that dispatch and combine take ---- */
+
+/* Scores of a token's experts: their softmax, or the sigmoid of each. */
+enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+/* What a group of experts is chosen by: its largest value, or the sum of its two largest (of the one, where only
+ * one can be chosen). */
+enum moe_group_score { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+
+/*
+ * Gate: the experts and weights of each token.
+ *   s = softmax(logits[t]) or sigmoid(logits[t]);   c = s + bias
+ *   the topk_groups best of `groups` equal groups of consecutive experts; the topk largest c in them, descending
+ *   expert_scales[t, k] = scale * s[id_k] / (renormalize ? sum over the chosen s : 1)
+ * Ties go to the lower id (group). c is compared as in binary64; without a bias the logits are compared, whose order
+ * is that of the scores. A chosen sum of 0 gives weights 0.
+ * A logit of -infinity or NaN is an expert that is not there: never chosen, score 0. Logits of +infinity share the
+ * softmax equally. A bias of -infinity or NaN keeps its expert from being chosen and leaves the scores as they are.
+ * Where fewer than topk experts can be chosen, and in the rows that token_mask leaves out, the pairs that are missing
+ * have id -1, weight 0 and pair_mask 0: dispatch and combine take such a routing with pair_mask as their MOE_MASK_PAIR.
+ *
+ *  logits        [N, E] fp16, bf16 or fp32 (dtype); rows that token_mask leaves out are not used
+ *  bias          [E] fp32 or NULL: bears on the choice alone, not on the weights
+ *  token_mask    uint8 [N] or NULL (every token): nonzero = active
+ *  expert_ids    [N, K] int32, distinct per token
+ *  expert_scales [N, K] fp32
+ *  pair_mask     uint8 [N, K] or NULL: 1 where the pair has an expert
+ * Ranges: 0 <= tokens < 2^24, 1 <= experts <= 2048 (special experts' ids may be among them), 1 <= topk <= 64,
+ * 1 <= groups <= 64, groups divides experts, topk <= topk_groups * experts / groups, scale finite and not 0; a value
+ * outside them, or an unknown score or group score, is MOE_ERR_SHAPE. Outputs are bitwise deterministic.
+ */
+int moe_gate(const void *logits, const float *bias, const uint8_t *token_mask, int tokens, int experts, int topk,
+             int dtype, int score, int groups, int topk_groups, int group_score, int renormalize, float scale,
+             int32_t *expert_ids, float *expert_scales, uint8_t *pair_mask, void *stream);
+
+/*
+ * Gradient of the gate: grad_logits [N, E] (the logits' dtype, every element written) from grad_scales [N, K] fp32,
+ * the gradient of expert_scales, for the ids and weights that moe_gate gave with the same score, renormalize and
+ * scale. The choice itself has no gradient, and none flows to the bias. With D = sum over k of grad_scales[k] * w[k]:
+ *   softmax, renormalised  dl[id_k] = w[k] * (grad[k] - D / scale), other logits 0
+ *   sigmoid, renormalised  dl[id_k] = w[k] * (grad[k] - D / scale) * (1 - s[id_k]), other logits 0
+ *   sigmoid                dl[id_k] = scale * grad[k] * s * (1 - s), other logits 0
+ *   softmax                dl[e] = s[e] * (scale * grad of e, 0 where e was not chosen, - D)
+ * Pairs with id -1 give and get nothing, whatever their weight and gradient hold; an id outside [0, E) counts as -1.
+ * Sums in fp32. Ranges as in moe_gate; a token's ids are distinct.
+ */
+int moe_gate_backward(const void *logits, const int32_t *expert_ids, const float *expert_scales,
+                      const float *grad_scales, int tokens, int experts, int topk, int dtype, int score,
+                      int renormalize, float scale, void *grad_logits, void *stream);
+
+/* ---- microscaled rows (OCP Microscaling v1.0) and the experts' product ---- */
+
+/* Element types of microscaled rows: E2M1 (MXFP4: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; two codes a byte,
+ * the element of even index in the low nibble) and E4M3 (MXFP8, as MOE_QUANT_MX writes them). */
+enum moe_mx_element { MOE_MX_E2M1 = 0, MOE_MX_E4M3 = 1 };
+
+/*
+ * Quantise rows [rows, cols] of fp16, bf16 or fp32 to microscaled ones: per block of 32 elements of a row (the last
+ * block may be 16) shared = floor(log2 max|x|) - emax clamped to [-127, 127] (emax 2 for E2M1, 8 for E4M3; -127 for a
+ * block of zeros), code = the element nearest to x * 2^-shared, ties to even, clamped to the largest one (6, 448),
+ * sign of x kept. E4M3 gives what MOE_QUANT_MX gives. A block that holds an infinity or a NaN gets the scale byte 255
+ * (NaN) and codes 0, so that it comes back as NaN.
+ *  x       [rows, cols], 16-byte aligned
+ *  codes   [rows, cols / 2] (E2M1) or [rows, cols] (E4M3) bytes, 16-byte aligned
+ *  scales  uint8 [rows, ceil(cols / 32)], E8M0 bytes shared + 127
+ * cols is a multiple of 16; rows * ceil(cols / 32) <= 2^38 - 128.
+ */
+int moe_mx_quantize(const void *x, int64_t rows, int cols, int dtype, int element, void *codes, uint8_t *scales,
+                    void *stream);
+
+/* The values that microscaled rows stand for, code * 2^(byte - 127), rounded once to out's dtype (fp16, bf16 or
+ * fp32; bf16 and fp32 hold every value of normal size exactly). Layouts and ranges as in moe_mx_quantize. */
+int moe_mx_dequantize(const void *codes, const uint8_t *scales, int64_t rows, int cols, int dtype, int element,
+                      void *out, void *stream);
+
+/* What the product does with its sums before it rounds them: nothing, or SwiGLU: with n weight rows, row i of the
+ * first n / 2 (the gate) and row n / 2 + i (the up projection) give column i, gate / (1 + exp(-gate)) * up. */
+enum moe_activation { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 };
+
+/*
+ * Experts' product on dispatch's row order: out[row] = act(sum over k of x[row, k] * weights[e, n, k]), with e the
+ * expert that ep_recv_count gives `row` (rank-major, as dispatch writes the rows). Sums in fp32, rounded once.
+ *  x             microscaled rows [rows, k]: E2M1 or E4M3 (element), 16-byte aligned; dispatch's expand_x and
+ *                dynamic_scales under MOE_QUANT_MX, or moe_mx_quantize's outputs
+ *  x_scales      uint8 [rows, ceil(k / 32)]
+ *  weights       E2M1 codes [E, n, k / 2], 16-byte aligned; weight_scales uint8 [E, n, ceil(k / 32)]
+ *  ep_recv_count [W, S] int32: dispatch's, unchanged
+ *  out           [rows, n], or [rows, n / 2] with MOE_ACT_SWIGLU, fp16 or bf16 (dtype). Rows behind the last that
+ *                ep_recv_count counts are left as they were
+ * A scale byte of 255 makes every result of its row NaN.
+ * Ranges: ep_world and experts as in moe_dispatch, rows >= 0, k a multiple of 16, n >= 1 (even with SwiGLU). Counts
+ * that ep_recv_count should not hold (negative, descending, beyond rows) leave the kernel in bounds and the outputs
+ * unspecified. Needs no workspace.
+ */
+int moe_expert_product(const void *x, const uint8_t *x_scales, int element, const uint8_t *weights,
+                       const uint8_t *weight_scales, const int32_t *ep_recv_count, int ep_world,
+                       int experts_per_rank, int rows, int k, int n, int activation, int dtype, void *out,
+                       void *stream);
 
 /* A static, human-readable name for a status code. */
 const char *moe_status_str(int status);

@@ -1,0 +1,591 @@
+"""Microscaled rows and the experts' product on them.
+
+The plain implementations work in binary64 on the CPU, from the definitions in include/moe_ep.h. Quantisation and
+dequantisation must be equal to them bit for bit.
+
+Tolerances of the product. E2M1 x E2M1: a matrix instruction adds 128 exact products and the accumulator with fp32
+rounding; k / 128 of them, three joins of the wavefronts' parts and the step over the last elements follow each other,
+each off by at most 2^-23 of the sum of magnitudes M = sum |x w|. E4M3 rows: the instruction lines the 8-bit products
+of up to 16 neighbouring elements up with their largest and keeps 13 bits below it, so each product is off by at most
+2^-13 of the largest of its 16: at most 16 * 2^-13 M = 2^-9 M in all. The output is then rounded, half a step. SwiGLU
+passes an error e of the gate on as at most 1.1 |up| e and one of the up projection as |silu(gate)| e, and its own
+exp, division and product take up to 16 * 2^-24 of the result (|gate| * 2^-24 more for exp's argument).
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import combine_ep_recv_amd as moe
+import oracle
+import workloads as wl
+
+DEV = "cuda"
+E2M1, E4M3 = moe.MOE_MX_E2M1, moe.MOE_MX_E4M3
+NONE, SWIGLU = moe.MOE_ACT_NONE, moe.MOE_ACT_SWIGLU
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+FP4 = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
+
+
+def e4m3_values():
+    c = np.arange(127)
+    e, m = c >> 3, c & 7
+    return np.where(e > 0, (1 + m / 8) * 2.0 ** (e - 7), m / 8 * 2.0 ** -6)
+
+
+TABLE = {E2M1: FP4, E4M3: e4m3_values()}
+
+
+def plain_quantize(x, element):
+    """(codes one per element, scale bytes) of x [rows, cols] in binary64."""
+    x = np.asarray(x, np.float64)
+    rows, cols = x.shape
+    nb, emax, table = -(-cols // 32), (2, 8)[element], TABLE[element]
+    codes, scales = np.zeros((rows, cols), np.uint8), np.zeros((rows, nb), np.uint8)
+    for b in range(nb):
+        v = x[:, 32 * b:32 * b + 32]
+        bad = ~np.isfinite(v).all(1)
+        v = np.where(bad[:, None], 0.0, v)
+        top = np.abs(v).max(1)
+        shared = np.where(top > 0, np.clip(np.frexp(np.where(top > 0, top, 1))[1] - 1 - emax, -127, 127), -127)
+        a = np.minimum(np.abs(v) * 2.0 ** -shared.astype(np.float64)[:, None], table[-1])
+        low = np.clip(np.searchsorted(table, a, side="right") - 1, 0, len(table) - 2)
+        below, above = a - table[low], table[low + 1] - a
+        q = low + ((above < below) | ((above == below) & (low % 2 == 1)))
+        sign = np.signbit(v) << (3 if element == E2M1 else 7)
+        codes[:, 32 * b:32 * b + 32] = np.where(bad[:, None], 0, q | sign)
+        scales[:, b] = np.where(bad, 255, shared + 127)
+    return codes, scales
+
+
+def pack(codes, element):
+    return codes if element == E4M3 else (codes[..., 0::2] | (codes[..., 1::2] << 4))
+
+
+def unpack(codes, element):
+    if element == E4M3:
+        return codes
+    out = np.empty(codes.shape[:-1] + (2 * codes.shape[-1],), np.uint8)
+    out[..., 0::2], out[..., 1::2] = codes & 15, codes >> 4
+    return out
+
+
+def values(codes, scales, element):
+    """Binary64 values of one-per-element codes."""
+    bits = 3 if element == E2M1 else 7
+    v = TABLE[element][codes & ((1 << bits) - 1)]
+    v = np.where(codes >> bits, -v, v)
+    s = np.where(scales == 255, np.nan, 2.0 ** (scales.astype(np.float64) - 127))
+    return v * np.repeat(s, 32, -1)[..., :v.shape[-1]]
+
+
+def rows_of(n, cols, dtype, seed):
+    """Rows of different size with outliers, blocks of zeros, negative zeros, subnormals and ties."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(n, cols, generator=g) * torch.exp(2 * torch.randn(n, 1, generator=g))
+    x[:, ::7] *= 20
+    x = x.to(dtype)
+    f = torch.finfo(dtype)
+    if n > 6:
+        x[1] = 0
+        x[2] = -0.0
+        x[3] = f.tiny * torch.randn(cols, generator=g).to(dtype)
+        x[4] = f.max
+        x[4, ::2] = -f.max
+        x[5] = (torch.arange(cols) % 65).to(dtype) / 8 - 4           # every tie of both element types
+        x[6] = f.smallest_normal * 0.5
+    return x
+
+
+# ---- host only ----
+
+A = 1 << 20
+
+
+def P(v):
+    return None if v is None else ctypes.c_void_p(v)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(rows=-1), moe.MOE_ERR_SHAPE), (dict(cols=8), moe.MOE_ERR_SHAPE), (dict(cols=40), moe.MOE_ERR_SHAPE),
+    (dict(cols=0), moe.MOE_ERR_SHAPE), (dict(dtype=0), moe.MOE_ERR_DTYPE), (dict(element=2), moe.MOE_ERR_QUANT),
+    (dict(rows=(1 << 31) - 1, cols=1 << 13), moe.MOE_ERR_SHAPE),
+    (dict(x=None), moe.MOE_ERR_NULLPTR), (dict(codes=None), moe.MOE_ERR_NULLPTR), (dict(scales=None), moe.MOE_ERR_NULLPTR),
+    (dict(x=A + 8), moe.MOE_ERR_ALIGN), (dict(codes=A + 8), moe.MOE_ERR_ALIGN),
+    (dict(rows=0, x=None, codes=None, scales=None), moe.MOE_OK),
+])
+def test_mx_calls_refuse_before_a_launch(kw, want):
+    p = dict(x=A, rows=4, cols=64, dtype=2, element=0, codes=2 * A, scales=3 * A)
+    p.update(kw)
+    lib = moe.library()
+    assert lib.moe_mx_quantize(P(p["x"]), p["rows"], p["cols"], p["dtype"], p["element"], P(p["codes"]), P(p["scales"]),
+                               None) == want
+    assert lib.moe_mx_dequantize(P(p["codes"]), P(p["scales"]), p["rows"], p["cols"], p["dtype"], p["element"],
+                                 P(p["x"]), None) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(W=1), moe.MOE_ERR_SHAPE), (dict(W=769), moe.MOE_ERR_SHAPE), (dict(epr=0), moe.MOE_ERR_SHAPE),
+    (dict(W=8, epr=129), moe.MOE_ERR_SHAPE), (dict(rows=-1), moe.MOE_ERR_SHAPE), (dict(k=8), moe.MOE_ERR_SHAPE),
+    (dict(k=72), moe.MOE_ERR_SHAPE), (dict(n=0), moe.MOE_ERR_SHAPE), (dict(act=1, n=7), moe.MOE_ERR_SHAPE),
+    (dict(act=2), moe.MOE_ERR_SHAPE), (dict(element=2), moe.MOE_ERR_QUANT), (dict(dtype=0), moe.MOE_ERR_DTYPE),
+    (dict(dtype=3), moe.MOE_ERR_DTYPE), (dict(rows=1 << 30, n=1 << 20), moe.MOE_ERR_SHAPE),
+    (dict(x=None), moe.MOE_ERR_NULLPTR), (dict(xs=None), moe.MOE_ERR_NULLPTR), (dict(w=None), moe.MOE_ERR_NULLPTR),
+    (dict(ws=None), moe.MOE_ERR_NULLPTR), (dict(erc=None), moe.MOE_ERR_NULLPTR), (dict(out=None), moe.MOE_ERR_NULLPTR),
+    (dict(x=A + 8), moe.MOE_ERR_ALIGN), (dict(w=A + 4), moe.MOE_ERR_ALIGN), (dict(erc=A + 2), moe.MOE_ERR_ALIGN),
+    (dict(out=A + 1), moe.MOE_ERR_ALIGN), (dict(rows=0, x=None, out=None), moe.MOE_OK),
+])
+def test_product_refuses_before_a_launch(kw, want):
+    p = dict(x=A, xs=2 * A, element=0, w=3 * A, ws=4 * A, erc=5 * A, W=2, epr=2, rows=8, k=64, n=32, act=0, dtype=2,
+             out=6 * A)
+    p.update(kw)
+    assert moe.library().moe_expert_product(P(p["x"]), P(p["xs"]), p["element"], P(p["w"]), P(p["ws"]), P(p["erc"]), p["W"],
+                                            p["epr"], p["rows"], p["k"], p["n"], p["act"], p["dtype"], P(p["out"]),
+                                            None) == want
+
+
+class _Recorder:
+    def __init__(self):
+        self.calls = []
+        self.moe_status_str = moe.library().moe_status_str
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append(name)
+            return moe.MOE_OK
+        return call
+
+
+@pytest.fixture
+def rec(monkeypatch):
+    r = _Recorder()
+    monkeypatch.setattr(moe, "library", lambda: r)
+    monkeypatch.setattr(moe, "_gpu_device", lambda name, t: t.device)
+    monkeypatch.setattr(moe, "_stream_ptr", lambda device: 0)
+    return r
+
+
+def _product_args(W=2, epr=3, rows=10, k=48, n=32, element=E2M1):
+    E = W * epr
+    x = torch.zeros((rows, k // 2), dtype=torch.uint8) if element == E2M1 else torch.zeros((rows, k)).to(torch.float8_e4m3fn)
+    return dict(out=torch.zeros((rows, n), dtype=torch.bfloat16), x=x, x_scales=torch.zeros((rows, 2), dtype=torch.uint8),
+                weights=torch.zeros((E, n, k // 2), dtype=torch.uint8),
+                weight_scales=torch.zeros((E, n, 2), dtype=torch.uint8),
+                ep_recv_count=torch.zeros((W, E), dtype=torch.int32))
+
+
+def test_well_formed_mx_calls_reach_the_library(rec):
+    for element in (E2M1, E4M3):
+        moe.expert_product_into(**_product_args(element=element))
+        c, s = moe.quantize_mx(torch.zeros(3, 2, 48), element)
+        assert c.shape == ((3, 2, 24) if element == E2M1 else (3, 2, 48)) and s.shape == (3, 2, 2)
+        assert moe.dequantize_mx(c, s).shape == (3, 2, 48)
+    a = _product_args()
+    del a["out"]
+    assert moe.expert_product(**a, activation=SWIGLU).shape == (10, 16)
+    assert rec.calls == ["moe_expert_product", "moe_mx_quantize", "moe_mx_dequantize"] * 2 + ["moe_expert_product"]
+
+
+@pytest.mark.parametrize("field,value", [
+    ("x", torch.zeros((10, 24), dtype=torch.int8)), ("x", torch.zeros((9, 24), dtype=torch.uint8)),
+    ("x", torch.zeros((24, 10), dtype=torch.uint8).t()), ("x", torch.zeros(240, dtype=torch.uint8)),
+    ("x_scales", torch.zeros((10, 1), dtype=torch.uint8)), ("x_scales", torch.zeros((10, 2))),
+    ("weights", torch.zeros((6, 32, 23), dtype=torch.uint8)), ("weights", torch.zeros((7, 32, 24), dtype=torch.uint8)),
+    ("weights", torch.zeros((6, 32, 24), dtype=torch.int8)), ("weight_scales", torch.zeros((6, 31, 2), dtype=torch.uint8)),
+    ("ep_recv_count", torch.zeros((2, 5), dtype=torch.int32)), ("ep_recv_count", torch.zeros((2, 6), dtype=torch.int64)),
+    ("ep_recv_count", torch.zeros((4, 6), dtype=torch.int32)), ("out", torch.zeros((10, 32))),
+    ("out", torch.zeros((10, 16), dtype=torch.bfloat16)), ("out", torch.zeros((9, 32), dtype=torch.bfloat16)),
+], ids=lambda v: v if isinstance(v, str) else "")
+def test_product_rejects_before_the_call(rec, field, value):
+    args = _product_args()
+    args[field] = value
+    with pytest.raises(moe.MoeError):
+        moe.expert_product_into(**args)
+    assert rec.calls == []
+
+
+def test_mx_wrappers_reject_before_the_call(rec):
+    ok = torch.zeros((4, 24), dtype=torch.uint8), torch.zeros((4, 2), dtype=torch.uint8)
+    for call in (lambda: moe.quantize_mx(torch.zeros(4, 40)), lambda: moe.quantize_mx(torch.zeros(4, 48).double()),
+                 lambda: moe.quantize_mx(torch.zeros(48, 4).t()), lambda: moe.quantize_mx(torch.zeros(4, 48), 2),
+                 lambda: moe.quantize_mx_into(*ok, torch.zeros(4, 64)),
+                 lambda: moe.quantize_mx_into(ok[0], torch.zeros((4, 1), dtype=torch.uint8), torch.zeros(4, 48)),
+                 lambda: moe.quantize_mx_into(ok[0].char(), ok[1], torch.zeros(4, 48)),
+                 lambda: moe.dequantize_mx(ok[0], ok[1][:3]), lambda: moe.dequantize_mx(*ok, torch.int32),
+                 lambda: moe.dequantize_mx_into(torch.zeros(4, 64), *ok)):
+        with pytest.raises(moe.MoeError):
+            call()
+    assert rec.calls == []
+
+
+def test_cpu_tensors_are_rejected():
+    with pytest.raises(moe.MoeError):
+        moe.quantize_mx(torch.zeros(4, 64))
+    with pytest.raises(moe.MoeError):
+        moe.expert_product_into(**_product_args())
+
+
+def test_plain_e4m3_quantiser_is_the_oracles():
+    w = wl.custom(2, 4, 80, 1, 2, "bf16", "uniform_distinct", quant_mode=4, name="mx_rows")
+    x = rows_of(8, 80, torch.bfloat16, 3)
+    x[4] = 1.0
+    ids = np.arange(8, dtype=np.int32).reshape(8, 1) % 4
+    d = oracle.dispatch(x.view(torch.int16).numpy().view(np.uint16), ids, 2, 2, 4, bf16=True)
+    src = d["assist_info"][:, 0] * 4 + d["assist_info"][:, 1]
+    codes, scales = plain_quantize(x.double().numpy()[src], E4M3)
+    assert (codes == d["expand_x"].view(np.uint8)).all() and (scales == d["dynamic_scales"]).all()
+
+
+# ---- GPU: quantisation ----
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("element", [E2M1, E4M3])
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows,cols", [(1, 16), (1, 32), (7, 48), (130, 64), (33, 2064), (9, 7168), (1000, 16), (257, 80)])
+def test_quantize_is_exact(element, dtype, rows, cols):
+    x = rows_of(rows, cols, dtype, rows + cols)
+    codes, scales = moe.quantize_mx(x.to(DEV), element)
+    want, ws = plain_quantize(x.double().numpy(), element)
+    assert (scales.cpu().numpy() == ws).all()
+    assert (codes.view(torch.uint8).cpu().numpy() == pack(want, element)).all()
+    for out in TYPES:
+        got = moe.dequantize_mx(codes, scales, out).cpu()
+        v = torch.from_numpy(values(want, ws, element))
+        ref = v.float().to(out)                   # fp32 holds every value; then one rounding
+        assert torch.equal(got.view(torch.uint8), ref.view(torch.uint8)), (out, (got != ref).nonzero()[:3])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("element", [E2M1, E4M3])
+def test_quantize_every_16_bit_value_against_a_block_top(element):
+    """Every finite bf16 and fp16 value beside a block maximum of 1, 1.9 and the value itself."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    for dtype in (torch.bfloat16, torch.float16):
+        v = bits.view(dtype)
+        v = v[torch.isfinite(v)]
+        x = torch.zeros((3, v.numel(), 32), dtype=dtype)
+        x[:, :, 3] = v
+        x[0, :, 30], x[1, :, 30] = 1.0, 1.9
+        x = x.view(-1, 32)
+        codes, scales = moe.quantize_mx(x.to(DEV), element)
+        want, ws = plain_quantize(x.double().numpy(), element)
+        assert (scales.cpu().numpy() == ws).all()
+        assert (codes.view(torch.uint8).cpu().numpy() == pack(want, element)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("element", [E2M1, E4M3])
+@pytest.mark.parametrize("cols", [64, 80])
+def test_quantize_marks_blocks_that_are_not_finite(element, cols):
+    x = torch.randn(12, cols, generator=torch.Generator().manual_seed(1))
+    x[1, 3], x[2, 40], x[3, cols - 1], x[4] = float("nan"), float("inf"), -float("inf"), float("nan")
+    for dtype in TYPES:
+        codes, scales = moe.quantize_mx(x.to(dtype).to(DEV), element)
+        want, ws = plain_quantize(x.to(dtype).double().numpy(), element)
+        assert (scales.cpu().numpy() == ws).all()
+        assert (codes.view(torch.uint8).cpu().numpy() == pack(want, element)).all()
+        back = moe.dequantize_mx(codes, scales, dtype).cpu()
+        assert torch.equal(torch.isnan(back), torch.from_numpy(np.repeat(ws == 255, 32, 1)[:, :cols]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("element", [E2M1, E4M3])
+@pytest.mark.parametrize("cols", [96, 112])
+def test_dequantize_takes_every_code_and_scale(element, cols):
+    g = torch.Generator().manual_seed(4)
+    per = 2 if element == E2M1 else 1
+    codes = torch.randint(0, 256, (300, cols // per), generator=g, dtype=torch.int32).to(torch.uint8)
+    if element == E4M3:
+        codes[(codes & 127) == 127] = 5                       # NaN codes: below
+    nb = -(-cols // 32)
+    scales = (torch.arange(300 * nb, dtype=torch.int32) % 256).to(torch.uint8).view(300, nb)
+    typed = codes if element == E2M1 else codes.view(torch.float8_e4m3fn)
+    v = torch.from_numpy(values(unpack(codes.numpy(), element), scales.numpy(), element))
+    for out in TYPES:
+        got = moe.dequantize_mx(typed.to(DEV), scales.to(DEV), out).cpu()
+        ref = v.float().to(out)                               # products below fp32's smallest round there first
+        same = (got == ref) | (got.isnan() & ref.isnan())
+        assert same.all(), (out, (~same).nonzero()[:3])
+    if element == E4M3:
+        got = moe.dequantize_mx(torch.full((1, 32), 127, dtype=torch.uint8).view(torch.float8_e4m3fn).to(DEV),
+                                torch.full((1, 1), 127, dtype=torch.uint8, device=DEV))
+        assert got.isnan().all()
+
+
+@pytest.mark.gpu
+def test_quantize_leaves_the_neighbours_alone():
+    for element, per in ((E2M1, 2), (E4M3, 1)):
+        for rows, cols in ((3, 16), (5, 80), (1, 48)):
+            size, nb = rows * cols // per, rows * -(-cols // 32)
+            codes = torch.full((size + 512,), 0xA5, dtype=torch.uint8, device=DEV)
+            scales = torch.full((nb + 512,), 0xA5, dtype=torch.uint8, device=DEV)
+            c = codes[256:256 + size].view(rows, cols // per)
+            s = scales[256:256 + nb].view(rows, -1)
+            moe.quantize_mx_into(c if element == E2M1 else c.view(torch.float8_e4m3fn), s, torch.randn(rows, cols, device=DEV))
+            for t, n in ((codes, size), (scales, nb)):
+                assert (t[:256] == 0xA5).all() and (t[256 + n:] == 0xA5).all()
+
+
+@pytest.mark.gpu
+def test_e4m3_rows_are_dispatchs():
+    x = rows_of(64, 2064, torch.float16, 7)
+    x[4] = 2.0
+    ids = torch.arange(64, dtype=torch.int32).view(64, 1) % 8
+    ex, dyn, assist, _ = moe.dispatch(x.to(DEV), ids.to(DEV), 4, 2, moe.MOE_QUANT_MX)
+    src = (assist[:, 0] * 16 + assist[:, 1]).long()
+    codes, scales = moe.quantize_mx(x.to(DEV)[src].contiguous(), E4M3)
+    assert torch.equal(codes.view(torch.uint8), ex.view(torch.uint8)) and torch.equal(scales, dyn)
+
+
+# ---- GPU: the product ----
+
+def counts_for(per_expert, W, seed):
+    """ep_recv_count for the given rows of each expert, spread over the source ranks."""
+    rng = np.random.default_rng(seed)
+    E = len(per_expert)
+    seg = np.stack([rng.multinomial(c, np.ones(W) / W) for c in per_expert])      # [E, W]
+    return torch.from_numpy(seg.reshape(W, (E // W) * W).cumsum(1).astype(np.int32))
+
+
+def draw_product(per_expert, W, k, n, element, seed, spare=0, spread=6):
+    """Random codes and scales: (x, xs, w, ws, counts) as numpy one-per-element codes."""
+    rng = np.random.default_rng(seed)
+    E, rows, nb = len(per_expert), int(sum(per_expert)) + spare, -(-k // 32)
+    top = 16 if element == E2M1 else 256
+    x = rng.integers(0, top, (rows, k)).astype(np.uint8)
+    if element == E4M3:
+        x[(x & 127) == 127] = 9
+    w = rng.integers(0, 16, (E, n, k)).astype(np.uint8)
+    xs = rng.integers(127 - spread, 127 + spread, (rows, nb)).astype(np.uint8)
+    ws = rng.integers(127 - spread, 127 + spread, (E, n, nb)).astype(np.uint8)
+    return x, xs, w, ws, counts_for(per_expert, W, seed)
+
+
+def on_gpu(x, xs, w, ws, counts, element):
+    x = torch.from_numpy(pack(x, element)).to(DEV)
+    return (x.view(torch.float8_e4m3fn) if element == E4M3 else x, torch.from_numpy(xs).to(DEV),
+            torch.from_numpy(pack(w, E2M1)).to(DEV), torch.from_numpy(ws).to(DEV), counts.to(DEV))
+
+
+def check_product(per_expert, W, k, n, element, act=NONE, dtype=torch.bfloat16, seed=0, spare=0, spread=6):
+    x, xs, w, ws, counts = draw_product(per_expert, W, k, n, element, seed, spare, spread)
+    fo = n // 2 if act == SWIGLU else n
+    out = torch.full((x.shape[0], fo), 7.0, dtype=dtype, device=DEV)
+    moe.expert_product_into(out, *on_gpu(x, xs, w, ws, counts, element), activation=act)
+    got = out.cpu().double().numpy()
+    X, row, f = values(x, xs, element), 0, torch.finfo(dtype)
+    part = (k / 128 + 5) * 2.0 ** -23 if element == E2M1 else 2.0 ** -9 + (k / 128 + 5) * 2.0 ** -23
+    for e, c in enumerate(per_expert):
+        if c == 0:
+            continue
+        V = values(w[e], ws[e], E2M1)
+        y, mag = X[row:row + c] @ V.T, np.abs(X[row:row + c]) @ np.abs(V).T
+        room = part * mag
+        if act == SWIGLU:
+            g, u, dg, du = y[:, :fo], y[:, fo:], room[:, :fo], room[:, fo:]
+            with np.errstate(over="ignore"):
+                s = g / (1 + np.exp(-g))
+            y = s * u
+            # silu of a gate that is off by dg: its slope is at most 1.1 in size
+            room = 1.1 * dg * (np.abs(u) + du) + np.abs(s) * du + (16 + np.abs(g)) * 2.0 ** -24 * np.abs(y)
+        ref = np.clip(y, -f.max, f.max) if dtype == torch.float16 else y
+        mine = np.clip(got[row:row + c], -f.max, f.max)
+        err = np.abs(mine - ref)
+        limit = room + f.eps / 2 * (np.abs(ref) + room) + f.tiny * f.eps
+        assert (err <= limit).all(), (e, c, err.max(), np.argwhere(err > limit)[:4], (err / limit).max())
+        row += c
+    assert (got[row:] == 7.0).all()                # rows behind the last are left alone
+    return got
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("element", [E2M1, E4M3])
+@pytest.mark.parametrize("act", [NONE, SWIGLU])
+@pytest.mark.parametrize("k,n", [(16, 2), (32, 16), (48, 30), (128, 64), (144, 66), (512, 64), (528, 130), (1040, 96),
+                                 (1664, 34)])
+def test_product_shapes(element, act, k, n):
+    check_product([1, 0, 3, 16], 2, k, n, element, act, seed=k + n, spare=2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("element", [E2M1, E4M3])
+@pytest.mark.parametrize("per_expert,W", [([0, 0], 2), ([1, 0], 2), ([0, 17], 2), ([40, 0, 0, 5], 4), ([33] * 8, 8),
+                                          ([0] * 15 + [300], 16), ([129, 64, 65, 128], 2), ([600, 3], 2),
+                                          ([2] * 257 + [0] * 255, 2), ([1] * 1024, 512), ([257, 256, 255, 1], 2)],
+                         ids=lambda v: str(v) if isinstance(v, int) else "%d experts %d rows" % (len(v), sum(v)))
+def test_product_rows_per_expert(element, per_expert, W):
+    check_product(per_expert, W, 160, 40, element, seed=len(per_expert), spare=1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("element", [E2M1, E4M3])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("act", [NONE, SWIGLU])
+@pytest.mark.parametrize("per_expert", [[20, 1], [200, 150], [700, 90]], ids=str)
+def test_product_types(element, dtype, act, per_expert):
+    check_product(per_expert, 2, 1536, 192, element, act, dtype, seed=9, spread=2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("element", [E2M1, E4M3])
+@pytest.mark.parametrize("k", [64, 512, 1168])
+@pytest.mark.parametrize("rows", [5, 40, 300])
+def test_product_is_exact_on_small_whole_numbers(element, k, rows):
+    """Whole numbers whose sums stay within the instruction's 13 bits a group and fp32's 24: every element, block
+    and scale has to be in its place for the result to be equal."""
+    rng = np.random.default_rng(k + rows)
+    per, W, n = [rows, 0, 3, 7], 2, 48
+    E, total, nb = 4, sum(per), -(-k // 32)
+    small = {E2M1: np.array([0, 2, 4, 5, 10, 12, 13]), E4M3: np.array([0, 56, 64, 68, 72, 184, 192, 196])}   # 0 1 2 3 (4) -1 ..
+    x = rng.choice(small[element], (total, k)).astype(np.uint8)
+    w = rng.choice(small[E2M1], (E, n, k)).astype(np.uint8)
+    xs = rng.integers(127, 129, (total, nb)).astype(np.uint8)
+    ws = rng.integers(127, 129, (E, n, nb)).astype(np.uint8)
+    counts = counts_for(per, W, 1)
+    out = moe.expert_product(*on_gpu(x, xs, w, ws, counts, element), dtype=torch.bfloat16).cpu()
+    X, row = values(x, xs, element), 0
+    for e, c in enumerate(per):
+        y = X[row:row + c] @ values(w[e], ws[e], E2M1).T
+        assert np.abs(X[row:row + c]) .max(initial=0) <= 8 and np.abs(y).max(initial=0) < 2 ** 24
+        assert torch.equal(out[row:row + c], torch.from_numpy(y).to(torch.bfloat16)), (e, c)
+        row += c
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("element", [E2M1, E4M3])
+def test_product_rows_do_not_touch_each_other(element):
+    """A row's result does not depend on what the other rows hold: NaN rows spoil only themselves, a NaN weight row
+    only its column, and rows behind the last one are never read into a result."""
+    per, W, k, n = [30, 70, 1, 200], 2, 656, 48
+    x, xs, w, ws, counts = draw_product(per, W, k, n, element, 3, spare=9, spread=2)
+    base = moe.expert_product(*on_gpu(x, xs, w, ws, counts, element)).cpu()
+    total = sum(per)
+    xs2, ws2 = xs.copy(), ws.copy()
+    xs2[[0, 29, 100, total - 1], 3] = 255
+    xs2[total:] = 255
+    ws2[1, 17, 20] = 255
+    got = moe.expert_product(*on_gpu(x, xs2, w, ws2, counts, element)).cpu()
+    bad = torch.zeros((total, n), dtype=torch.bool)
+    bad[[0, 29, 100, total - 1]] = True
+    bad[30:100, 17] = True
+    assert torch.equal(got[:total].isnan(), bad)
+    assert torch.equal(got[:total][~bad], base[:total][~bad])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", ["negative", "descending", "huge"])
+def test_product_stays_in_bounds_on_counts_it_should_not_get(bad):
+    per, W, k, n = [30, 70, 1, 20], 2, 160, 48
+    x, xs, w, ws, counts = draw_product(per, W, k, n, E2M1, 3)
+    counts = {"negative": -counts, "descending": counts.flip(1).contiguous(),
+              "huge": torch.full_like(counts, 2 ** 31 - 1)}[bad]
+    rows = x.shape[0]
+    whole = torch.full((rows + 64, n), 7.0, dtype=torch.bfloat16, device=DEV)
+    moe.expert_product_into(whole[32:32 + rows], *on_gpu(x, xs, w, ws, counts, E2M1))
+    assert (whole[:32] == 7.0).all() and (whole[32 + rows:] == 7.0).all()
+
+
+@pytest.mark.gpu
+def test_product_out_of_any_alignment():
+    """Odd column counts and an output that starts at an odd element."""
+    per, W, k = [20, 5], 2, 96
+    for n in (1, 3, 37, 66):
+        x, xs, w, ws, counts = draw_product(per, W, k, n, E2M1, n)
+        want = moe.expert_product(*on_gpu(x, xs, w, ws, counts, E2M1))
+        flat = torch.full((25 * n + 9,), 7.0, dtype=torch.bfloat16, device=DEV)
+        out = flat[5:5 + 25 * n].view(25, n)
+        moe.expert_product_into(out, *on_gpu(x, xs, w, ws, counts, E2M1))
+        assert torch.equal(out, want) and (flat[:5] == 7.0).all() and (flat[5 + 25 * n:] == 7.0).all()
+        X, row = values(x, xs, E2M1), 0
+        for e, c in enumerate(per):
+            y = X[row:row + c] @ values(w[e], ws[e], E2M1).T
+            assert np.abs(out[row:row + c].cpu().double().numpy() - y).max() <= 2.0 ** -8 * np.abs(y).max()
+            row += c
+
+
+@pytest.mark.gpu
+def test_two_products_at_once_and_replayed():
+    args = [draw_product([40, 3, 0, 90], 2, 1040, 96, el, s, spread=2) for el, s in ((E2M1, 1), (E4M3, 2))]
+    dev = [on_gpu(*a, el) for a, el in zip(args, (E2M1, E4M3))]
+    want = [moe.expert_product(*d, activation=SWIGLU) for d in dev]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream(), torch.cuda.Stream()], [torch.empty_like(w) for w in want]
+    for _ in range(5):
+        for s, d, o in zip(streams, dev, outs):
+            with torch.cuda.stream(s):
+                moe.expert_product_into(o, *d, activation=SWIGLU)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+    x = torch.randn(133, 1040, device=DEV)
+    codes, scales = moe.quantize_mx(x)
+    y = torch.empty_like(want[0])
+    d = dev[0]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.quantize_mx_into(codes, scales, x)
+        moe.expert_product_into(y, codes, scales, *d[2:], activation=SWIGLU)
+    for i in range(4):
+        x.copy_(torch.randn(133, 1040, generator=torch.Generator().manual_seed(i)))
+        d[4].copy_(counts_for([40 - i, 3 + i, 0, 90], 2, i))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        ref = moe.expert_product(*moe.quantize_mx(x), *d[2:], activation=SWIGLU)
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("first", [E2M1, E4M3])
+def test_the_whole_layer(first):
+    """gate -> dispatch -> product with SwiGLU -> quantise -> product -> combine, each stage against binary64 from
+    the stage's own inputs; the combined tokens against the second product's rows."""
+    W, bs, epr, h, f, K = 4, 12, 4, 160, 96, 4
+    N, E = W * bs, W * epr
+    g = torch.Generator().manual_seed(17)
+    x = torch.randn(N, h, generator=g).bfloat16()
+    logits = torch.randn(N, E, generator=g)
+    logits[3, 2:] = -float("inf")
+    w1, w2 = torch.randn(E, 2 * f, h, generator=g) * h ** -0.5, torch.randn(E, h, f, generator=g) * f ** -0.5
+    q1, s1 = moe.quantize_mx(w1.to(DEV))
+    q2, s2 = moe.quantize_mx(w2.to(DEV))
+    ids, wt, on = moe.gate(logits.to(DEV), K, moe.MOE_SCORE_SIGMOID, with_pair_mask=True)
+    if first == E4M3:
+        rows, rs, assist, erc = moe.dispatch(x.to(DEV), ids, W, epr, moe.MOE_QUANT_MX, x_active_mask=on)
+    else:
+        plain, _, assist, erc = moe.dispatch(x.to(DEV), ids, W, epr, x_active_mask=on)
+        rows, rs = moe.quantize_mx(plain)
+    A = int(on.sum())
+    y1 = moe.expert_product(rows, rs, q1, s1, erc, SWIGLU)
+    r2, rs2 = moe.quantize_mx(y1)
+    y2 = moe.expert_product(r2, rs2, q2, s2, erc)
+    out = moe.combine(y2, assist, erc, ids, wt, W, epr, x_active_mask=on).cpu().double()
+
+    expert = torch.cat([torch.full((int(c),), e) for e, c in enumerate(
+        torch.diff(torch.cat((torch.zeros(W, 1), erc.cpu()[:, W - 1::W].double()), 1), dim=1).flatten())])
+    assert len(expert) == A
+    a = assist.cpu()[:A].long()
+    tok = a[:, 0] * bs + a[:, 1]
+    assert torch.equal(ids.cpu()[tok, a[:, 2]].long(), expert)
+    X = values(unpack(rows.view(torch.uint8).cpu().numpy()[:A], first), rs.cpu().numpy()[:A], first)
+    V1 = values(unpack(q1.cpu().numpy(), E2M1), s1.cpu().numpy(), E2M1)
+    V2 = values(unpack(q2.cpu().numpy(), E2M1), s2.cpu().numpy(), E2M1)
+    z = np.einsum("rk,rnk->rn", X, V1[expert.numpy()])
+    mag = np.einsum("rk,rnk->rn", np.abs(X), np.abs(V1[expert.numpy()]))
+    G, Up, dg, du = z[:, :f], z[:, f:], mag[:, :f] * 2.0 ** -8, mag[:, f:] * 2.0 ** -8
+    want = G / (1 + np.exp(-G)) * Up
+    room = 1.1 * dg * (np.abs(Up) + du) + np.abs(G) * du + 2.0 ** -8 * np.abs(want) + 2.0 ** -8 * 1.1 * dg * np.abs(Up)
+    assert (np.abs(y1[:A].cpu().double().numpy() - want) <= room).all()
+    Y = values(unpack(r2.cpu().numpy()[:A], E2M1), rs2.cpu().numpy()[:A], E2M1)
+    z2 = np.einsum("rk,rnk->rn", Y, V2[expert.numpy()])
+    m2 = np.einsum("rk,rnk->rn", np.abs(Y), np.abs(V2[expert.numpy()]))
+    got2 = y2[:A].cpu().double().numpy()
+    assert (np.abs(got2 - z2) <= 2.0 ** -8 * np.abs(z2) + 8 * 2.0 ** -23 * m2 * 1.01 + 1e-30).all()
+    ref = np.zeros((N, h))
+    size = np.zeros((N, h))
+    np.add.at(ref, tok.numpy(), got2 * wt.cpu().double().numpy()[tok, a[:, 2]][:, None])
+    np.add.at(size, tok.numpy(), np.abs(got2 * wt.cpu().double().numpy()[tok, a[:, 2]][:, None]))
+    assert (np.abs(out.numpy() - ref) <= 2.0 ** -8 * np.abs(ref) + (2 * K) * 2.0 ** -24 * 1.01 * size + 1e-30).all()
