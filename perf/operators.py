@@ -216,6 +216,8 @@ def _gate_plain(case, logits, bias, mask):
     low = float("-inf")
     l = logits.double()
     ok = l > low
+    if bias is not None:
+        ok = ok & (bias > low)
     if mask is not None:
         ok = ok & mask[:, None]
     l = torch.where(ok, l, low)
@@ -225,8 +227,6 @@ def _gate_plain(case, logits, bias, mask):
         s = e / e.sum(1, keepdim=True).clamp(min=1e-300)
     else:
         s = 1.0 / (1.0 + torch.exp(-l))
-    if bias is not None:
-        ok = ok & (bias > low)                                    # the bias bears on the choice alone
     c = torch.where(ok, s + bias.double() if bias is not None else l, low)
     if G > 1:
         v = torch.where(ok, s + bias.double() if bias is not None else s, low)
