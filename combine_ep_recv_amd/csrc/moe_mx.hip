@@ -289,7 +289,8 @@ __device__ Tile find_tile(const ProductArgs &a, int mt)
         at += c;
     }
     __syncthreads();
-    return found;
+    return Tile{__builtin_amdgcn_readfirstlane(found.expert), __builtin_amdgcn_readfirstlane(found.row),
+                __builtin_amdgcn_readfirstlane(found.end)};
 }
 
 // One 16 x 16 x 128 step: weights (E2M1) by rows of elements of format XF (0: E4M3, 4: E2M1), the scale bytes in
@@ -467,6 +468,169 @@ __global__ __launch_bounds__(kProductThreads) void expert_product_kernel(Product
     }
 }
 
+// The scale word of a lane in the superstep that starts at block `b`: its blocks b + g, b + 4 + g, ..., 127 (the
+// power 1) for those that the row does not have.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t *row, int b, int nb, int g, uint32_t sel)
+{
+    if (b + 16 <= nb) return load_scales(row + b, sel);
+    uint32_t v = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v |= (b + 4 * i + g < nb ? (uint32_t)row[b + 4 * i + g] : 127u) << (8 * i);
+    return v;
+}
+
+// Rows of one expert, 16 * FR at a time, against 256 weight rows: each of the four wavefronts has 64 of its own (32
+// of the gate's and the matching 32 of the up projection's with GLU) and all of k. A step's input rows go through
+// LDS, in the order that the matrix instruction's lanes take them, and are read by every wavefront; the weights,
+// which no two wavefronts share, go straight to registers, kAhead steps before their use.
+template <class T, int XF, int FR, bool GLU>
+__global__ __launch_bounds__(kProductThreads, 2) void expert_product_wide_kernel(ProductArgs a)
+{
+    const int nt = blockIdx.x % a.ntiles, mt = blockIdx.x / a.ntiles;
+    const Tile tile = find_tile<FR * 16>(a, mt);
+    if (tile.expert < 0) return;
+    constexpr int kWaves = kProductThreads / kWave;
+    constexpr int kParts = XF == 4 ? 1 : 2;                   // 16-byte pieces of a lane's 32 elements
+    constexpr int kChunks = FR * kParts / kWaves;             // pieces that a thread carries into LDS in a step
+    constexpr int kRing = FR <= 4 ? 4 : 2, kAhead = kRing - 1;
+    static_assert(FR * kParts % kWaves == 0, "every wavefront carries whole fragments");
+    __shared__ u32x4 xl[2][FR * kParts][kWave];
+    __shared__ uint32_t xsl[2][FR][kWave];
+
+    const int tid = threadIdx.x, lane = tid % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int r = lane % 16, g = lane / 16;
+    constexpr int kOut = GLU ? kFrags / 2 : kFrags;
+    const int half = a.n / 2, col0 = (nt * kWaves + wave) * kOut * 16;
+    const uint32_t wrow = a.k / 2, xrow = XF == 4 ? a.k / 2 : a.k;
+    const uint8_t *wb = a.w + (size_t)tile.expert * a.n * wrow, *wsb = a.ws + (size_t)tile.expert * a.n * a.nb;
+    const uint8_t *xb = a.x + (size_t)tile.row * xrow, *xsb = a.xs + (size_t)tile.row * a.nb;
+    const int last = tile.end - 1 - tile.row;                 // rows past the expert's last read the last one
+    uint32_t wo[kFrags], wso[kFrags];
+#pragma unroll
+    for (int j = 0; j < kFrags; ++j) {
+        // columns past the last one read the last one's weights; their results are not stored
+        const uint32_t row = (GLU && j >= kOut ? half : 0) + min(col0 + (j % kOut) * 16 + r, a.fo - 1);
+        wo[j] = row * wrow;
+        wso[j] = row * a.nb;
+    }
+    uint32_t xo[kChunks];                                     // piece i of this thread: fragment and part
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) xo[i] = min((wave + i * kWaves) % FR * 16 + r, last) * xrow;
+    const uint32_t sel = 0x0c0c0400u + 0x0101u * g;
+    f32x4 acc[FR][kFrags];
+#pragma unroll
+    for (int f = 0; f < FR; ++f)
+#pragma unroll
+        for (int j = 0; j < kFrags; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    const int steps = (a.k + kStep - 1) / kStep;
+    u32x4 wr[kRing][kFrags], xr[kChunks];
+    auto load_w = [&](int slot, int step) {
+        const int at = step * kStep;
+        if (at + kStep <= a.k) {
+#pragma unroll
+            for (int j = 0; j < kFrags; ++j)
+                wr[slot][j] = *reinterpret_cast<const u32x4_a8 *>(wb + (wo[j] + at / 2 + 16 * g));
+        } else if (at < a.k) {
+#pragma unroll
+            for (int j = 0; j < kFrags; ++j) {
+                const i32x8 v = load_last<4>(wb + wo[j], at, g, a.k);
+                wr[slot][j] = u32x4{(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
+            }
+        }
+    };
+    auto load_x = [&](int step) {
+        const int at = step * kStep;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int part = (wave + i * kWaves) / FR;
+            if constexpr (XF == 4) {
+                if (at + kStep <= a.k) xr[i] = *reinterpret_cast<const u32x4_a8 *>(xb + (xo[i] + at / 2 + 16 * g));
+                else {
+                    const i32x8 v = load_last<4>(xb + xo[i], at, g, a.k);
+                    xr[i] = u32x4{(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
+                }
+            } else {
+                const int p = at + 64 * part + 16 * g;
+                xr[i] = u32x4{0, 0, 0, 0};
+                if (p < a.k) xr[i] = *reinterpret_cast<const u32x4 *>(xb + (xo[i] + p));
+            }
+        }
+    };
+    auto keep_x = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) xl[buf][wave + i * kWaves][lane] = xr[i];
+    };
+    // scale words: of the weights in registers, of the input rows in LDS (FR / 4 fragments a wavefront)
+    uint32_t ws[kFrags], wsn[kFrags], xsn[FR / kWaves];
+    auto load_scale = [&](int super) {
+#pragma unroll
+        for (int j = 0; j < kFrags; ++j) wsn[j] = scale_word(wsb + wso[j], super * 16, a.nb, g, sel);
+#pragma unroll
+        for (int i = 0; i < FR / kWaves; ++i) {
+            const int f = wave + i * kWaves;
+            xsn[i] = scale_word(xsb + (uint32_t)(min(f * 16 + r, last) * a.nb), super * 16, a.nb, g, sel);
+        }
+    };
+    auto keep_scale = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < FR / kWaves; ++i) xsl[buf][wave + i * kWaves][lane] = xsn[i];
+    };
+
+    load_scale(0);
+    load_x(0);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load_w(i, i);
+    keep_scale(0);
+    keep_x(0);
+    __syncthreads();
+    for (int super = 0; super * 4 < steps; ++super) {
+        uint32_t xs[FR];
+#pragma unroll
+        for (int j = 0; j < kFrags; ++j) ws[j] = wsn[j];
+#pragma unroll
+        for (int f = 0; f < FR; ++f) xs[f] = xsl[super & 1][f][lane];
+        const bool more = super * 4 + 4 < steps;
+        // One step: fetch the next step's input rows, and the weights kAhead steps on, while this one multiplies
+#define MOE_WIDE_STEP(I)                                                                              \
+        if (super * 4 + I < steps) {                                                                  \
+            const int step = super * 4 + I;                                                           \
+            if (step + 1 < steps) load_x(step + 1);                                                   \
+            load_w((I + kAhead) % kRing, step + kAhead);                                              \
+            if (I == 0 && more) load_scale(super + 1);                                                \
+            _Pragma("unroll") for (int f = 0; f < FR; ++f) {                                          \
+                const i32x8 xf = join(xl[I & 1][f][lane], xl[I & 1][kParts == 2 ? FR + f : f][lane]); \
+                _Pragma("unroll") for (int j = 0; j < kFrags; ++j)                                    \
+                    acc[f][j] = mma<XF, I>(join(wr[I % kRing][j], wr[I % kRing][j]), xf, acc[f][j], ws[j], xs[f]); \
+            }                                                                                         \
+            if (step + 1 < steps) keep_x((I + 1) & 1);                                                \
+            if (I == 3 && more) keep_scale((super + 1) & 1);                                          \
+            __syncthreads();                                                                          \
+        }
+        MOE_WIDE_STEP(0)
+        MOE_WIDE_STEP(1)
+        MOE_WIDE_STEP(2)
+        MOE_WIDE_STEP(3)
+#undef MOE_WIDE_STEP
+    }
+#pragma unroll
+    for (int f = 0; f < FR; ++f) {
+        const int row = tile.row + f * 16 + r;
+        if (row >= tile.end) continue;
+#pragma unroll
+        for (int j = 0; j < kOut; ++j) {
+            f32x4 v = acc[f][j];
+            if (GLU) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = swiglu(v[i], acc[f][j + kOut][i]);
+            }
+            const int col = col0 + j * 16 + 4 * g;
+            if (col < a.fo) store_out<T>(a, row, col, v);
+        }
+    }
+}
+
 int check_mx(long long rows, int cols, int dtype, int element)
 {
     if (rows < 0 || rows > kMaxRows || cols < kPiece || cols % kPiece) return MOE_ERR_SHAPE;
@@ -572,11 +736,15 @@ int moe_expert_product(const void *x, const uint8_t *x_scales, int element, cons
     a.n = n;
     a.nb = (k + kBlock - 1) / kBlock;
     a.fo = glu ? n / 2 : n;
-    constexpr int kRowTile = 16;
-    const int cols = (glu ? kFrags / 2 : kFrags) * 16;
+    // offsets inside one expert's weights, and inside the rows of one tile, are 32-bit
+    if ((long long)n * k > 4ll << 30 || k > 1 << 24) return MOE_ERR_SHAPE;
+    const int each = rows / a.E;                // rows of an expert, were they even
+    const int frags = each <= 8 ? 1 : (each <= 40 ? 4 : 8);
+    const bool wide = frags > 1;
+    const int cols = (glu ? kFrags / 2 : kFrags) * 16 * (wide ? kProductThreads / kWave : 1);
     a.ntiles = (a.fo + cols - 1) / cols;
     // a tile starts at every expert's first row, so at most this many
-    const long long mtiles = rows / kRowTile + std::min(a.E, rows);
+    const long long mtiles = rows / (frags * 16) + std::min(a.E, rows);
     if (mtiles * a.ntiles > INT_MAX) return MOE_ERR_SHAPE;
     if (rows == 0) return MOE_OK;
     if (!x || !x_scales || !weights || !weight_scales || !ep_recv_count || !out) return MOE_ERR_NULLPTR;
@@ -591,10 +759,16 @@ int moe_expert_product(const void *x, const uint8_t *x_scales, int element, cons
     const dim3 g((unsigned)(mtiles * a.ntiles)), b(kProductThreads);
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
+#define MOE_PRODUCT_G(T, XF, G)                                                                       \
+    do {                                                                                              \
+        if (frags == 1) hipLaunchKernelGGL((expert_product_kernel<T, XF, 1, G>), g, b, 0, st, a);     \
+        else if (frags == 4) hipLaunchKernelGGL((expert_product_wide_kernel<T, XF, 4, G>), g, b, 0, st, a); \
+        else hipLaunchKernelGGL((expert_product_wide_kernel<T, XF, 8, G>), g, b, 0, st, a);           \
+    } while (0)
 #define MOE_PRODUCT(T, XF)                                                                            \
     do {                                                                                              \
-        if (glu) hipLaunchKernelGGL((expert_product_kernel<T, XF, kRowTile / 16, true>), g, b, 0, st, a);  \
-        else hipLaunchKernelGGL((expert_product_kernel<T, XF, kRowTile / 16, false>), g, b, 0, st, a);     \
+        if (glu) MOE_PRODUCT_G(T, XF, true);                                                          \
+        else MOE_PRODUCT_G(T, XF, false);                                                             \
     } while (0)
     if (dtype == MOE_FP16) {
         if (element == MOE_MX_E2M1) MOE_PRODUCT(F16, 4);
@@ -604,6 +778,7 @@ int moe_expert_product(const void *x, const uint8_t *x_scales, int element, cons
         else MOE_PRODUCT(BF16, 0);
     }
 #undef MOE_PRODUCT
+#undef MOE_PRODUCT_G
     return launched();
 }
 
