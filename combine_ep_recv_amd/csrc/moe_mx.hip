@@ -340,10 +340,13 @@ __device__ __forceinline__ i32x8 load_last(const uint8_t *row, int at, int g, in
     return join(lo, hi);
 }
 // The scale bytes of a lane's blocks in four steps: byte g of each word of the row's 16 bytes, one word
+__device__ __forceinline__ uint32_t pick_scales(u32x4 d, uint32_t sel)
+{
+    return __builtin_amdgcn_perm(d[1], d[0], sel) | (__builtin_amdgcn_perm(d[3], d[2], sel) << 16);
+}
 __device__ __forceinline__ uint32_t load_scales(const uint8_t *p, uint32_t sel)
 {
-    const u32x4 d = *reinterpret_cast<const u32x4_a1 *>(p);
-    return __builtin_amdgcn_perm(d[1], d[0], sel) | (__builtin_amdgcn_perm(d[3], d[2], sel) << 16);
+    return pick_scales(*reinterpret_cast<const u32x4_a1 *>(p), sel);
 }
 
 template <class T>
@@ -468,17 +471,6 @@ __global__ __launch_bounds__(kProductThreads) void expert_product_kernel(Product
     }
 }
 
-// The scale word of a lane in the superstep that starts at block `b`: its blocks b + g, b + 4 + g, ..., 127 (the
-// power 1) for those that the row does not have.
-__device__ __forceinline__ uint32_t scale_word(const uint8_t *row, int b, int nb, int g, uint32_t sel)
-{
-    if (b + 16 <= nb) return load_scales(row + b, sel);
-    uint32_t v = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v |= (b + 4 * i + g < nb ? (uint32_t)row[b + 4 * i + g] : 127u) << (8 * i);
-    return v;
-}
-
 // Rows of one expert, 16 * FR at a time, against 256 weight rows: each of the four wavefronts has 64 of its own (32
 // of the gate's and the matching 32 of the up projection's with GLU) and all of k. A step's input rows go through
 // LDS, in the order that the matrix instruction's lanes take them, and are read by every wavefront; the weights,
@@ -524,88 +516,69 @@ __global__ __launch_bounds__(kProductThreads, 2) void expert_product_wide_kernel
 #pragma unroll
         for (int j = 0; j < kFrags; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const int steps = (a.k + kStep - 1) / kStep;
-    u32x4 wr[kRing][kFrags], xr[kChunks];
+    const int supers = a.k / kSuper;
+    u32x4 wr[kRing][kFrags], xr[kChunks], wsr[kFrags], xsr[FR / kWaves];
+    // Loads of whole steps and supersteps. Beyond the last one the last one is read again, and not used: a branch
+    // here would make the compiler wait for the load at its end.
     auto load_w = [&](int slot, int step) {
-        const int at = step * kStep;
-        if (at + kStep <= a.k) {
+        const uint32_t at = min(step, supers * 4 - 1) * (kStep / 2) + 16 * g;
 #pragma unroll
-            for (int j = 0; j < kFrags; ++j)
-                wr[slot][j] = *reinterpret_cast<const u32x4_a8 *>(wb + (wo[j] + at / 2 + 16 * g));
-        } else if (at < a.k) {
-#pragma unroll
-            for (int j = 0; j < kFrags; ++j) {
-                const i32x8 v = load_last<4>(wb + wo[j], at, g, a.k);
-                wr[slot][j] = u32x4{(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
-            }
-        }
+        for (int j = 0; j < kFrags; ++j) wr[slot][j] = *reinterpret_cast<const u32x4_a8 *>(wb + (wo[j] + at));
     };
     auto load_x = [&](int step) {
-        const int at = step * kStep;
+        const uint32_t at = min(step, supers * 4 - 1) * (XF == 4 ? kStep / 2 : kStep) + 16 * g;
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int part = (wave + i * kWaves) / FR;
-            if constexpr (XF == 4) {
-                if (at + kStep <= a.k) xr[i] = *reinterpret_cast<const u32x4_a8 *>(xb + (xo[i] + at / 2 + 16 * g));
-                else {
-                    const i32x8 v = load_last<4>(xb + xo[i], at, g, a.k);
-                    xr[i] = u32x4{(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
-                }
-            } else {
-                const int p = at + 64 * part + 16 * g;
-                xr[i] = u32x4{0, 0, 0, 0};
-                if (p < a.k) xr[i] = *reinterpret_cast<const u32x4 *>(xb + (xo[i] + p));
-            }
-        }
+        for (int i = 0; i < kChunks; ++i)
+            xr[i] = *reinterpret_cast<const u32x4_a8 *>(xb + (xo[i] + at + 64 * ((wave + i * kWaves) / FR)));
     };
     auto keep_x = [&](int buf) {
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) xl[buf][wave + i * kWaves][lane] = xr[i];
     };
     // scale words: of the weights in registers, of the input rows in LDS (FR / 4 fragments a wavefront)
-    uint32_t ws[kFrags], wsn[kFrags], xsn[FR / kWaves];
+    uint32_t ws[kFrags], xsn[FR / kWaves], xso[FR / kWaves];
+#pragma unroll
+    for (int i = 0; i < FR / kWaves; ++i) xso[i] = (uint32_t)min((wave + i * kWaves) * 16 + r, last) * a.nb;
     auto load_scale = [&](int super) {
+        const uint32_t at = min(super, supers - 1) * 16;
 #pragma unroll
-        for (int j = 0; j < kFrags; ++j) wsn[j] = scale_word(wsb + wso[j], super * 16, a.nb, g, sel);
+        for (int j = 0; j < kFrags; ++j) wsr[j] = *reinterpret_cast<const u32x4_a1 *>(wsb + (wso[j] + at));
 #pragma unroll
-        for (int i = 0; i < FR / kWaves; ++i) {
-            const int f = wave + i * kWaves;
-            xsn[i] = scale_word(xsb + (uint32_t)(min(f * 16 + r, last) * a.nb), super * 16, a.nb, g, sel);
-        }
+        for (int i = 0; i < FR / kWaves; ++i) xsr[i] = *reinterpret_cast<const u32x4_a1 *>(xsb + (xso[i] + at));
     };
     auto keep_scale = [&](int buf) {
 #pragma unroll
-        for (int i = 0; i < FR / kWaves; ++i) xsl[buf][wave + i * kWaves][lane] = xsn[i];
+        for (int j = 0; j < kFrags; ++j) ws[j] = pick_scales(wsr[j], sel);
+#pragma unroll
+        for (int i = 0; i < FR / kWaves; ++i) xsl[buf][wave + i * kWaves][lane] = pick_scales(xsr[i], sel);
     };
 
-    load_scale(0);
-    load_x(0);
+    if (supers > 0) {
+        load_scale(0);
+        load_x(0);
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) load_w(i, i);
-    keep_scale(0);
-    keep_x(0);
-    __syncthreads();
-    for (int super = 0; super * 4 < steps; ++super) {
+        for (int i = 0; i < kAhead; ++i) load_w(i, i);
+        keep_scale(0);
+        keep_x(0);
+        __syncthreads();
+    }
+    for (int super = 0; super < supers; ++super) {
         uint32_t xs[FR];
 #pragma unroll
-        for (int j = 0; j < kFrags; ++j) ws[j] = wsn[j];
-#pragma unroll
         for (int f = 0; f < FR; ++f) xs[f] = xsl[super & 1][f][lane];
-        const bool more = super * 4 + 4 < steps;
         // One step: fetch the next step's input rows, and the weights kAhead steps on, while this one multiplies
 #define MOE_WIDE_STEP(I)                                                                              \
-        if (super * 4 + I < steps) {                                                                  \
-            const int step = super * 4 + I;                                                           \
-            if (step + 1 < steps) load_x(step + 1);                                                   \
-            load_w((I + kAhead) % kRing, step + kAhead);                                              \
-            if (I == 0 && more) load_scale(super + 1);                                                \
+        {                                                                                             \
+            load_x(super * 4 + I + 1);                                                                \
+            load_w((I + kAhead) % kRing, super * 4 + I + kAhead);                                     \
+            if (I == 2) load_scale(super + 1);                                                        \
             _Pragma("unroll") for (int f = 0; f < FR; ++f) {                                          \
                 const i32x8 xf = join(xl[I & 1][f][lane], xl[I & 1][kParts == 2 ? FR + f : f][lane]); \
                 _Pragma("unroll") for (int j = 0; j < kFrags; ++j)                                    \
                     acc[f][j] = mma<XF, I>(join(wr[I % kRing][j], wr[I % kRing][j]), xf, acc[f][j], ws[j], xs[f]); \
             }                                                                                         \
-            if (step + 1 < steps) keep_x((I + 1) & 1);                                                \
-            if (I == 3 && more) keep_scale((super + 1) & 1);                                          \
+            keep_x((I + 1) & 1);                                                                      \
+            if (I == 3) keep_scale((super + 1) & 1);                                                  \
             __syncthreads();                                                                          \
         }
         MOE_WIDE_STEP(0)
@@ -613,6 +586,32 @@ __global__ __launch_bounds__(kProductThreads, 2) void expert_product_wide_kernel
         MOE_WIDE_STEP(2)
         MOE_WIDE_STEP(3)
 #undef MOE_WIDE_STEP
+    }
+    // the last k % 512 elements, a step at a time (every wavefront is past its last read of xl here)
+    for (int at = supers * kSuper; at < a.k; at += kStep) {
+        const int b = at / kBlock + g;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const i32x8 v = load_last<XF>(xb + xo[i], at, g, a.k);
+            const int h = (wave + i * kWaves) / FR * 4;
+            xl[0][wave + i * kWaves][lane] = u32x4{(uint32_t)v[h], (uint32_t)v[h + 1], (uint32_t)v[h + 2], (uint32_t)v[h + 3]};
+        }
+#pragma unroll
+        for (int i = 0; i < FR / kWaves; ++i) xsl[0][wave + i * kWaves][lane] = b < a.nb ? xsb[xso[i] + b] : 127;
+        i32x8 wf[kFrags];
+#pragma unroll
+        for (int j = 0; j < kFrags; ++j) {
+            wf[j] = load_last<4>(wb + wo[j], at, g, a.k);
+            ws[j] = b < a.nb ? wsb[wso[j] + b] : 127;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int f = 0; f < FR; ++f) {
+            const i32x8 xf = join(xl[0][f][lane], xl[0][kParts == 2 ? FR + f : f][lane]);
+#pragma unroll
+            for (int j = 0; j < kFrags; ++j) acc[f][j] = mma<XF, 0>(wf[j], xf, acc[f][j], ws[j], xsl[0][f][lane]);
+        }
+        __syncthreads();
     }
 #pragma unroll
     for (int f = 0; f < FR; ++f) {
