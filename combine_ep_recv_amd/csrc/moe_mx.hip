@@ -572,14 +572,22 @@ __global__ __launch_bounds__(kProductThreads, 2) void expert_product_wide_kernel
             load_x(super * 4 + I + 1);                                                                \
             load_w((I + kAhead) % kRing, super * 4 + I + kAhead);                                     \
             if (I == 2) load_scale(super + 1);                                                        \
+            __builtin_amdgcn_sched_barrier(0);                                                        \
             _Pragma("unroll") for (int f = 0; f < FR; ++f) {                                          \
                 const i32x8 xf = join(xl[I & 1][f][lane], xl[I & 1][kParts == 2 ? FR + f : f][lane]); \
                 _Pragma("unroll") for (int j = 0; j < kFrags; ++j)                                    \
                     acc[f][j] = mma<XF, I>(join(wr[I % kRing][j], wr[I % kRing][j]), xf, acc[f][j], ws[j], xs[f]); \
             }                                                                                         \
+            __builtin_amdgcn_sched_group_barrier(0x100, 2 * kParts, 0);                               \
+            _Pragma("unroll") for (int f = 0; f < FR; ++f) {                                          \
+                __builtin_amdgcn_sched_group_barrier(0x008, kFrags, 0);                               \
+                __builtin_amdgcn_sched_group_barrier(0x100, kParts, 0);                               \
+            }                                                                                         \
+            __builtin_amdgcn_sched_barrier(0);                                                        \
             keep_x((I + 1) & 1);                                                                      \
             if (I == 3) keep_scale((super + 1) & 1);                                                  \
             __syncthreads();                                                                          \
+            __builtin_amdgcn_sched_barrier(0);                                                        \
         }
         MOE_WIDE_STEP(0)
         MOE_WIDE_STEP(1)
