@@ -339,14 +339,35 @@ __device__ __forceinline__ i32x8 load_last(const uint8_t *row, int at, int g, in
     }
     return join(lo, hi);
 }
-// The scale bytes of a lane's blocks in four steps: byte g of each word of the row's 16 bytes, one word
-__device__ __forceinline__ uint32_t pick_scales(u32x4 d, uint32_t sel)
+// 16 bytes of a step, piece p of a row (`row` points at its own first piece), with zeros past the row's k elements
+template <int XF>
+__device__ __forceinline__ u32x4 load_piece_or_zero(const uint8_t *row, int at, int p, int k)
 {
-    return __builtin_amdgcn_perm(d[1], d[0], sel) | (__builtin_amdgcn_perm(d[3], d[2], sel) << 16);
+    constexpr int kElems = XF == 4 ? 32 : 16;
+    const int first = at + p * kElems;
+    u32x4 v = {0, 0, 0, 0};
+    const uint8_t *q = row + (XF == 4 ? at / 2 : at);
+    if (first + kElems <= k) v = *reinterpret_cast<const u32x4_a8 *>(q);
+    else if (first < k) {                              // E2M1 only: half a block
+        const u32x2 h = *reinterpret_cast<const u32x2 *>(q);
+        v[0] = h[0];
+        v[1] = h[1];
+    }
+    return v;
 }
+// The scale bytes of a lane's blocks in four steps: byte g of each word of the row's 16 bytes, one word
 __device__ __forceinline__ uint32_t load_scales(const uint8_t *p, uint32_t sel)
 {
-    return pick_scales(*reinterpret_cast<const u32x4_a1 *>(p), sel);
+    const u32x4 d = *reinterpret_cast<const u32x4_a1 *>(p);
+    return __builtin_amdgcn_perm(d[1], d[0], sel) | (__builtin_amdgcn_perm(d[3], d[2], sel) << 16);
+}
+// ... for every g: a transpose of 4 x 4 bytes
+__device__ __forceinline__ u32x4 by_group(u32x4 d)
+{
+    const uint32_t a = __builtin_amdgcn_perm(d[1], d[0], 0x05010400u), b = __builtin_amdgcn_perm(d[3], d[2], 0x05010400u);
+    const uint32_t c = __builtin_amdgcn_perm(d[1], d[0], 0x07030602u), e = __builtin_amdgcn_perm(d[3], d[2], 0x07030602u);
+    return u32x4{__builtin_amdgcn_perm(b, a, 0x05040100u), __builtin_amdgcn_perm(b, a, 0x07060302u),
+                 __builtin_amdgcn_perm(e, c, 0x05040100u), __builtin_amdgcn_perm(e, c, 0x07060302u)};
 }
 
 template <class T>
@@ -472,120 +493,133 @@ __global__ __launch_bounds__(kProductThreads) void expert_product_kernel(Product
 }
 
 // Rows of one expert, 16 * FR at a time, against 256 weight rows: each of the four wavefronts has 64 of its own (32
-// of the gate's and the matching 32 of the up projection's with GLU) and all of k. A step's input rows go through
-// LDS, in the order that the matrix instruction's lanes take them, and are read by every wavefront; the weights,
-// which no two wavefronts share, go straight to registers, kAhead steps before their use.
+// of the gate's and the matching 32 of the up projection's with GLU) and all of k, in steps of 128. Both sides go
+// through LDS: a matrix instruction's lane holds 16 bytes of a row whose neighbours sit in lanes 16 apart, so loading
+// straight into its layout makes the cache look at every lane's 16 bytes by itself (one look-up a clock), where four
+// adjacent lanes that read 64 bytes of a row count as one. LDS keeps 64 (E4M3: 128) bytes of each row; the 16-byte
+// pieces of a row are swapped by its number so that the writers' and the readers' eight lanes a clock meet every bank
+// once. Scale bytes come a superstep (four steps) at a time and are turned into a word per (row, g) there.
 template <class T, int XF, int FR, bool GLU>
 __global__ __launch_bounds__(kProductThreads, 2) void expert_product_wide_kernel(ProductArgs a)
 {
     const int nt = blockIdx.x % a.ntiles, mt = blockIdx.x / a.ntiles;
     const Tile tile = find_tile<FR * 16>(a, mt);
     if (tile.expert < 0) return;
-    constexpr int kWaves = kProductThreads / kWave;
-    constexpr int kParts = XF == 4 ? 1 : 2;                   // 16-byte pieces of a lane's 32 elements
-    constexpr int kChunks = FR * kParts / kWaves;             // pieces that a thread carries into LDS in a step
-    constexpr int kRing = FR <= 4 ? 4 : 2, kAhead = kRing - 1;
-    static_assert(FR * kParts % kWaves == 0, "every wavefront carries whole fragments");
-    __shared__ u32x4 xl[2][FR * kParts][kWave];
-    __shared__ uint32_t xsl[2][FR][kWave];
+    constexpr int kWaves = kProductThreads / kWave, kRowsW = kWaves * kFrags * 16, kRowsX = FR * 16;
+    constexpr int kPx = XF == 4 ? 4 : 8;                      // 16-byte pieces of an input row in a step
+    constexpr int kLoadsW = kRowsW * 4 / kProductThreads, kLoadsX = kRowsX * kPx / kProductThreads;
+    static_assert(kRowsW == kProductThreads && kRowsX <= kProductThreads, "one scale row a thread");
+    static_assert(kRowsX * kPx % kProductThreads == 0, "every thread carries as many pieces");
+    __shared__ u32x4 wl[2][kRowsW * 4], xl[2][kRowsX * kPx], wsl[2][kRowsW], xsl[2][kRowsX];
 
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int r = lane % 16, g = lane / 16;
     constexpr int kOut = GLU ? kFrags / 2 : kFrags;
-    const int half = a.n / 2, col0 = (nt * kWaves + wave) * kOut * 16;
+    const int half = a.n / 2, tile0 = nt * kWaves * kOut * 16;
     const uint32_t wrow = a.k / 2, xrow = XF == 4 ? a.k / 2 : a.k;
     const uint8_t *wb = a.w + (size_t)tile.expert * a.n * wrow, *wsb = a.ws + (size_t)tile.expert * a.n * a.nb;
     const uint8_t *xb = a.x + (size_t)tile.row * xrow, *xsb = a.xs + (size_t)tile.row * a.nb;
     const int last = tile.end - 1 - tile.row;                 // rows past the expert's last read the last one
-    uint32_t wo[kFrags], wso[kFrags];
+    // weight row of a place in the tile; columns past the last one read the last one's, and are not stored
+    auto weight_row = [&](int q) -> uint32_t {
+        const int c = GLU ? q / 64 * 32 + q % 32 : q;
+        return (GLU && q % 64 >= 32 ? half : 0) + min(tile0 + c, a.fo - 1);
+    };
+    // this thread's pieces: where in a row's step, and the place in LDS
+    uint32_t wo[kLoadsW], xo[kLoadsX];
+    int wat[kLoadsW], xat[kLoadsX];
 #pragma unroll
-    for (int j = 0; j < kFrags; ++j) {
-        // columns past the last one read the last one's weights; their results are not stored
-        const uint32_t row = (GLU && j >= kOut ? half : 0) + min(col0 + (j % kOut) * 16 + r, a.fo - 1);
-        wo[j] = row * wrow;
-        wso[j] = row * a.nb;
+    for (int i = 0; i < kLoadsW; ++i) {
+        const int c = tid + i * kProductThreads, q = c / 4, p = c % 4;
+        wo[i] = weight_row(q) * wrow + 16 * p;
+        wat[i] = q * 4 + (p ^ ((q >> 1) & 3));
     }
-    uint32_t xo[kChunks];                                     // piece i of this thread: fragment and part
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) xo[i] = min((wave + i * kWaves) % FR * 16 + r, last) * xrow;
-    const uint32_t sel = 0x0c0c0400u + 0x0101u * g;
+    for (int i = 0; i < kLoadsX; ++i) {
+        const int c = tid + i * kProductThreads, q = c / kPx, p = c % kPx;
+        xo[i] = (uint32_t)min(q, last) * xrow + 16 * p;
+        xat[i] = q * kPx + (XF == 4 ? p ^ ((q >> 1) & 3) : p ^ (q & 7));
+    }
+    const uint32_t wso = weight_row(tid) * a.nb, xso = (uint32_t)min(tid % kRowsX, last) * a.nb;
+    // a reader's pieces: of fragment 0, the others lie 16 rows apart
+    const int wfrag = (wave * 64 + r) * 4 + (g ^ ((r >> 1) & 3));
+    const int xfrag = XF == 4 ? r * 4 + (g ^ ((r >> 1) & 3)) : r * 8 + (g ^ (r & 7));
+    const int xfrag2 = XF == 4 ? xfrag : r * 8 + ((4 + g) ^ (r & 7));
+
     f32x4 acc[FR][kFrags];
 #pragma unroll
     for (int f = 0; f < FR; ++f)
 #pragma unroll
         for (int j = 0; j < kFrags; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const int supers = a.k / kSuper;
-    u32x4 wr[kRing][kFrags], xr[kChunks], wsr[kFrags], xsr[FR / kWaves];
+    const int supers = a.k / kSuper, steps = supers * 4;
+    u32x4 wr[kLoadsW], xr[kLoadsX], wsr, xsr;
     // Loads of whole steps and supersteps. Beyond the last one the last one is read again, and not used: a branch
     // here would make the compiler wait for the load at its end.
-    auto load_w = [&](int slot, int step) {
-        const uint32_t at = min(step, supers * 4 - 1) * (kStep / 2) + 16 * g;
+    auto load = [&](int step) {
+        const uint32_t at = min(step, steps - 1);
 #pragma unroll
-        for (int j = 0; j < kFrags; ++j) wr[slot][j] = *reinterpret_cast<const u32x4_a8 *>(wb + (wo[j] + at));
+        for (int i = 0; i < kLoadsW; ++i) wr[i] = *reinterpret_cast<const u32x4_a8 *>(wb + (wo[i] + at * (kStep / 2)));
+#pragma unroll
+        for (int i = 0; i < kLoadsX; ++i)
+            xr[i] = *reinterpret_cast<const u32x4_a8 *>(xb + (xo[i] + at * (XF == 4 ? kStep / 2 : kStep)));
     };
-    auto load_x = [&](int step) {
-        const uint32_t at = min(step, supers * 4 - 1) * (XF == 4 ? kStep / 2 : kStep) + 16 * g;
+    auto keep = [&](int buf) {
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i)
-            xr[i] = *reinterpret_cast<const u32x4_a8 *>(xb + (xo[i] + at + 64 * ((wave + i * kWaves) / FR)));
+        for (int i = 0; i < kLoadsW; ++i) wl[buf][wat[i]] = wr[i];
+#pragma unroll
+        for (int i = 0; i < kLoadsX; ++i) xl[buf][xat[i]] = xr[i];
     };
-    auto keep_x = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) xl[buf][wave + i * kWaves][lane] = xr[i];
-    };
-    // scale words: of the weights in registers, of the input rows in LDS (FR / 4 fragments a wavefront)
-    uint32_t ws[kFrags], xsn[FR / kWaves], xso[FR / kWaves];
-#pragma unroll
-    for (int i = 0; i < FR / kWaves; ++i) xso[i] = (uint32_t)min((wave + i * kWaves) * 16 + r, last) * a.nb;
-    auto load_scale = [&](int super) {
+    auto load_scales = [&](int super) {
         const uint32_t at = min(super, supers - 1) * 16;
-#pragma unroll
-        for (int j = 0; j < kFrags; ++j) wsr[j] = *reinterpret_cast<const u32x4_a1 *>(wsb + (wso[j] + at));
-#pragma unroll
-        for (int i = 0; i < FR / kWaves; ++i) xsr[i] = *reinterpret_cast<const u32x4_a1 *>(xsb + (xso[i] + at));
+        wsr = *reinterpret_cast<const u32x4_a1 *>(wsb + (wso + at));
+        xsr = *reinterpret_cast<const u32x4_a1 *>(xsb + (xso + at));
     };
-    auto keep_scale = [&](int buf) {
-#pragma unroll
-        for (int j = 0; j < kFrags; ++j) ws[j] = pick_scales(wsr[j], sel);
-#pragma unroll
-        for (int i = 0; i < FR / kWaves; ++i) xsl[buf][wave + i * kWaves][lane] = pick_scales(xsr[i], sel);
+    auto keep_scales = [&](int buf) {
+        wsl[buf][tid] = by_group(wsr);
+        xsl[buf][tid % kRowsX] = by_group(xsr);          // threads of the same row write the same bytes
     };
+    const uint32_t *wsw = reinterpret_cast<const uint32_t *>(wsl) + (wave * 64 + r) * 4 + g;
+    const uint32_t *xsw = reinterpret_cast<const uint32_t *>(xsl) + r * 4 + g;
 
     if (supers > 0) {
-        load_scale(0);
-        load_x(0);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) load_w(i, i);
-        keep_scale(0);
-        keep_x(0);
+        load_scales(0);
+        load(0);
+        keep_scales(0);
+        keep(0);
+        load(1);
         __syncthreads();
     }
     for (int super = 0; super < supers; ++super) {
-        uint32_t xs[FR];
+        uint32_t ws[kFrags], xs[FR];
 #pragma unroll
-        for (int f = 0; f < FR; ++f) xs[f] = xsl[super & 1][f][lane];
-        // One step: fetch the next step's input rows, and the weights kAhead steps on, while this one multiplies
+        for (int j = 0; j < kFrags; ++j) ws[j] = wsw[(super & 1) * kRowsW * 4 + j * 64];
+#pragma unroll
+        for (int f = 0; f < FR; ++f) xs[f] = xsw[(super & 1) * kRowsX * 4 + f * 64];
+        // One step: what was fetched for the next one goes into the other half of LDS, the one after is fetched
+        // meanwhile, and this one multiplies
 #define MOE_WIDE_STEP(I)                                                                              \
         {                                                                                             \
-            load_x(super * 4 + I + 1);                                                                \
-            load_w((I + kAhead) % kRing, super * 4 + I + kAhead);                                     \
-            if (I == 2) load_scale(super + 1);                                                        \
+            keep((I + 1) & 1);                                                                        \
+            if (I == 3) keep_scales((super + 1) & 1);                                                 \
+            load(super * 4 + I + 2);                                                                  \
+            if (I == 1) load_scales(super + 1);                                                       \
             __builtin_amdgcn_sched_barrier(0);                                                        \
+            i32x8 wf[kFrags];                                                                         \
+            _Pragma("unroll") for (int j = 0; j < kFrags; ++j)                                        \
+                wf[j] = join(wl[I & 1][wfrag + j * 64], wl[I & 1][wfrag + j * 64]);                   \
             _Pragma("unroll") for (int f = 0; f < FR; ++f) {                                          \
-                const i32x8 xf = join(xl[I & 1][f][lane], xl[I & 1][kParts == 2 ? FR + f : f][lane]); \
+                const i32x8 xf = join(xl[I & 1][xfrag + f * 16 * kPx], xl[I & 1][xfrag2 + f * 16 * kPx]); \
                 _Pragma("unroll") for (int j = 0; j < kFrags; ++j)                                    \
-                    acc[f][j] = mma<XF, I>(join(wr[I % kRing][j], wr[I % kRing][j]), xf, acc[f][j], ws[j], xs[f]); \
+                    acc[f][j] = mma<XF, I>(wf[j], xf, acc[f][j], ws[j], xs[f]);                       \
             }                                                                                         \
-            __builtin_amdgcn_sched_group_barrier(0x100, 2 * kParts, 0);                               \
+            __builtin_amdgcn_sched_group_barrier(0x100, kFrags + 2 * kPx / 4, 0);                     \
             _Pragma("unroll") for (int f = 0; f < FR; ++f) {                                          \
                 __builtin_amdgcn_sched_group_barrier(0x008, kFrags, 0);                               \
-                __builtin_amdgcn_sched_group_barrier(0x100, kParts, 0);                               \
+                __builtin_amdgcn_sched_group_barrier(0x100, kPx / 4, 0);                              \
             }                                                                                         \
             __builtin_amdgcn_sched_barrier(0);                                                        \
-            keep_x((I + 1) & 1);                                                                      \
-            if (I == 3) keep_scale((super + 1) & 1);                                                  \
             __syncthreads();                                                                          \
             __builtin_amdgcn_sched_barrier(0);                                                        \
         }
@@ -595,29 +629,32 @@ __global__ __launch_bounds__(kProductThreads, 2) void expert_product_wide_kernel
         MOE_WIDE_STEP(3)
 #undef MOE_WIDE_STEP
     }
-    // the last k % 512 elements, a step at a time (every wavefront is past its last read of xl here)
+    // the last k % 512 elements, a step at a time (every wavefront is past its last read of LDS here)
     for (int at = supers * kSuper; at < a.k; at += kStep) {
-        const int b = at / kBlock + g;
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const i32x8 v = load_last<XF>(xb + xo[i], at, g, a.k);
-            const int h = (wave + i * kWaves) / FR * 4;
-            xl[0][wave + i * kWaves][lane] = u32x4{(uint32_t)v[h], (uint32_t)v[h + 1], (uint32_t)v[h + 2], (uint32_t)v[h + 3]};
+        for (int i = 0; i < kLoadsW; ++i)
+            wl[0][wat[i]] = load_piece_or_zero<4>(wb + wo[i], at, (tid + i * kProductThreads) % 4, a.k);
+#pragma unroll
+        for (int i = 0; i < kLoadsX; ++i)
+            xl[0][xat[i]] = load_piece_or_zero<XF>(xb + xo[i], at, (tid + i * kProductThreads) % kPx, a.k);
+        const int b = at / kBlock;
+        u32x4 ws4, xs4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ws4[i] = b + i < a.nb ? wsb[wso + b + i] : 127;
+            xs4[i] = b + i < a.nb ? xsb[xso + b + i] : 127;
         }
-#pragma unroll
-        for (int i = 0; i < FR / kWaves; ++i) xsl[0][wave + i * kWaves][lane] = b < a.nb ? xsb[xso[i] + b] : 127;
+        wsl[0][tid] = ws4;
+        xsl[0][tid % kRowsX] = xs4;
+        __syncthreads();
         i32x8 wf[kFrags];
 #pragma unroll
-        for (int j = 0; j < kFrags; ++j) {
-            wf[j] = load_last<4>(wb + wo[j], at, g, a.k);
-            ws[j] = b < a.nb ? wsb[wso[j] + b] : 127;
-        }
-        __syncthreads();
+        for (int j = 0; j < kFrags; ++j) wf[j] = join(wl[0][wfrag + j * 64], wl[0][wfrag + j * 64]);
 #pragma unroll
         for (int f = 0; f < FR; ++f) {
-            const i32x8 xf = join(xl[0][f][lane], xl[0][kParts == 2 ? FR + f : f][lane]);
+            const i32x8 xf = join(xl[0][xfrag + f * 16 * kPx], xl[0][xfrag2 + f * 16 * kPx]);
 #pragma unroll
-            for (int j = 0; j < kFrags; ++j) acc[f][j] = mma<XF, 0>(wf[j], xf, acc[f][j], ws[j], xsl[0][f][lane]);
+            for (int j = 0; j < kFrags; ++j) acc[f][j] = mma<XF, 0>(wf[j], xf, acc[f][j], wsw[j * 64], xsw[f * 64]);
         }
         __syncthreads();
     }
@@ -632,7 +669,7 @@ __global__ __launch_bounds__(kProductThreads, 2) void expert_product_wide_kernel
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = swiglu(v[i], acc[f][j + kOut][i]);
             }
-            const int col = col0 + j * 16 + 4 * g;
+            const int col = tile0 + (wave * kOut + j) * 16 + 4 * g;
             if (col < a.fo) store_out<T>(a, row, col, v);
         }
     }
