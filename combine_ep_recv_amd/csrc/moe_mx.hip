@@ -211,6 +211,7 @@ constexpr int kMaxExperts = 1024;          // dispatch's limits
 constexpr int kMinWorld = 2, kMaxWorld = 768;
 constexpr int kStep = 128;                 // elements of k in one matrix instruction
 constexpr int kSuper = 4 * kStep;          // ... in a group of four, whose 16 scale bytes are one load
+constexpr int kWorkgroups = 1024;          // at most: every CU's fill, with tiles to spare for none
 constexpr int kFrags = 4;                  // 16-wide weight fragments of a workgroup
 
 struct ProductArgs {
@@ -222,20 +223,25 @@ struct ProductArgs {
 };
 
 struct Tile {
-    int expert, row, end;                  // expert -1: no such tile
+    int expert, row, end;                  // rows row..end-1 of the expert, whose last row is end - 1
 };
 
-// Row tile `mt` of BM rows: expert e's rows follow expert e-1's, and each expert starts a tile of its own. The
-// counts are ep_recv_count's differences, held within [0, rows] whatever the array holds. All threads call it.
+// Where each expert's rows and row tiles begin: expert e's rows follow expert e-1's, and each expert starts a tile of
+// its own. One copy in each workgroup's LDS, made once: workgroups stay for many tiles.
+struct Plan {
+    uint32_t row[kMaxExperts + 1], tile[kMaxExperts + 1];
+    uint32_t part[2][kProductThreads / kWave];
+    int expert;
+};
+
+// Fills the plan for tiles of BM rows and returns their number. The counts are ep_recv_count's differences, held
+// within [0, rows] whatever the array holds. All threads call it.
 template <int BM>
-__device__ Tile find_tile(const ProductArgs &a, int mt)
+__device__ int make_plan(const ProductArgs &a, Plan &plan)
 {
-    __shared__ uint32_t part[2][kProductThreads / kWave];
-    __shared__ Tile found;
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     constexpr int kEach = kMaxExperts / kProductThreads;
     const uint32_t most = (uint32_t)a.rows;
-    if (tid == 0) found.expert = -1;
     uint32_t count[kEach], sum = 0;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
@@ -256,11 +262,11 @@ __device__ Tile find_tile(const ProductArgs &a, int mt)
         const uint32_t v = __shfl_up(inc, d);
         if (lane >= d) inc = min(most, inc + v);
     }
-    if (lane == kWave - 1) part[0][wave] = inc;
+    if (lane == kWave - 1) plan.part[0][wave] = inc;
     uint32_t before = __shfl_up(inc, 1);
     if (lane == 0) before = 0;
     __syncthreads();
-    for (int i = 0; i < wave; ++i) before = min(most, before + part[0][i]);
+    for (int i = 0; i < wave; ++i) before = min(most, before + plan.part[0][i]);
     uint32_t start[kEach + 1], tiles = 0;
     start[0] = before;
 #pragma unroll
@@ -274,23 +280,35 @@ __device__ Tile find_tile(const ProductArgs &a, int mt)
         const uint32_t v = __shfl_up(inc, d);
         if (lane >= d) inc += v;
     }
-    if (lane == kWave - 1) part[1][wave] = inc;
+    if (lane == kWave - 1) plan.part[1][wave] = inc;
     uint32_t at = inc - tiles;
     __syncthreads();
-    for (int i = 0; i < wave; ++i) at += part[1][i];
+    for (int i = 0; i < wave; ++i) at += plan.part[1][i];
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-        const uint32_t c = (start[i + 1] - start[i] + BM - 1) / BM;
-        if ((uint32_t)mt >= at && (uint32_t)mt < at + c) {
-            found.expert = tid * kEach + i;
-            found.row = (int)start[i] + (mt - (int)at) * BM;
-            found.end = (int)start[i + 1];
-        }
-        at += c;
+        plan.row[tid * kEach + i] = start[i];
+        plan.tile[tid * kEach + i] = at;
+        at += (start[i + 1] - start[i] + BM - 1) / BM;
+    }
+    if (tid == kProductThreads - 1) {
+        plan.row[kMaxExperts] = start[kEach];
+        plan.tile[kMaxExperts] = at;
     }
     __syncthreads();
-    return Tile{__builtin_amdgcn_readfirstlane(found.expert), __builtin_amdgcn_readfirstlane(found.row),
-                __builtin_amdgcn_readfirstlane(found.end)};
+    return __builtin_amdgcn_readfirstlane(plan.tile[kMaxExperts]);
+}
+
+// Row tile `mt` of the plan (below its number of tiles). All threads call it; it holds a barrier.
+template <int BM>
+__device__ Tile find_tile(Plan &plan, int mt)
+{
+    const int tid = threadIdx.x;
+    for (int e = tid; e < kMaxExperts; e += kProductThreads)
+        if (plan.tile[e] <= (uint32_t)mt && (uint32_t)mt < plan.tile[e + 1]) plan.expert = e;
+    __syncthreads();
+    const int e = __builtin_amdgcn_readfirstlane(plan.expert);
+    return Tile{e, (int)__builtin_amdgcn_readfirstlane(plan.row[e] + (mt - plan.tile[e]) * BM),
+                (int)__builtin_amdgcn_readfirstlane(plan.row[e + 1])};
 }
 
 // One 16 x 16 x 128 step: weights (E2M1) by rows of elements of format XF (0: E4M3, 4: E2M1), the scale bytes in
@@ -386,16 +404,24 @@ __device__ __forceinline__ void store_out(const ProductArgs &a, int row, int col
     }
 }
 
-__device__ __forceinline__ float swiglu(float gate, float up) { return gate / (1.f + expf(-gate)) * up; }
+// silu(gate) * up by the hardware's exponential and reciprocal (an ulp each; the exponent's argument is off by |gate|
+// half steps): far below the 16-bit rounding behind it
+__device__ __forceinline__ float swiglu(float gate, float up)
+{
+    return gate * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(gate * -1.44269504f)) * up;
+}
 
 // Rows of one expert, 16 * FR at a time, against 64 weight rows (32 of the gate's and 32 of the up projection's
 // with GLU). The four wavefronts share out k in supersteps of 512 and add up in LDS, wavefront 0's part first.
 template <class T, int XF, int FR, bool GLU>
 __global__ __launch_bounds__(kProductThreads) void expert_product_kernel(ProductArgs a)
 {
-    const int nt = blockIdx.x % a.ntiles, mt = blockIdx.x / a.ntiles;
-    const Tile tile = find_tile<FR * 16>(a, mt);
-    if (tile.expert < 0) return;
+    __shared__ Plan plan;
+    __shared__ f32x4 part[kProductThreads / kWave][kFrags][kWave];
+    const int total = make_plan<FR * 16>(a, plan) * a.ntiles;
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    const int nt = t % a.ntiles;
+    const Tile tile = find_tile<FR * 16>(plan, t / a.ntiles);
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const int r = lane % 16, g = lane / 16;
     constexpr int kOut = GLU ? kFrags / 2 : kFrags;          // output fragments of 16 columns
@@ -468,7 +494,6 @@ __global__ __launch_bounds__(kProductThreads) void expert_product_kernel(Product
             for (int j = 0; j < kFrags; ++j) acc[f][j] = mma<XF, 0>(wf[j], xf[f], acc[f][j], ws[j], xs[f]);
     }
 
-    __shared__ f32x4 part[kProductThreads / kWave][kFrags][kWave];
 #pragma unroll
     for (int f = 0; f < FR; ++f) {
         if (f) __syncthreads();
@@ -490,137 +515,167 @@ __global__ __launch_bounds__(kProductThreads) void expert_product_kernel(Product
             if (row < tile.end && col < a.fo) store_out<T>(a, row, col, v);
         }
     }
+    __syncthreads();
+    }
 }
 
-// Rows of one expert, 16 * FR at a time, against 256 weight rows: each of the four wavefronts has 64 of its own (32
-// of the gate's and the matching 32 of the up projection's with GLU) and all of k, in steps of 128. Both sides go
-// through LDS: a matrix instruction's lane holds 16 bytes of a row whose neighbours sit in lanes 16 apart, so loading
-// straight into its layout makes the cache look at every lane's 16 bytes by itself (one look-up a clock), where four
-// adjacent lanes that read 64 bytes of a row count as one. LDS keeps 64 (E4M3: 128) bytes of each row; the 16-byte
-// pieces of a row are swapped by its number so that the writers' and the readers' eight lanes a clock meet every bank
-// once. Scale bytes come a superstep (four steps) at a time and are turned into a word per (row, g) there.
-template <class T, int XF, int FR, bool GLU>
-__global__ __launch_bounds__(kProductThreads, 2) void expert_product_wide_kernel(ProductArgs a)
+// Rows of one expert, 16 * FR * WM at a time, against 16 * NF * WN weight rows (half of them the gate's, half the
+// matching ones of the up projection with GLU): WM x WN wavefronts, each with FR x NF fragments of its own and all of k.
+//
+// Both sides go through LDS: a matrix instruction's lane holds 16 bytes of a row whose neighbours sit in lanes 16
+// apart, so loading straight into its layout makes the cache look at every lane's 16 bytes by itself (one look-up a
+// clock), where eight adjacent lanes that read a line of 128 bytes count as one. A stage is 128 bytes of an input
+// row, kSub instruction steps: 256 elements of E2M1, 128 of E4M3. The 16-byte pieces of a row are swapped by its number
+// so that the eight lanes that LDS serves in a clock meet every bank once, writing and reading.
+//
+// A stage's pieces are fetched into registers two stages ahead and written to the idle half of LDS one ahead, a few
+// between each fragment's matrix instructions, so that those never run dry. Input fragments are read two ahead. The
+// barrier comes when the current half has been read, two fragments before a stage's end; the next stage's first
+// fragments are read behind it while those two multiply. Scale bytes come 512 elements (four steps) at a time and
+// become a word per (row, g) on the way.
+template <class T, int XF, int FR, int NF, int WM, bool GLU>
+__global__ __launch_bounds__(kProductThreads, FR *NF <= 16 ? 2 : 1) void expert_product_wide_kernel(ProductArgs a)
 {
-    const int nt = blockIdx.x % a.ntiles, mt = blockIdx.x / a.ntiles;
-    const Tile tile = find_tile<FR * 16>(a, mt);
-    if (tile.expert < 0) return;
-    constexpr int kWaves = kProductThreads / kWave, kRowsW = kWaves * kFrags * 16, kRowsX = FR * 16;
-    constexpr int kPx = XF == 4 ? 4 : 8;                      // 16-byte pieces of an input row in a step
-    constexpr int kLoadsW = kRowsW * 4 / kProductThreads, kLoadsX = kRowsX * kPx / kProductThreads;
-    static_assert(kRowsW == kProductThreads && kRowsX <= kProductThreads, "one scale row a thread");
+    constexpr int kWaves = kProductThreads / kWave, WN = kWaves / WM, kRowsW = WN * NF * 16, kRowsX = WM * FR * 16;
+    constexpr int kSub = XF == 4 ? 2 : 1, kStages = 4 / kSub;  // steps of a stage, stages of 512 elements
+    constexpr int kPw = 4 * kSub, kPx = 8;                    // 16-byte pieces of a row in a stage
+    constexpr int kLoadsW = kRowsW * kPw / kProductThreads, kLoadsX = kRowsX * kPx / kProductThreads;
+    constexpr int kLoads = kLoadsW + kLoadsX;
+    constexpr int kScalesW = kRowsW / kProductThreads;        // scale rows of the weights that a thread carries
+    static_assert(kRowsW % kProductThreads == 0 && kRowsX <= kProductThreads, "whole scale rows a thread");
     static_assert(kRowsX * kPx % kProductThreads == 0, "every thread carries as many pieces");
-    __shared__ u32x4 wl[2][kRowsW * 4], xl[2][kRowsX * kPx], wsl[2][kRowsW], xsl[2][kRowsX];
+    __shared__ Plan plan;
+    __shared__ u32x4 wl[2][kRowsW * kPw], xl[2][kRowsX * kPx], wsl[2][kRowsW], xsl[2][kRowsX];
 
+    const int total = make_plan<kRowsX>(a, plan) * a.ntiles;
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    const int nt = t % a.ntiles;
+    const Tile tile = find_tile<kRowsX>(plan, t / a.ntiles);
     const int tid = threadIdx.x, lane = tid % kWave;
-    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave), wm = wave / WN, wn = wave % WN;
     const int r = lane % 16, g = lane / 16;
-    constexpr int kOut = GLU ? kFrags / 2 : kFrags;
-    const int half = a.n / 2, tile0 = nt * kWaves * kOut * 16;
+    constexpr int kOut = GLU ? NF / 2 : NF, kOwn = NF * 16;   // output fragments and weight rows of a wavefront
+    const int half = a.n / 2, tile0 = nt * WN * kOut * 16;
     const uint32_t wrow = a.k / 2, xrow = XF == 4 ? a.k / 2 : a.k;
     const uint8_t *wb = a.w + (size_t)tile.expert * a.n * wrow, *wsb = a.ws + (size_t)tile.expert * a.n * a.nb;
     const uint8_t *xb = a.x + (size_t)tile.row * xrow, *xsb = a.xs + (size_t)tile.row * a.nb;
     const int last = tile.end - 1 - tile.row;                 // rows past the expert's last read the last one
     // weight row of a place in the tile; columns past the last one read the last one's, and are not stored
     auto weight_row = [&](int q) -> uint32_t {
-        const int c = GLU ? q / 64 * 32 + q % 32 : q;
-        return (GLU && q % 64 >= 32 ? half : 0) + min(tile0 + c, a.fo - 1);
+        const int c = GLU ? q / kOwn * (kOwn / 2) + q % (kOwn / 2) : q;
+        return (GLU && q % kOwn >= kOwn / 2 ? half : 0) + min(tile0 + c, a.fo - 1);
     };
-    // this thread's pieces: where in a row's step, and the place in LDS
+    // piece p of row q in LDS, for rows of 4 and of 8 pieces
+    auto place4 = [](int q, int p) { return q * 4 + (p ^ ((q >> 1) & 3)); };
+    auto place8 = [](int q, int p) { return q * 8 + (p ^ (q & 7)); };
+    // this thread's pieces: where in a row's stage, and the place in LDS (piece i: kProductThreads * i further)
     uint32_t wo[kLoadsW], xo[kLoadsX];
-    int wat[kLoadsW], xat[kLoadsX];
 #pragma unroll
-    for (int i = 0; i < kLoadsW; ++i) {
-        const int c = tid + i * kProductThreads, q = c / 4, p = c % 4;
-        wo[i] = weight_row(q) * wrow + 16 * p;
-        wat[i] = q * 4 + (p ^ ((q >> 1) & 3));
-    }
+    for (int i = 0; i < kLoadsW; ++i) wo[i] = weight_row((tid + i * kProductThreads) / kPw) * wrow + 16 * (tid % kPw);
 #pragma unroll
-    for (int i = 0; i < kLoadsX; ++i) {
-        const int c = tid + i * kProductThreads, q = c / kPx, p = c % kPx;
-        xo[i] = (uint32_t)min(q, last) * xrow + 16 * p;
-        xat[i] = q * kPx + (XF == 4 ? p ^ ((q >> 1) & 3) : p ^ (q & 7));
-    }
-    const uint32_t wso = weight_row(tid) * a.nb, xso = (uint32_t)min(tid % kRowsX, last) * a.nb;
+    for (int i = 0; i < kLoadsX; ++i) xo[i] = (uint32_t)min((tid + i * kProductThreads) / kPx, last) * xrow + 16 * (tid % kPx);
+    const int wat = kSub == 2 ? place8(tid / 8, tid % 8) : place4(tid / 4, tid % 4), xat = place8(tid / 8, tid % 8);
+    uint32_t wso[kScalesW];
+#pragma unroll
+    for (int i = 0; i < kScalesW; ++i) wso[i] = weight_row(tid + i * kProductThreads) * a.nb;
+    const uint32_t xso = (uint32_t)min(tid % kRowsX, last) * a.nb;
     // a reader's pieces: of fragment 0, the others lie 16 rows apart
-    const int wfrag = (wave * 64 + r) * 4 + (g ^ ((r >> 1) & 3));
-    const int xfrag = XF == 4 ? r * 4 + (g ^ ((r >> 1) & 3)) : r * 8 + (g ^ (r & 7));
-    const int xfrag2 = XF == 4 ? xfrag : r * 8 + ((4 + g) ^ (r & 7));
+    const int lo = place8(r, g), hi = place8(r, 4 + g);
+    const int wfrag[2] = {wn * kOwn * kPw + (kSub == 2 ? lo : place4(r, g)), wn * kOwn * kPw + hi};
+    const int xfrag[2] = {wm * FR * 16 * kPx + lo, wm * FR * 16 * kPx + hi};
 
-    f32x4 acc[FR][kFrags];
+    f32x4 acc[FR][NF];
 #pragma unroll
     for (int f = 0; f < FR; ++f)
 #pragma unroll
-        for (int j = 0; j < kFrags; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < NF; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const int supers = a.k / kSuper, steps = supers * 4;
-    u32x4 wr[kLoadsW], xr[kLoadsX], wsr, xsr;
-    // Loads of whole steps and supersteps. Beyond the last one the last one is read again, and not used: a branch
-    // here would make the compiler wait for the load at its end.
-    auto load = [&](int step) {
-        const uint32_t at = min(step, steps - 1);
-#pragma unroll
-        for (int i = 0; i < kLoadsW; ++i) wr[i] = *reinterpret_cast<const u32x4_a8 *>(wb + (wo[i] + at * (kStep / 2)));
-#pragma unroll
-        for (int i = 0; i < kLoadsX; ++i)
-            xr[i] = *reinterpret_cast<const u32x4_a8 *>(xb + (xo[i] + at * (XF == 4 ? kStep / 2 : kStep)));
+    const int supers = a.k / kSuper, stages = supers * kStages;
+    u32x4 piece[kLoads], wsr[kScalesW], xsr;
+    // Loads of whole stages. Beyond the last one the last one is read again, and not used: a branch here would make
+    // the compiler wait for the load at its end.
+    auto load = [&](int i, int stage) {
+        const uint32_t at = min(stage, stages - 1);
+        if (i < kLoadsW) piece[i] = *reinterpret_cast<const u32x4_a8 *>(wb + (wo[i] + at * (16 * kPw)));
+        else piece[i] = *reinterpret_cast<const u32x4_a8 *>(xb + (xo[i - kLoadsW] + at * (16 * kPx)));
     };
-    auto keep = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < kLoadsW; ++i) wl[buf][wat[i]] = wr[i];
-#pragma unroll
-        for (int i = 0; i < kLoadsX; ++i) xl[buf][xat[i]] = xr[i];
+    auto keep = [&](int i, int buf) {
+        if (i < kLoadsW) wl[buf][wat + i * kProductThreads] = piece[i];
+        else xl[buf][xat + (i - kLoadsW) * kProductThreads] = piece[i];
     };
     auto load_scales = [&](int super) {
         const uint32_t at = min(super, supers - 1) * 16;
-        wsr = *reinterpret_cast<const u32x4_a1 *>(wsb + (wso + at));
+#pragma unroll
+        for (int i = 0; i < kScalesW; ++i) wsr[i] = *reinterpret_cast<const u32x4_a1 *>(wsb + (wso[i] + at));
         xsr = *reinterpret_cast<const u32x4_a1 *>(xsb + (xso + at));
     };
     auto keep_scales = [&](int buf) {
-        wsl[buf][tid] = by_group(wsr);
+#pragma unroll
+        for (int i = 0; i < kScalesW; ++i) wsl[buf][tid + i * kProductThreads] = by_group(wsr[i]);
         xsl[buf][tid % kRowsX] = by_group(xsr);          // threads of the same row write the same bytes
     };
-    const uint32_t *wsw = reinterpret_cast<const uint32_t *>(wsl) + (wave * 64 + r) * 4 + g;
-    const uint32_t *xsw = reinterpret_cast<const uint32_t *>(xsl) + r * 4 + g;
-
+    const uint32_t *wsw = reinterpret_cast<const uint32_t *>(wsl) + (wn * kOwn + r) * 4 + g;
+    const uint32_t *xsw = reinterpret_cast<const uint32_t *>(xsl) + (wm * FR * 16 + r) * 4 + g;
+    i32x8 wf[2][NF], xf[FR];
+    uint32_t ws[NF], xs[FR];
+    // fragments of step i of 512 elements
+    auto read_w = [&](int i) {
+        const u32x4 *l = wl[i / kSub & 1] + wfrag[i % kSub];
+#pragma unroll
+        for (int j = 0; j < NF; ++j) wf[i & 1][j] = join(l[j * 16 * kPw], l[j * 16 * kPw]);
+    };
+    auto read_x = [&](int i, int f) {
+        const u32x4 *l = xl[i / kSub & 1] + f * 16 * kPx;
+        xf[f] = XF == 4 ? join(l[xfrag[i % kSub]], l[xfrag[i % kSub]]) : join(l[xfrag[0]], l[xfrag[1]]);
+    };
+    auto read_scales = [&](int buf) {
+#pragma unroll
+        for (int j = 0; j < NF; ++j) ws[j] = wsw[buf * kRowsW * 4 + j * 64];
+#pragma unroll
+        for (int f = 0; f < FR; ++f) xs[f] = xsw[buf * kRowsX * 4 + f * 64];
+    };
     if (supers > 0) {
         load_scales(0);
-        load(0);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) load(i, 0);
         keep_scales(0);
-        keep(0);
-        load(1);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) keep(i, 0);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) load(i, 1);
         __syncthreads();
+        read_w(0);
+        read_x(0, 0);
+        read_x(0, 1);
+        read_scales(0);
     }
     for (int super = 0; super < supers; ++super) {
-        uint32_t ws[kFrags], xs[FR];
-#pragma unroll
-        for (int j = 0; j < kFrags; ++j) ws[j] = wsw[(super & 1) * kRowsW * 4 + j * 64];
-#pragma unroll
-        for (int f = 0; f < FR; ++f) xs[f] = xsw[(super & 1) * kRowsX * 4 + f * 64];
-        // One step: what was fetched for the next one goes into the other half of LDS, the one after is fetched
-        // meanwhile, and this one multiplies
 #define MOE_WIDE_STEP(I)                                                                              \
         {                                                                                             \
-            keep((I + 1) & 1);                                                                        \
-            if (I == 3) keep_scales((super + 1) & 1);                                                 \
-            load(super * 4 + I + 2);                                                                  \
+            constexpr int kStage = I / kSub, kGroups = (FR - 2) * kSub;                               \
             if (I == 1) load_scales(super + 1);                                                       \
-            __builtin_amdgcn_sched_barrier(0);                                                        \
-            i32x8 wf[kFrags];                                                                         \
-            _Pragma("unroll") for (int j = 0; j < kFrags; ++j)                                        \
-                wf[j] = join(wl[I & 1][wfrag + j * 64], wl[I & 1][wfrag + j * 64]);                   \
-            _Pragma("unroll") for (int f = 0; f < FR; ++f) {                                          \
-                const i32x8 xf = join(xl[I & 1][xfrag + f * 16 * kPx], xl[I & 1][xfrag2 + f * 16 * kPx]); \
-                _Pragma("unroll") for (int j = 0; j < kFrags; ++j)                                    \
-                    acc[f][j] = mma<XF, I>(wf[j], xf, acc[f][j], ws[j], xs[f]);                       \
+            if (I == 3) keep_scales((super + 1) & 1);                                                 \
+            _Pragma("unroll") for (int f = 0; f < FR - 2; ++f) {                                      \
+                const int group = I % kSub * (FR - 2) + f;                                            \
+                read_x(I, f + 2);                                                                     \
+                _Pragma("unroll") for (int i = group * kLoads / kGroups; i < (group + 1) * kLoads / kGroups; ++i) { \
+                    keep(i, (kStage + 1) & 1);                                                        \
+                    load(i, super * kStages + kStage + 2);                                            \
+                }                                                                                     \
+                _Pragma("unroll") for (int j = 0; j < NF; ++j)                                        \
+                    acc[f][j] = mma<XF, I>(wf[I & 1][j], xf[f], acc[f][j], ws[j], xs[f]);             \
+                __builtin_amdgcn_sched_barrier(0);                                                    \
             }                                                                                         \
-            __builtin_amdgcn_sched_group_barrier(0x100, kFrags + 2 * kPx / 4, 0);                     \
-            _Pragma("unroll") for (int f = 0; f < FR; ++f) {                                          \
-                __builtin_amdgcn_sched_group_barrier(0x008, kFrags, 0);                               \
-                __builtin_amdgcn_sched_group_barrier(0x100, kPx / 4, 0);                              \
-            }                                                                                         \
+            if (I % kSub == kSub - 1) __syncthreads();                                                \
             __builtin_amdgcn_sched_barrier(0);                                                        \
-            __syncthreads();                                                                          \
+            read_w((I + 1) & 3);                                                                      \
+            read_x((I + 1) & 3, 0);                                                                   \
+            read_x((I + 1) & 3, 1);                                                                   \
+            __builtin_amdgcn_sched_barrier(0);                                                        \
+            _Pragma("unroll") for (int f = FR - 2; f < FR; ++f)                                       \
+                _Pragma("unroll") for (int j = 0; j < NF; ++j)                                        \
+                    acc[f][j] = mma<XF, I>(wf[I & 1][j], xf[f], acc[f][j], ws[j], xs[f]);             \
+            if (I == 3) read_scales((super + 1) & 1);                                                 \
             __builtin_amdgcn_sched_barrier(0);                                                        \
         }
         MOE_WIDE_STEP(0)
@@ -629,38 +684,42 @@ __global__ __launch_bounds__(kProductThreads, 2) void expert_product_wide_kernel
         MOE_WIDE_STEP(3)
 #undef MOE_WIDE_STEP
     }
-    // the last k % 512 elements, a step at a time (every wavefront is past its last read of LDS here)
+    // the last k % 512 elements, a step at a time
     for (int at = supers * kSuper; at < a.k; at += kStep) {
-#pragma unroll
-        for (int i = 0; i < kLoadsW; ++i)
-            wl[0][wat[i]] = load_piece_or_zero<4>(wb + wo[i], at, (tid + i * kProductThreads) % 4, a.k);
-#pragma unroll
-        for (int i = 0; i < kLoadsX; ++i)
-            xl[0][xat[i]] = load_piece_or_zero<XF>(xb + xo[i], at, (tid + i * kProductThreads) % kPx, a.k);
-        const int b = at / kBlock;
-        u32x4 ws4, xs4;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            ws4[i] = b + i < a.nb ? wsb[wso + b + i] : 127;
-            xs4[i] = b + i < a.nb ? xsb[xso + b + i] : 127;
-        }
-        wsl[0][tid] = ws4;
-        xsl[0][tid % kRowsX] = xs4;
         __syncthreads();
-        i32x8 wf[kFrags];
+        constexpr int kTx = XF == 4 ? 4 : 8;                  // pieces of an input row in one step
+#pragma unroll 1
+        for (int c = tid; c < kRowsW * 4; c += kProductThreads)
+            wl[0][kSub == 2 ? place8(c / 4, c % 4) : place4(c / 4, c % 4)] =
+                load_piece_or_zero<4>(wb + weight_row(c / 4) * wrow + 16 * (c % 4), at, c % 4, a.k);
+#pragma unroll 1
+        for (int c = tid; c < kRowsX * kTx; c += kProductThreads)
+            xl[0][place8(c / kTx, c % kTx)] =
+                load_piece_or_zero<XF>(xb + (uint32_t)min(c / kTx, last) * xrow + 16 * (c % kTx), at, c % kTx, a.k);
+        const int b = at / kBlock;
+        u32x4 v;
 #pragma unroll
-        for (int j = 0; j < kFrags; ++j) wf[j] = join(wl[0][wfrag + j * 64], wl[0][wfrag + j * 64]);
+        for (int j = 0; j < kScalesW; ++j) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = b + i < a.nb ? wsb[wso[j] + b + i] : 127;
+            wsl[0][tid + j * kProductThreads] = v;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = b + i < a.nb ? xsb[xso + b + i] : 127;
+        xsl[0][tid % kRowsX] = v;
+        __syncthreads();
+        read_w(0);
+        read_scales(0);
 #pragma unroll
         for (int f = 0; f < FR; ++f) {
-            const i32x8 xf = join(xl[0][xfrag + f * 16 * kPx], xl[0][xfrag2 + f * 16 * kPx]);
+            read_x(0, f);
 #pragma unroll
-            for (int j = 0; j < kFrags; ++j) acc[f][j] = mma<XF, 0>(wf[j], xf, acc[f][j], wsw[j * 64], xsw[f * 64]);
+            for (int j = 0; j < NF; ++j) acc[f][j] = mma<XF, 0>(wf[0][j], xf[f], acc[f][j], ws[j], xs[f]);
         }
-        __syncthreads();
     }
 #pragma unroll
     for (int f = 0; f < FR; ++f) {
-        const int row = tile.row + f * 16 + r;
+        const int row = tile.row + (wm * FR + f) * 16 + r;
         if (row >= tile.end) continue;
 #pragma unroll
         for (int j = 0; j < kOut; ++j) {
@@ -669,9 +728,11 @@ __global__ __launch_bounds__(kProductThreads, 2) void expert_product_wide_kernel
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = swiglu(v[i], acc[f][j + kOut][i]);
             }
-            const int col = tile0 + (wave * kOut + j) * 16 + 4 * g;
+            const int col = tile0 + (wn * kOut + j) * 16 + 4 * g;
             if (col < a.fo) store_out<T>(a, row, col, v);
         }
+    }
+    __syncthreads();
     }
 }
 
@@ -783,12 +844,12 @@ int moe_expert_product(const void *x, const uint8_t *x_scales, int element, cons
     // offsets inside one expert's weights, and inside the rows of one tile, are 32-bit
     if ((long long)n * k > 4ll << 30 || k > 1 << 24) return MOE_ERR_SHAPE;
     const int each = rows / a.E;                // rows of an expert, were they even
-    const int frags = each <= 8 ? 1 : (each <= 40 ? 4 : 8);
-    const bool wide = frags > 1;
-    const int cols = (glu ? kFrags / 2 : kFrags) * 16 * (wide ? kProductThreads / kWave : 1);
+    // rows and columns of a tile
+    const int tall = each <= 8 ? 16 : (each <= 40 ? 64 : (each <= 150 ? 128 : 192));
+    const int cols = (tall == 16 ? kFrags * 16 : 256) / (glu ? 2 : 1);
     a.ntiles = (a.fo + cols - 1) / cols;
     // a tile starts at every expert's first row, so at most this many
-    const long long mtiles = rows / (frags * 16) + std::min(a.E, rows);
+    const long long mtiles = rows / tall + std::min(a.E, rows);
     if (mtiles * a.ntiles > INT_MAX) return MOE_ERR_SHAPE;
     if (rows == 0) return MOE_OK;
     if (!x || !x_scales || !weights || !weight_scales || !ep_recv_count || !out) return MOE_ERR_NULLPTR;
@@ -800,14 +861,15 @@ int moe_expert_product(const void *x, const uint8_t *x_scales, int element, cons
     a.ws = weight_scales;
     a.erc = ep_recv_count;
     a.out = out;
-    const dim3 g((unsigned)(mtiles * a.ntiles)), b(kProductThreads);
+    const dim3 g((unsigned)std::min<long long>(mtiles * a.ntiles, kWorkgroups)), b(kProductThreads);
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
 #define MOE_PRODUCT_G(T, XF, G)                                                                       \
     do {                                                                                              \
-        if (frags == 1) hipLaunchKernelGGL((expert_product_kernel<T, XF, 1, G>), g, b, 0, st, a);     \
-        else if (frags == 4) hipLaunchKernelGGL((expert_product_wide_kernel<T, XF, 4, G>), g, b, 0, st, a); \
-        else hipLaunchKernelGGL((expert_product_wide_kernel<T, XF, 8, G>), g, b, 0, st, a);           \
+        if (tall == 16) hipLaunchKernelGGL((expert_product_kernel<T, XF, 1, G>), g, b, 0, st, a);     \
+        else if (tall == 64) hipLaunchKernelGGL((expert_product_wide_kernel<T, XF, 4, 4, 1, G>), g, b, 0, st, a); \
+        else if (tall == 128) hipLaunchKernelGGL((expert_product_wide_kernel<T, XF, 4, 8, 2, G>), g, b, 0, st, a); \
+        else hipLaunchKernelGGL((expert_product_wide_kernel<T, XF, 6, 8, 2, G>), g, b, 0, st, a);     \
     } while (0)
 #define MOE_PRODUCT(T, XF)                                                                            \
     do {                                                                                              \
