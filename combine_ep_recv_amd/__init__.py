@@ -455,29 +455,38 @@ def _launch(name: str, device, *args):
     else:
         with torch.cuda.device(device):
             rc = f(*args)
-    _check(name, rc)
+    if rc != MOE_OK:
+        _check(name, rc)
+
+
+_FLOAT_CODES = {torch.float32: MOE_FP32, torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16}
 
 
 def _float_code(name, dt: torch.dtype) -> int:
     """moe_dtype of a floating tensor."""
-    if dt == torch.float32:
-        return MOE_FP32
-    if dt == torch.bfloat16:
-        return MOE_BF16
-    if dt == torch.float16:
-        return MOE_FP16
-    raise MoeError(name, MOE_ERR_DTYPE, "unsupported dtype %s" % dt)
+    code = _FLOAT_CODES.get(dt)
+    if code is None:
+        raise MoeError(name, MOE_ERR_DTYPE, "unsupported dtype %s" % dt)
+    return code
 
 
-def _gate_shape(fn, logits, ids):
-    """(tokens, experts, topk, device) of a gate call."""
+def _address(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _new(shape, dtype, device):
+    """torch.empty of one or two dimensions, at two thirds of its cost."""
+    return torch.empty_strided(shape, shape[1:] + (1,), dtype=dtype, device=device)
+
+
+def _logits(fn, logits):
+    """(device, tokens, experts, dtype code) of a gate's logits, checked."""
     dev = _gpu_device("logits", logits)
-    if logits.dim() != 2 or not isinstance(ids, torch.Tensor) or ids.dim() != 2:
-        raise MoeError(fn, MOE_ERR_SHAPE, "logits and expert_ids must be 2-D")
-    N, E = logits.shape
-    _check_tensor("logits", logits, logits.dtype, (N, E), dev)
-    _check_tensor("expert_ids", ids, torch.int32, (N, ids.shape[1]), dev)
-    return N, E, ids.shape[1], dev
+    if logits.dim() != 2:
+        raise MoeError(fn, MOE_ERR_SHAPE, "logits must be 2-D")
+    dt = _float_code(fn, logits.dtype)
+    _check_tensor("logits", logits, logits.dtype, logits.shape, dev)
+    return (dev, *logits.shape, dt)
 
 
 def _byte_mask(name, mask, shape, device):
@@ -485,7 +494,19 @@ def _byte_mask(name, mask, shape, device):
             or mask.device != device or not mask.is_contiguous()):
         raise MoeError(name, MOE_ERR_MASK, "%s must be a contiguous bool or uint8 tensor of shape %s on %s"
                        % (name, tuple(shape), device))
-    return _ptr(mask)
+
+
+def _gate(head, ids, w, logits, topk, score, bias, groups, topk_groups, group_score, renormalize, scale, token_mask,
+          pair_mask):
+    """moe_gate on outputs that have been checked (or made); head: _logits' result."""
+    dev, N, E, dt = head
+    if bias is not None:
+        _check_tensor("bias", bias, torch.float32, (E,), dev)
+    if token_mask is not None:
+        _byte_mask("token_mask", token_mask, (N,), dev)
+    _launch("moe_gate", dev, logits.data_ptr(), _address(bias), _address(token_mask), N, E, topk, dt, int(score),
+            int(groups), int(topk_groups), int(group_score), 1 if renormalize else 0, float(scale), ids.data_ptr(),
+            w.data_ptr(), _address(pair_mask), _stream_ptr(dev))
 
 
 def gate_into(expert_ids: torch.Tensor, expert_scales: torch.Tensor, logits: torch.Tensor,
@@ -494,16 +515,16 @@ def gate_into(expert_ids: torch.Tensor, expert_scales: torch.Tensor, logits: tor
               token_mask: Optional[torch.Tensor] = None, pair_mask: Optional[torch.Tensor] = None):
     """moe_gate into preallocated expert_ids [N, topk] int32, expert_scales [N, topk] fp32 and, when given,
     pair_mask [N, topk] bool or uint8, on the current stream. See gate for the rest."""
-    N, E, K, dev = _gate_shape("moe_gate", logits, expert_ids)
-    dt = _float_code("moe_gate", logits.dtype)
+    head = _logits("moe_gate", logits)
+    if not isinstance(expert_ids, torch.Tensor) or expert_ids.dim() != 2:
+        raise MoeError("moe_gate", MOE_ERR_SHAPE, "expert_ids must be 2-D")
+    dev, N, K = head[0], head[1], expert_ids.shape[1]
+    _check_tensor("expert_ids", expert_ids, torch.int32, (N, K), dev)
     _check_tensor("expert_scales", expert_scales, torch.float32, (N, K), dev)
-    if bias is not None:
-        _check_tensor("bias", bias, torch.float32, (E,), dev)
-    mp = None if token_mask is None else _byte_mask("token_mask", token_mask, (N,), dev)
-    pp = None if pair_mask is None else _byte_mask("pair_mask", pair_mask, (N, K), dev)
-    _launch("moe_gate", dev, _ptr(logits), _ptr(bias), mp, N, E, K, dt, int(score), int(groups), int(topk_groups),
-            int(group_score), int(bool(renormalize)), float(scale), _ptr(expert_ids), _ptr(expert_scales), pp,
-            _stream_ptr(dev))
+    if pair_mask is not None:
+        _byte_mask("pair_mask", pair_mask, (N, K), dev)
+    _gate(head, expert_ids, expert_scales, logits, K, score, bias, groups, topk_groups, group_score, renormalize,
+          scale, token_mask, pair_mask)
     return expert_ids, expert_scales
 
 
@@ -522,15 +543,29 @@ def gate(logits: torch.Tensor, topk: int, score: int = MOE_SCORE_SOFTMAX, bias: 
     take the mask as x_active_mask. The outputs carry no autograd graph: gate_backward gives the
     gradient of the logits.
     """
-    dev = _gpu_device("logits", logits)
-    if logits.dim() != 2 or topk < 1:
-        raise MoeError("moe_gate", MOE_ERR_SHAPE, "logits must be 2-D and topk at least 1")
-    N = logits.shape[0]
-    ids = torch.empty((N, topk), dtype=torch.int32, device=dev)
-    w = torch.empty((N, topk), dtype=torch.float32, device=dev)
-    on = torch.empty((N, topk), dtype=torch.bool, device=dev) if with_pair_mask else None
-    gate_into(ids, w, logits, score, bias, groups, topk_groups, group_score, renormalize, scale, token_mask, on)
+    head = _logits("moe_gate", logits)
+    topk = int(topk)
+    if topk < 1:
+        raise MoeError("moe_gate", MOE_ERR_SHAPE, "topk must be at least 1")
+    dev, shape = head[0], (head[1], topk)
+    ids, w = _new(shape, torch.int32, dev), _new(shape, torch.float32, dev)
+    on = _new(shape, torch.bool, dev) if with_pair_mask else None
+    _gate(head, ids, w, logits, topk, score, bias, groups, topk_groups, group_score, renormalize, scale, token_mask,
+          on)
     return (ids, w, on) if with_pair_mask else (ids, w)
+
+
+def _gate_backward(head, out, logits, ids, w, grad, score, renormalize, scale):
+    dev, N, E, dt = head
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise MoeError("moe_gate_backward", MOE_ERR_SHAPE, "expert_ids must be 2-D")
+    K = ids.shape[1]
+    _check_tensor("expert_ids", ids, torch.int32, (N, K), dev)
+    _check_tensor("expert_scales", w, torch.float32, (N, K), dev)
+    _check_tensor("grad_scales", grad, torch.float32, (N, K), dev)
+    _launch("moe_gate_backward", dev, logits.data_ptr(), ids.data_ptr(), w.data_ptr(), grad.data_ptr(), N, E, K, dt,
+            int(score), 1 if renormalize else 0, float(scale), out.data_ptr(), _stream_ptr(dev))
+    return out
 
 
 def gate_backward_into(grad_logits: torch.Tensor, logits: torch.Tensor, expert_ids: torch.Tensor,
@@ -538,14 +573,9 @@ def gate_backward_into(grad_logits: torch.Tensor, logits: torch.Tensor, expert_i
                        renormalize: bool = True, scale: float = 1.0):
     """moe_gate_backward into a preallocated grad_logits (logits' shape and dtype; every element is
     written) on the current stream."""
-    N, E, K, dev = _gate_shape("moe_gate_backward", logits, expert_ids)
-    dt = _float_code("moe_gate_backward", logits.dtype)
-    _check_tensor("expert_scales", expert_scales, torch.float32, (N, K), dev)
-    _check_tensor("grad_scales", grad_scales, torch.float32, (N, K), dev)
-    _check_tensor("grad_logits", grad_logits, logits.dtype, (N, E), dev)
-    _launch("moe_gate_backward", dev, _ptr(logits), _ptr(expert_ids), _ptr(expert_scales), _ptr(grad_scales), N, E,
-            K, dt, int(score), int(bool(renormalize)), float(scale), _ptr(grad_logits), _stream_ptr(dev))
-    return grad_logits
+    head = _logits("moe_gate_backward", logits)
+    _check_tensor("grad_logits", grad_logits, logits.dtype, logits.shape, head[0])
+    return _gate_backward(head, grad_logits, logits, expert_ids, expert_scales, grad_scales, score, renormalize, scale)
 
 
 def gate_backward(logits: torch.Tensor, expert_ids: torch.Tensor, expert_scales: torch.Tensor,
@@ -554,9 +584,9 @@ def gate_backward(logits: torch.Tensor, expert_ids: torch.Tensor, expert_scales:
     """Gradient of gate's logits from grad_scales, the gradient of its expert_scales: [N, E] in the
     logits' dtype. expert_ids and expert_scales are gate's outputs for the same score, renormalize and
     scale; pairs with id -1 give and get nothing."""
-    _gpu_device("logits", logits)
-    return gate_backward_into(torch.empty_like(logits, memory_format=torch.contiguous_format), logits, expert_ids,
-                              expert_scales, grad_scales, score, renormalize, scale)
+    head = _logits("moe_gate_backward", logits)
+    return _gate_backward(head, _new((head[1], head[2]), logits.dtype, head[0]), logits, expert_ids, expert_scales,
+                          grad_scales, score, renormalize, scale)
 
 
 # ---- microscaled rows and the experts' product ----
@@ -589,6 +619,14 @@ def _flat(shape):
     return n
 
 
+def _quantize(codes, scales, x, rows, cols, element):
+    """moe_mx_quantize of checked tensors."""
+    dev = x.device
+    _launch("moe_mx_quantize", dev, x.data_ptr(), rows, cols, _float_code("moe_mx_quantize", x.dtype), element,
+            codes.data_ptr(), scales.data_ptr(), _stream_ptr(dev))
+    return codes, scales
+
+
 def quantize_mx_into(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor):
     """moe_mx_quantize of x [..., cols] into preallocated codes (float8_e4m3fn [..., cols], or uint8
     [..., cols / 2] for packed E2M1) and scales (uint8 [..., ceil(cols / 32)]), on the current stream."""
@@ -597,13 +635,11 @@ def quantize_mx_into(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor)
     if x.dim() < 1 or codes.dim() < 1:
         raise MoeError("moe_mx_quantize", MOE_ERR_SHAPE, "x must have at least one dimension")
     element, shape = _mx_rows("codes", codes)
-    dt = _float_code("moe_mx_quantize", x.dtype)
+    _float_code("moe_mx_quantize", x.dtype)
     _check_tensor("x", x, x.dtype, shape, dev)
     _check_tensor("codes", codes, codes.dtype, codes.shape, dev)
     _check_tensor("scales", scales, torch.uint8, shape[:-1] + (-(-shape[-1] // MX_BLOCK),), dev)
-    _launch("moe_mx_quantize", dev, _ptr(x), _flat(shape[:-1]), shape[-1], dt, element, _ptr(codes), _ptr(scales),
-            _stream_ptr(dev))
-    return codes, scales
+    return _quantize(codes, scales, x, _flat(shape[:-1]), shape[-1], element)
 
 
 def quantize_mx(x: torch.Tensor, element: int = MOE_MX_E2M1):
@@ -615,26 +651,35 @@ def quantize_mx(x: torch.Tensor, element: int = MOE_MX_E2M1):
     dt, per = _mx_codes(element)
     if x.dim() < 1 or x.shape[-1] < 1 or x.shape[-1] % 16:
         raise MoeError("moe_mx_quantize", MOE_ERR_SHAPE, "the last dimension must be a multiple of 16")
-    lead, cols = tuple(x.shape[:-1]), x.shape[-1]
+    _float_code("moe_mx_quantize", x.dtype)
+    _check_tensor("x", x, x.dtype, x.shape, dev)
+    shape = tuple(x.shape)
+    lead, cols = shape[:-1], shape[-1]
     codes = torch.empty(lead + (cols // per,), dtype=dt, device=dev)
     scales = torch.empty(lead + (-(-cols // MX_BLOCK),), dtype=torch.uint8, device=dev)
-    return quantize_mx_into(codes, scales, x)
+    return _quantize(codes, scales, x, _flat(lead), cols, element)
+
+
+def _dequantize(out, codes, scales, shape, element):
+    """moe_mx_dequantize of a checked out."""
+    dev = out.device
+    _check_tensor("codes", codes, codes.dtype, codes.shape, dev)
+    _check_tensor("scales", scales, torch.uint8, shape[:-1] + (-(-shape[-1] // MX_BLOCK),), dev)
+    _launch("moe_mx_dequantize", dev, codes.data_ptr(), scales.data_ptr(), _flat(shape[:-1]), shape[-1],
+            _float_code("moe_mx_dequantize", out.dtype), element, out.data_ptr(), _stream_ptr(dev))
+    return out
 
 
 def dequantize_mx_into(out: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
     """moe_mx_dequantize into a preallocated out [..., cols] (fp16, bf16 or fp32) on the current stream."""
-    dev = _gpu_device("codes", codes)
-    _gpu_device("out", out)
+    _gpu_device("codes", codes)
+    dev = _gpu_device("out", out)
     if codes.dim() < 1:
         raise MoeError("moe_mx_dequantize", MOE_ERR_SHAPE, "codes must have at least one dimension")
     element, shape = _mx_rows("codes", codes)
-    dt = _float_code("moe_mx_dequantize", out.dtype)
-    _check_tensor("codes", codes, codes.dtype, codes.shape, dev)
-    _check_tensor("scales", scales, torch.uint8, shape[:-1] + (-(-shape[-1] // MX_BLOCK),), dev)
+    _float_code("moe_mx_dequantize", out.dtype)
     _check_tensor("out", out, out.dtype, shape, dev)
-    _launch("moe_mx_dequantize", dev, _ptr(codes), _ptr(scales), _flat(shape[:-1]), shape[-1], dt, element,
-            _ptr(out), _stream_ptr(dev))
-    return out
+    return _dequantize(out, codes, scales, shape, element)
 
 
 def dequantize_mx(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
@@ -643,7 +688,8 @@ def dequantize_mx(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype 
     if codes.dim() < 1:
         raise MoeError("moe_mx_dequantize", MOE_ERR_SHAPE, "codes must have at least one dimension")
     _float_code("moe_mx_dequantize", dtype)
-    return dequantize_mx_into(torch.empty(_mx_rows("codes", codes)[1], dtype=dtype, device=dev), codes, scales)
+    element, shape = _mx_rows("codes", codes)
+    return _dequantize(torch.empty(shape, dtype=dtype, device=dev), codes, scales, shape, element)
 
 
 def expert_product_into(out: torch.Tensor, x: torch.Tensor, x_scales: torch.Tensor, weights: torch.Tensor,
@@ -670,9 +716,9 @@ def expert_product_into(out: torch.Tensor, x: torch.Tensor, x_scales: torch.Tens
     _check_tensor("weight_scales", weight_scales, torch.uint8, (E, n, nb), dev)
     _check_tensor("ep_recv_count", ep_recv_count, torch.int32, (W, E), dev)
     _check_tensor("out", out, out.dtype, (rows, n // 2 if activation == MOE_ACT_SWIGLU else n), dev)
-    _launch("moe_expert_product", dev, _ptr(x), _ptr(x_scales), element, _ptr(weights), _ptr(weight_scales),
-            _ptr(ep_recv_count), W, E // W, rows, k, n, int(activation), dtype_code(out.dtype), _ptr(out),
-            _stream_ptr(dev))
+    _launch("moe_expert_product", dev, x.data_ptr(), x_scales.data_ptr(), element, weights.data_ptr(),
+            weight_scales.data_ptr(), ep_recv_count.data_ptr(), W, E // W, rows, k, n, int(activation),
+            dtype_code(out.dtype), out.data_ptr(), _stream_ptr(dev))
     return out
 
 

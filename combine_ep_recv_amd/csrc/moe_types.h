@@ -31,12 +31,7 @@ struct F32 {
     static __device__ __forceinline__ raw store(float f) { return __float_as_uint(f); }
 };
 
-// One DPP move (row shift or broadcast); lanes without a source keep v, which max and the masked sum ignore.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float dpp(float old, float v)
-{
-    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL, ROWS, 0xf, false));
-}
+// One DPP move (row shift or broadcast); lanes without a source get `old`.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ double dpp(double old, double v)
 {
@@ -56,10 +51,63 @@ __device__ __forceinline__ double lane_value(double v, int lane)
 __device__ __forceinline__ float max_of(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ double max_of(double a, double b) { return fmax(a, b); }
 
-// Maximum and sum over the 64 lanes, the same value in every lane: row shifts by 1, 2, 4 and 8, then the last
-// lane of a row to the rows above. Every lane of the wavefront is active. The order of the sum is fixed.
-template <class T>
-__device__ __forceinline__ T wave_max(T v)
+// Reductions over a group of LANES lanes (the 64 of a wavefront, or each row of 16), the same value in every lane of
+// the group. Every lane of the wavefront is active. The order of a sum is fixed. Each step is one instruction that
+// moves and combines, behind the two cycles that a move needs after its operand was written (the compiler spends five
+// instructions on it). Of 64 lanes: row shifts by 1, 2, 4 and 8 (lanes without a source keep their value), the last
+// lane of a row to the rows above, then lane 63 to all. Of 16: rotations; a sum takes shifts, so that every lane gets
+// the last one's.
+#define MOE_REDUCE_64(op)                                                                             \
+    "s_nop 1\n\t" op " %0, %0, %0 row_shr:1 row_mask:0xf bank_mask:0xf\n\t"                          \
+    "s_nop 1\n\t" op " %0, %0, %0 row_shr:2 row_mask:0xf bank_mask:0xf\n\t"                          \
+    "s_nop 1\n\t" op " %0, %0, %0 row_shr:4 row_mask:0xf bank_mask:0xf\n\t"                          \
+    "s_nop 1\n\t" op " %0, %0, %0 row_shr:8 row_mask:0xf bank_mask:0xf\n\t"                          \
+    "s_nop 1\n\t" op " %0, %0, %0 row_bcast:15 row_mask:0xa bank_mask:0xf\n\t"                       \
+    "s_nop 1\n\t" op " %0, %0, %0 row_bcast:31 row_mask:0xc bank_mask:0xf\n\t"                       \
+    "s_nop 1"
+#define MOE_REDUCE_16(op)                                                                             \
+    "s_nop 1\n\t" op " %0, %0, %0 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"                          \
+    "s_nop 1\n\t" op " %0, %0, %0 row_ror:4 row_mask:0xf bank_mask:0xf\n\t"                          \
+    "s_nop 1\n\t" op " %0, %0, %0 row_ror:2 row_mask:0xf bank_mask:0xf\n\t"                          \
+    "s_nop 1\n\t" op " %0, %0, %0 row_ror:1 row_mask:0xf bank_mask:0xf"
+template <int LANES = kWave>
+__device__ __forceinline__ float wave_max(float v)
+{
+    if constexpr (LANES == 16) {
+        asm(MOE_REDUCE_16("v_max_f32_dpp") : "+v"(v));
+        return v;
+    }
+    asm(MOE_REDUCE_64("v_max_f32_dpp") : "+v"(v));
+    return lane_value(v, 63);
+}
+template <int LANES = kWave>
+__device__ __forceinline__ uint32_t wave_min(uint32_t v)
+{
+    if constexpr (LANES == 16) {
+        asm(MOE_REDUCE_16("v_min_u32_dpp") : "+v"(v));
+        return v;
+    }
+    asm(MOE_REDUCE_64("v_min_u32_dpp") : "+v"(v));
+    return __builtin_amdgcn_readlane(v, 63);
+}
+template <int LANES = kWave>
+__device__ __forceinline__ float wave_sum(float v)
+{
+    if constexpr (LANES == 16) {
+        asm("s_nop 1\n\tv_add_f32_dpp %0, %0, %0 row_shr:1 row_mask:0xf bank_mask:0xf\n\t"
+            "s_nop 1\n\tv_add_f32_dpp %0, %0, %0 row_shr:2 row_mask:0xf bank_mask:0xf\n\t"
+            "s_nop 1\n\tv_add_f32_dpp %0, %0, %0 row_shr:4 row_mask:0xf bank_mask:0xf\n\t"
+            "s_nop 1\n\tv_add_f32_dpp %0, %0, %0 row_shr:8 row_mask:0xf bank_mask:0xf\n\t"
+            "s_nop 1\n\tv_mov_b32_dpp %0, %0 row_newbcast:15 row_mask:0xf bank_mask:0xf"
+            : "+v"(v));
+        return v;
+    }
+    asm(MOE_REDUCE_64("v_add_f32_dpp") : "+v"(v));
+    return lane_value(v, 63);
+}
+#undef MOE_REDUCE_64
+#undef MOE_REDUCE_16
+__device__ __forceinline__ double wave_max(double v)
 {
     v = max_of(v, dpp<0x111, 0xf>(v, v));
     v = max_of(v, dpp<0x112, 0xf>(v, v));
@@ -69,10 +117,9 @@ __device__ __forceinline__ T wave_max(T v)
     v = max_of(v, dpp<0x143, 0xc>(v, v));
     return lane_value(v, 63);
 }
-template <class T>
-__device__ __forceinline__ T wave_sum(T v)
+__device__ __forceinline__ double wave_sum(double v)
 {
-    const T z = 0;
+    const double z = 0;
     v += dpp<0x111, 0xf>(z, v);
     v += dpp<0x112, 0xf>(z, v);
     v += dpp<0x114, 0xf>(z, v);

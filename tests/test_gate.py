@@ -456,3 +456,46 @@ def test_gate_feeds_dispatch_and_combine():
     # K products of fp16 values summed in fp32 and one rounding to fp16
     assert (out - want).abs().le(want.abs() * (2.0 ** -11 + 2 * K * U) + 2.0 ** -24).all()
     assert (out[7] == 0).all() and int(erc[:, -1].sum()) == int(on.sum())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,E,K,groups,topk_groups", [(513, 16, 4, 1, 1), (1061, 33, 8, 1, 1), (2049, 64, 16, 8, 3),
+                                                      (4099, 128, 1, 1, 1), (6001, 160, 8, 16, 4), (8197, 256, 8, 8, 4),
+                                                      (9731, 304, 8, 1, 1), (10243, 320, 15, 5, 2), (21001, 96, 3, 6, 6)])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+def test_gate_of_long_batches(N, E, K, groups, topk_groups, score):
+    """Batches long enough for several tokens to share a wavefront; a third of the rows hold few distinct logits (ties),
+    some have missing experts or infinities, some tokens are masked. 300 rows are looked at, the last ones among them."""
+    g = torch.Generator().manual_seed(N)
+    for dtype, bias, group_score in ((torch.bfloat16, False, MAX), (torch.float32, True, TOP2), (torch.float16, True, MAX),
+                                     (torch.float32, False, TOP2)):
+        L = draw(N, E, dtype, N + 1)
+        L[::3] = L[::3].round()
+        L[7::31, :E // 2] = -float("inf")
+        L[11::37] = float("nan")
+        L[13::41, E - 1] = float("inf")
+        L[17::43] -= 90.0
+        m = torch.rand(N, generator=g) < 0.8
+        L[~m] = float("nan")
+        b = torch.randint(-2, 3, (E,), generator=g) * 0.25 if bias and dtype == torch.float16 else (
+            torch.randn(E, generator=g) * 0.05 if bias else None)
+        kw = dict(score=score, groups=groups, topk_groups=topk_groups, group_score=group_score, renormalize=bias, scale=1.5)
+        ids, w, on = moe.gate(L.to(DEV), K, bias=None if b is None else b.to(DEV), token_mask=m.to(DEV),
+                              with_pair_mask=True, **kw)
+        rows = torch.cat((torch.randperm(N, generator=g)[:280], torch.arange(N - 20, N)))
+        at = rows.to(DEV)
+        check(L[rows], ids[at], w[at], on[at], bias=b, token_mask=m[rows], **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+def test_gate_of_long_batches_on_the_last_bits(score):
+    """As test_gate_choices_that_hang_on_the_last_bits, several tokens to a wavefront: every token is decided anew."""
+    N, E = 1100, 32
+    L = draw(1, E, torch.float32, 12)
+    b = torch.from_numpy((0.5 - scores(L[0].numpy(), score)[0]).astype(np.float32))
+    L = L.expand(N, E).contiguous()
+    L[::2] = draw(N, E, torch.float32, 13)[::2]
+    ids, w = moe.gate(L.to(DEV), 8, score, bias=b.to(DEV))
+    check(L[:40], ids[:40], w[:40], bias=b, score=score)
+    assert (ids[1::2] == ids[1]).all() and (w[1::2] == w[1]).all()
