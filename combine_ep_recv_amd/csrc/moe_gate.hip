@@ -413,69 +413,81 @@ struct GateGradArgs {
     float scale;
 };
 
-template <class T, int PER, int WAVES, int SCORE, bool RENORM>
+// One wavefront per token. Lane k takes pair k; the pairs' gradients meet the experts in an LDS row, from which each lane
+// writes its experts', VEC neighbouring ones at a time (two where rows of 16-bit logits start at 4 bytes: half as many
+// loads and stores). The row of logits, where every expert needs its score, is on its way before anything else.
+template <class T, int PER, int VEC, int WAVES, int SCORE, bool RENORM>
 __global__ __launch_bounds__(WAVES *kWave) void gate_backward_kernel(GateGradArgs a)
 {
-    __shared__ float rows[WAVES][PER * kWave];
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    constexpr bool kDense = SCORE == MOE_SCORE_SOFTMAX && !RENORM;
+    using raw = typename T::raw;
+    typedef raw vec __attribute__((ext_vector_type(VEC)));
+    typedef float fvec __attribute__((ext_vector_type(VEC)));
+    __shared__ fvec rows[WAVES][PER * kWave];
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int t = blockIdx.x * WAVES + wave;
     if (t >= a.tokens) return;
-    const float low = -INFINITY;
-    const typename T::raw *row = static_cast<const typename T::raw *>(a.logits) + (size_t)t * a.experts;
-    int id = -1;
-    float w = 0.f, g = 0.f;
-    if (lane < a.topk) {
-        const size_t at = (size_t)t * a.topk + lane;
-        id = a.ids[at];
-        if (id < 0 || id >= a.experts) id = -1;
-        else {
-            w = a.weights[at];
-            g = a.grad[at];
-        }
+    const float low = -INFINITY, log2e = 1.44269504f;
+    const raw *row = static_cast<const raw *>(a.logits) + (size_t)t * a.experts;
+    const int groups = a.experts / VEC;                       // VEC divides experts
+    vec in[PER];
+    if (kDense) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) in[j] = reinterpret_cast<const vec *>(row)[min(j * kWave + lane, groups - 1)];
     }
+    const size_t at = (size_t)t * a.topk + min(lane, a.topk - 1);
+    int id = a.ids[at];
+    float w = a.weights[at], g = a.grad[at];
+    const bool mine = lane < a.topk && id >= 0 && id < a.experts;
+    if (!mine) w = g = 0.f;
     const float dot = wave_sum(g * w);
     float d = RENORM ? w * (g - dot / a.scale) : a.scale * g;
-    if (SCORE == MOE_SCORE_SIGMOID && id >= 0) {
+    if (SCORE == MOE_SCORE_SIGMOID && mine) {
         const float l = T::load(row[id]);
         d *= 1.f / (1.f + expf(l));
         if (!RENORM) d *= 1.f / (1.f + expf(-l));
     }
-    float *mine = rows[wave];
+    fvec *own = rows[wave];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) mine[j * kWave + lane] = 0.f;
+    for (int j = 0; j < PER; ++j) own[j * kWave + lane] = fvec(0.f);
     wave_fence();
-    if (id >= 0) atomicAdd(&mine[id], d);          // ids of a token are distinct
+    if (mine) atomicAdd(reinterpret_cast<float *>(own) + id, d);          // ids of a token are distinct
     wave_fence();
-    typename T::raw *out = static_cast<typename T::raw *>(a.out) + (size_t)t * a.experts;
-    if (SCORE == MOE_SCORE_SOFTMAX && !RENORM) {
-        const bool any = __ballot(id >= 0) != 0;
-        float l[PER], top = low, sum = 0.f;
+    float s[PER][VEC], top = low, sum = 0.f, inv = 0.f;
+    if (kDense) {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int e = j * kWave + lane;
-            l[j] = any && e < a.experts ? T::load(row[e]) : low;
-            if (!(l[j] > low)) l[j] = low;
-            top = fmaxf(top, l[j]);
-        }
+        for (int j = 0; j < PER; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                s[j][i] = j * kWave + lane < groups ? fmaxf(T::load(in[j][i]), low) : low;      // NaN too
+                top = fmaxf(top, s[j][i]);
+            }
         top = wave_max(top);
+        const bool endless = !(top < INFINITY);               // logits of +infinity share the softmax
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            l[j] = l[j] > low ? expf(l[j] == top ? 0.f : l[j] - top) : 0.f;
-            sum += l[j];
-        }
+        for (int j = 0; j < PER; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const float e = __builtin_amdgcn_exp2f((s[j][i] - top) * log2e);
+                s[j][i] = endless ? (s[j][i] == top ? 1.f : 0.f) : (s[j][i] > low ? e : 0.f);
+                sum += s[j][i];
+            }
         sum = wave_sum(sum);
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        inv = sum > 0.f && __ballot(mine) ? 1.f / sum : 0.f;  // a token without pairs gets nothing
+    }
+    raw *out = static_cast<raw *>(a.out) + (size_t)t * a.experts;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int e = j * kWave + lane;
-            if (e < a.experts) out[e] = T::store(l[j] * inv * (mine[e] - dot));
-        }
-    } else {
+    for (int j = 0; j < PER; ++j) {
+        const int e = j * kWave + lane;
+        const fvec x = own[e];
+        vec v;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int e = j * kWave + lane;
-            if (e < a.experts) out[e] = T::store(mine[e]);
+        for (int i = 0; i < VEC; ++i) {
+            float y = x[i];
+            if (kDense) y = inv > 0.f ? s[j][i] * inv * (y - dot) : 0.f;
+            v[i] = T::store(y);
         }
+        if (e < groups) reinterpret_cast<vec *>(out)[e] = v;
     }
 }
 
@@ -602,20 +614,38 @@ int moe_gate_backward(const void *logits, const int32_t *expert_ids, const float
     a.scale = scale;
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
+    // pairs of 16-bit logits: rows of an even length from a 4-byte boundary
+    const bool pairs = xs == 2 && experts % 2 == 0 && aligned(logits, 4) && aligned(grad_logits, 4);
     by_type(dtype, [&](auto type) {
-        by_row(experts, [&](auto per, auto waves) {
-            using T = decltype(type);
-            constexpr int P = decltype(per)::value, V = decltype(waves)::value;
+        using T = decltype(type);
+        auto launch = [&](auto per, auto vec, auto waves) {
+            constexpr int P = decltype(per)::value, C = decltype(vec)::value, V = decltype(waves)::value;
             const dim3 g((unsigned)((tokens + V - 1) / V)), b(V * kWave);
             if (score == MOE_SCORE_SOFTMAX && renormalize)
-                hipLaunchKernelGGL((gate_backward_kernel<T, P, V, MOE_SCORE_SOFTMAX, true>), g, b, 0, st, a);
+                hipLaunchKernelGGL((gate_backward_kernel<T, P, C, V, MOE_SCORE_SOFTMAX, true>), g, b, 0, st, a);
             else if (score == MOE_SCORE_SOFTMAX)
-                hipLaunchKernelGGL((gate_backward_kernel<T, P, V, MOE_SCORE_SOFTMAX, false>), g, b, 0, st, a);
+                hipLaunchKernelGGL((gate_backward_kernel<T, P, C, V, MOE_SCORE_SOFTMAX, false>), g, b, 0, st, a);
             else if (renormalize)
-                hipLaunchKernelGGL((gate_backward_kernel<T, P, V, MOE_SCORE_SIGMOID, true>), g, b, 0, st, a);
+                hipLaunchKernelGGL((gate_backward_kernel<T, P, C, V, MOE_SCORE_SIGMOID, true>), g, b, 0, st, a);
             else
-                hipLaunchKernelGGL((gate_backward_kernel<T, P, V, MOE_SCORE_SIGMOID, false>), g, b, 0, st, a);
-        });
+                hipLaunchKernelGGL((gate_backward_kernel<T, P, C, V, MOE_SCORE_SIGMOID, false>), g, b, 0, st, a);
+        };
+        using std::integral_constant;
+        using One = integral_constant<int, 1>;
+        using Two = integral_constant<int, 2>;
+        using Four = integral_constant<int, 4>;
+        if constexpr (sizeof(typename T::raw) == 2) {
+            if (pairs) {
+                if (experts <= 128) launch(One(), Two(), Four());
+                else if (experts <= 256) launch(Two(), Two(), Four());
+                else if (experts <= 384) launch(integral_constant<int, 3>(), Two(), Four());
+                else if (experts <= 512) launch(Four(), Two(), Four());
+                else if (experts <= 1024) launch(integral_constant<int, 8>(), Two(), Four());
+                else launch(integral_constant<int, 16>(), Two(), One());
+                return;
+            }
+        }
+        by_row(experts, [&](auto per, auto waves) { launch(per, One(), waves); });
     });
     return launched();
 }
