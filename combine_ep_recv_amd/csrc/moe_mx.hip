@@ -206,13 +206,11 @@ __global__ __launch_bounds__(kMxThreads) void dequantize_kernel(MxArgs a)
 // the experts' product
 // --------------------------------------------------------------------------
 
-constexpr int kProductThreads = 256;       // four wavefronts
 constexpr int kMaxExperts = 1024;          // dispatch's limits
 constexpr int kMinWorld = 2, kMaxWorld = 768;
 constexpr int kStep = 128;                 // elements of k in one matrix instruction
 constexpr int kSuper = 4 * kStep;          // ... in a group of four, whose 16 scale bytes are one load
 constexpr int kWorkgroups = 1024;          // at most: every CU's fill, with tiles to spare for none
-constexpr int kFrags = 4;                  // 16-wide weight fragments of a workgroup
 
 struct ProductArgs {
     const uint8_t *x, *xs, *w, *ws;
@@ -230,17 +228,32 @@ struct Tile {
 // its own. One copy in each workgroup's LDS, made once: workgroups stay for many tiles.
 struct Plan {
     uint32_t row[kMaxExperts + 1], tile[kMaxExperts + 1];
-    uint32_t part[2][kProductThreads / kWave];
+    uint32_t part[2][8];
     int expert;
 };
 
+// Inclusive sums over the 64 lanes that stop at `most` (which keeps them in 32 bits and in order; sums that never
+// reach it are plain ones).
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v, uint32_t most)
+{
+#define MOE_SCAN_STEP(CTRL, ROWS) v = min(most, v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false));
+    MOE_SCAN_STEP(0x111, 0xf)          // row shifts by 1, 2, 4 and 8
+    MOE_SCAN_STEP(0x112, 0xf)
+    MOE_SCAN_STEP(0x114, 0xf)
+    MOE_SCAN_STEP(0x118, 0xf)
+    MOE_SCAN_STEP(0x142, 0xa)          // the last lane of a row to the next row, of the lower half to the upper one
+    MOE_SCAN_STEP(0x143, 0xc)
+#undef MOE_SCAN_STEP
+    return v;
+}
+
 // Fills the plan for tiles of BM rows and returns their number. The counts are ep_recv_count's differences, held
 // within [0, rows] whatever the array holds. All threads call it.
-template <int BM>
+template <int BM, int THREADS>
 __device__ int make_plan(const ProductArgs &a, Plan &plan)
 {
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-    constexpr int kEach = kMaxExperts / kProductThreads;
+    constexpr int kEach = kMaxExperts / THREADS;
     const uint32_t most = (uint32_t)a.rows;
     uint32_t count[kEach], sum = 0;
 #pragma unroll
@@ -255,16 +268,10 @@ __device__ int make_plan(const ProductArgs &a, Plan &plan)
         }
         sum = min(most, sum + count[i]);
     }
-    // rows before this thread's experts (sums that stop at `rows`, which keeps them in 32 bits and in order)
-    uint32_t inc = sum;
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-        const uint32_t v = __shfl_up(inc, d);
-        if (lane >= d) inc = min(most, inc + v);
-    }
+    // rows before this thread's experts
+    uint32_t inc = wave_scan(sum, most);
     if (lane == kWave - 1) plan.part[0][wave] = inc;
-    uint32_t before = __shfl_up(inc, 1);
-    if (lane == 0) before = 0;
+    uint32_t before = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)inc, 0x138, 0xf, 0xf, false);    // one lane up
     __syncthreads();
     for (int i = 0; i < wave; ++i) before = min(most, before + plan.part[0][i]);
     uint32_t start[kEach + 1], tiles = 0;
@@ -274,12 +281,7 @@ __device__ int make_plan(const ProductArgs &a, Plan &plan)
         start[i + 1] = min(most, start[i] + count[i]);
         tiles += (start[i + 1] - start[i] + BM - 1) / BM;
     }
-    inc = tiles;
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-        const uint32_t v = __shfl_up(inc, d);
-        if (lane >= d) inc += v;
-    }
+    inc = wave_scan(tiles, 0x7fffffffu);
     if (lane == kWave - 1) plan.part[1][wave] = inc;
     uint32_t at = inc - tiles;
     __syncthreads();
@@ -290,7 +292,7 @@ __device__ int make_plan(const ProductArgs &a, Plan &plan)
         plan.tile[tid * kEach + i] = at;
         at += (start[i + 1] - start[i] + BM - 1) / BM;
     }
-    if (tid == kProductThreads - 1) {
+    if (tid == THREADS - 1) {
         plan.row[kMaxExperts] = start[kEach];
         plan.tile[kMaxExperts] = at;
     }
@@ -299,11 +301,10 @@ __device__ int make_plan(const ProductArgs &a, Plan &plan)
 }
 
 // Row tile `mt` of the plan (below its number of tiles). All threads call it; it holds a barrier.
-template <int BM>
-__device__ Tile find_tile(Plan &plan, int mt)
+template <int BM, int THREADS>
+__device__ Tile find_tile(const ProductArgs &a, Plan &plan, int mt)
 {
-    const int tid = threadIdx.x;
-    for (int e = tid; e < kMaxExperts; e += kProductThreads)
+    for (int e = threadIdx.x; e < a.E; e += THREADS)
         if (plan.tile[e] <= (uint32_t)mt && (uint32_t)mt < plan.tile[e + 1]) plan.expert = e;
     __syncthreads();
     const int e = __builtin_amdgcn_readfirstlane(plan.expert);
@@ -326,37 +327,6 @@ __device__ __forceinline__ i32x8 join(u32x4 lo, u32x4 hi)
     return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
-// The 32 elements of a step that starts at element `at` of a row, whole
-template <int XF>
-__device__ __forceinline__ i32x8 load_step(const uint8_t *row, int at, int g)
-{
-    if constexpr (XF == 4) {
-        const u32x4 v = *reinterpret_cast<const u32x4_a8 *>(row + (at + 32 * g) / 2);
-        return join(v, v);
-    } else {
-        return join(*reinterpret_cast<const u32x4 *>(row + at + 16 * g),
-                    *reinterpret_cast<const u32x4 *>(row + at + 64 + 16 * g));
-    }
-}
-// ... with zeros past the row's k elements
-template <int XF>
-__device__ __forceinline__ i32x8 load_last(const uint8_t *row, int at, int g, int k)
-{
-    u32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-    if constexpr (XF == 4) {
-        const int p = at + 32 * g;
-        if (p + 32 <= k) lo = *reinterpret_cast<const u32x4_a8 *>(row + p / 2);
-        else if (p < k) {
-            const u32x2 v = *reinterpret_cast<const u32x2 *>(row + p / 2);
-            lo[0] = v[0];
-            lo[1] = v[1];
-        }
-    } else {
-        if (at + 16 * g < k) lo = *reinterpret_cast<const u32x4 *>(row + at + 16 * g);
-        if (at + 64 + 16 * g < k) hi = *reinterpret_cast<const u32x4 *>(row + at + 64 + 16 * g);
-    }
-    return join(lo, hi);
-}
 // 16 bytes of a step, piece p of a row (`row` points at its own first piece), with zeros past the row's k elements
 template <int XF>
 __device__ __forceinline__ u32x4 load_piece_or_zero(const uint8_t *row, int at, int p, int k)
@@ -373,13 +343,8 @@ __device__ __forceinline__ u32x4 load_piece_or_zero(const uint8_t *row, int at, 
     }
     return v;
 }
-// The scale bytes of a lane's blocks in four steps: byte g of each word of the row's 16 bytes, one word
-__device__ __forceinline__ uint32_t load_scales(const uint8_t *p, uint32_t sel)
-{
-    const u32x4 d = *reinterpret_cast<const u32x4_a1 *>(p);
-    return __builtin_amdgcn_perm(d[1], d[0], sel) | (__builtin_amdgcn_perm(d[3], d[2], sel) << 16);
-}
-// ... for every g: a transpose of 4 x 4 bytes
+// The scale bytes of a row in four steps, 16 of them, as a word for each g: byte g of every word, a transpose of 4 x 4
+// bytes.
 __device__ __forceinline__ u32x4 by_group(u32x4 d)
 {
     const uint32_t a = __builtin_amdgcn_perm(d[1], d[0], 0x05010400u), b = __builtin_amdgcn_perm(d[3], d[2], 0x05010400u);
@@ -411,112 +376,25 @@ __device__ __forceinline__ float swiglu(float gate, float up)
     return gate * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(gate * -1.44269504f)) * up;
 }
 
-// Rows of one expert, 16 * FR at a time, against 64 weight rows (32 of the gate's and 32 of the up projection's
-// with GLU). The four wavefronts share out k in supersteps of 512 and add up in LDS, wavefront 0's part first.
-template <class T, int XF, int FR, bool GLU>
-__global__ __launch_bounds__(kProductThreads) void expert_product_kernel(ProductArgs a)
+// 16 bytes a lane from device memory into LDS, the wavefront's 1 KiB one after the other from `to`, past the registers.
+__device__ __forceinline__ void fetch_lds(const uint8_t *from, u32x4 *to)
 {
-    __shared__ Plan plan;
-    __shared__ f32x4 part[kProductThreads / kWave][kFrags][kWave];
-    const int total = make_plan<FR * 16>(a, plan) * a.ntiles;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
-    const int nt = t % a.ntiles;
-    const Tile tile = find_tile<FR * 16>(plan, t / a.ntiles);
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int r = lane % 16, g = lane / 16;
-    constexpr int kOut = GLU ? kFrags / 2 : kFrags;          // output fragments of 16 columns
-    const int half = a.n / 2, col0 = nt * kOut * 16;
-    const size_t wrow = (size_t)a.k / 2, xrow = XF == 4 ? (size_t)a.k / 2 : (size_t)a.k;
-    const uint8_t *wp[kFrags], *wsp[kFrags], *xp[FR], *xsp[FR];
-#pragma unroll
-    for (int j = 0; j < kFrags; ++j) {
-        // columns past the last one read the last one's weights; their results are not stored
-        const int c = min(col0 + (j % kOut) * 16 + r, a.fo - 1);
-        const size_t row = (size_t)tile.expert * a.n + (GLU && j >= kOut ? half : 0) + c;
-        wp[j] = a.w + row * wrow;
-        wsp[j] = a.ws + row * a.nb;
-    }
-#pragma unroll
-    for (int f = 0; f < FR; ++f) {
-        const size_t row = min(tile.row + f * 16 + r, tile.end - 1);
-        xp[f] = a.x + row * xrow;
-        xsp[f] = a.xs + row * a.nb;
-    }
-    f32x4 acc[FR][kFrags];
-#pragma unroll
-    for (int f = 0; f < FR; ++f)
-#pragma unroll
-        for (int j = 0; j < kFrags; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    const uint32_t sel = 0x0c0c0400u + 0x0101u * g;           // byte g of the low word, byte g of the high word
-    const int supers = a.k / kSuper;
-    for (int s = wave; s < supers; s += kProductThreads / kWave) {
-        uint32_t ws[kFrags], xs[FR];
-#pragma unroll
-        for (int j = 0; j < kFrags; ++j) ws[j] = load_scales(wsp[j] + 16 * s, sel);
-#pragma unroll
-        for (int f = 0; f < FR; ++f) xs[f] = load_scales(xsp[f] + 16 * s, sel);
-#define MOE_STEP(I)                                                                                   \
-        {                                                                                             \
-            i32x8 wf[kFrags], xf[FR];                                                                 \
-            _Pragma("unroll") for (int j = 0; j < kFrags; ++j)                                        \
-                wf[j] = load_step<4>(wp[j], kSuper * s + kStep * I, g);                               \
-            _Pragma("unroll") for (int f = 0; f < FR; ++f)                                            \
-                xf[f] = load_step<XF>(xp[f], kSuper * s + kStep * I, g);                              \
-            _Pragma("unroll") for (int f = 0; f < FR; ++f)                                            \
-                _Pragma("unroll") for (int j = 0; j < kFrags; ++j)                                    \
-                    acc[f][j] = mma<XF, I>(wf[j], xf[f], acc[f][j], ws[j], xs[f]);                    \
-        }
-        MOE_STEP(0)
-        MOE_STEP(1)
-        MOE_STEP(2)
-        MOE_STEP(3)
-#undef MOE_STEP
-    }
-    // the last k % 512 elements, one step to a wavefront in turn
-    for (int at = supers * kSuper + kStep * wave; at < a.k; at += kSuper) {
-        const int b = at / kBlock + g;
-        i32x8 wf[kFrags], xf[FR];
-        uint32_t ws[kFrags], xs[FR];
-#pragma unroll
-        for (int j = 0; j < kFrags; ++j) {
-            wf[j] = load_last<4>(wp[j], at, g, a.k);
-            ws[j] = b < a.nb ? wsp[j][b] : 127;
-        }
-#pragma unroll
-        for (int f = 0; f < FR; ++f) {
-            xf[f] = load_last<XF>(xp[f], at, g, a.k);
-            xs[f] = b < a.nb ? xsp[f][b] : 127;
-        }
-#pragma unroll
-        for (int f = 0; f < FR; ++f)
-#pragma unroll
-            for (int j = 0; j < kFrags; ++j) acc[f][j] = mma<XF, 0>(wf[j], xf[f], acc[f][j], ws[j], xs[f]);
-    }
-
-#pragma unroll
-    for (int f = 0; f < FR; ++f) {
-        if (f) __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kFrags; ++j) part[wave][j][lane] = acc[f][j];
-        __syncthreads();
-        if (wave < kOut) {
-            f32x4 v = part[0][wave][lane];
-#pragma unroll
-            for (int i = 1; i < kProductThreads / kWave; ++i) v += part[i][wave][lane];
-            if (GLU) {
-                f32x4 u = part[0][wave + kOut][lane];
-#pragma unroll
-                for (int i = 1; i < kProductThreads / kWave; ++i) u += part[i][wave + kOut][lane];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = swiglu(v[i], u[i]);
-            }
-            const int row = tile.row + f * 16 + r, col = col0 + wave * 16 + 4 * g;
-            if (row < tile.end && col < a.fo) store_out<T>(a, row, col, v);
-        }
-    }
-    __syncthreads();
-    }
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                     (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+}
+// A barrier behind which every wavefront's LDS reads and writes, and all but its youngest LEFT fetches into LDS, are
+// done. (The wait is the builtin: the compiler then knows which fetches are in and puts no wait of its own before the
+// reads. The fence of __syncthreads would wait for all of them; the empty asm keeps memory accesses in their place.)
+template <int LEFT>
+__device__ __forceinline__ void barrier_fetched()
+{
+    static_assert(LEFT < 64, "vmcnt has 6 bits");
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070 | (LEFT & 15) | (LEFT >> 4) << 14);      // vmcnt LEFT, lgkmcnt 0
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // Rows of one expert, 16 * FR * WM at a time, against 16 * NF * WN weight rows (half of them the gate's, half the
@@ -526,213 +404,212 @@ __global__ __launch_bounds__(kProductThreads) void expert_product_kernel(Product
 // apart, so loading straight into its layout makes the cache look at every lane's 16 bytes by itself (one look-up a
 // clock), where eight adjacent lanes that read a line of 128 bytes count as one. A stage is 128 bytes of an input
 // row, kSub instruction steps: 256 elements of E2M1, 128 of E4M3. The 16-byte pieces of a row are swapped by its number
-// so that the eight lanes that LDS serves in a clock meet every bank once, writing and reading.
+// (each lane fetches the piece that belongs where it writes) so that the eight lanes that LDS serves in a clock meet
+// every bank once.
 //
-// A stage's pieces are fetched into registers two stages ahead and written to the idle half of LDS one ahead, a few
-// between each fragment's matrix instructions, so that those never run dry. Input fragments are read two ahead. The
-// barrier comes when the current half has been read, two fragments before a stage's end; the next stage's first
-// fragments are read behind it while those two multiply. Scale bytes come 512 elements (four steps) at a time and
-// become a word per (row, g) on the way.
-template <class T, int XF, int FR, int NF, int WM, bool GLU>
-__global__ __launch_bounds__(kProductThreads, FR *NF <= 16 ? 2 : 1) void expert_product_wide_kernel(ProductArgs a)
+// LDS holds RING stages. The barrier comes when the current one has been read, two fragments before its end; behind it
+// the stage RING ahead is fetched in its place, and the next one's first fragments are read while those two multiply.
+// With two stages the next one is on its way while one is multiplied; with four, three are, for shapes that wait for
+// the weights from device memory. Input fragments are read two ahead. Scale bytes come 512 elements (four steps) at a time, through
+// registers, and become a word per (row, g) on the way.
+template <class T, int XF, int FR, int NF, int WM, int WN, int SUB, int RING, bool GLU>
+__global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(ProductArgs a)
 {
-    constexpr int kWaves = kProductThreads / kWave, WN = kWaves / WM, kRowsW = WN * NF * 16, kRowsX = WM * FR * 16;
-    constexpr int kSub = XF == 4 ? 2 : 1, kStages = 4 / kSub;  // steps of a stage, stages of 512 elements
-    constexpr int kPw = 4 * kSub, kPx = 8;                    // 16-byte pieces of a row in a stage
-    constexpr int kLoadsW = kRowsW * kPw / kProductThreads, kLoadsX = kRowsX * kPx / kProductThreads;
-    constexpr int kLoads = kLoadsW + kLoadsX;
-    constexpr int kScalesW = kRowsW / kProductThreads;        // scale rows of the weights that a thread carries
-    static_assert(kRowsW % kProductThreads == 0 && kRowsX <= kProductThreads, "whole scale rows a thread");
-    static_assert(kRowsX * kPx % kProductThreads == 0, "every thread carries as many pieces");
+    constexpr int kThreads = WM * WN * kWave, kRowsW = WN * NF * 16, kRowsX = WM * FR * 16;
+    constexpr int kSub = XF == 4 ? SUB : 1, kStages = 4 / kSub;   // steps of a stage, stages of 512 elements
+    constexpr int kPw = 4 * kSub, kPx = XF == 4 ? kPw : 8;    // 16-byte pieces of a row in a stage
+    constexpr int kLoadsW = kRowsW * kPw / kThreads, kLoadsX = kRowsX * kPx / kThreads, kLoads = kLoadsW + kLoadsX;
+    constexpr int kRows = kRowsW + kRowsX, kScales = (kRows + kThreads - 1) / kThreads;   // scale rows of a thread
+    static_assert(kRowsW * kPw % kThreads == 0 && kRowsX * kPx % kThreads == 0, "every thread carries as many pieces");
+    static_assert(RING == 2 || (RING == 4 && kStages == 4), "a stage's place in the ring is known where it is used");
+    // a stage's weights, then its inputs; an array a stage, so that the compiler tells them apart
+    constexpr int kSizeW = kRowsW * kPw, kSize = kSizeW + kRowsX * kPx;
+    __shared__ u32x4 l0[kSize], l1[kSize], l2[RING == 4 ? kSize : 1], l3[RING == 4 ? kSize : 1];
+    __shared__ u32x4 s0[kRows], s1[kRows];
+    auto ring = [&](int i) -> u32x4 * { return i % RING == 0 ? l0 : (i % RING == 1 ? l1 : (i % RING == 2 ? l2 : l3)); };
     __shared__ Plan plan;
-    __shared__ u32x4 wl[2][kRowsW * kPw], xl[2][kRowsX * kPx], wsl[2][kRowsW], xsl[2][kRowsX];
-
-    const int total = make_plan<kRowsX>(a, plan) * a.ntiles;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
-    const int nt = t % a.ntiles;
-    const Tile tile = find_tile<kRowsX>(plan, t / a.ntiles);
+    const int total = make_plan<kRowsX, kThreads>(a, plan) * a.ntiles;
     const int tid = threadIdx.x, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave), wm = wave / WN, wn = wave % WN;
     const int r = lane % 16, g = lane / 16;
     constexpr int kOut = GLU ? NF / 2 : NF, kOwn = NF * 16;   // output fragments and weight rows of a wavefront
-    const int half = a.n / 2, tile0 = nt * WN * kOut * 16;
+    const int half = a.n / 2;
     const uint32_t wrow = a.k / 2, xrow = XF == 4 ? a.k / 2 : a.k;
-    const uint8_t *wb = a.w + (size_t)tile.expert * a.n * wrow, *wsb = a.ws + (size_t)tile.expert * a.n * a.nb;
-    const uint8_t *xb = a.x + (size_t)tile.row * xrow, *xsb = a.xs + (size_t)tile.row * a.nb;
-    const int last = tile.end - 1 - tile.row;                 // rows past the expert's last read the last one
-    // weight row of a place in the tile; columns past the last one read the last one's, and are not stored
-    auto weight_row = [&](int q) -> uint32_t {
-        const int c = GLU ? q / kOwn * (kOwn / 2) + q % (kOwn / 2) : q;
-        return (GLU && q % kOwn >= kOwn / 2 ? half : 0) + min(tile0 + c, a.fo - 1);
-    };
+    const int supers = a.k / kSuper, stages = supers * kStages;
     // piece p of row q in LDS, for rows of 4 and of 8 pieces
     auto place4 = [](int q, int p) { return q * 4 + (p ^ ((q >> 1) & 3)); };
     auto place8 = [](int q, int p) { return q * 8 + (p ^ (q & 7)); };
-    // this thread's pieces: where in a row's stage, and the place in LDS (piece i: kProductThreads * i further)
-    uint32_t wo[kLoadsW], xo[kLoadsX];
-#pragma unroll
-    for (int i = 0; i < kLoadsW; ++i) wo[i] = weight_row((tid + i * kProductThreads) / kPw) * wrow + 16 * (tid % kPw);
-#pragma unroll
-    for (int i = 0; i < kLoadsX; ++i) xo[i] = (uint32_t)min((tid + i * kProductThreads) / kPx, last) * xrow + 16 * (tid % kPx);
-    const int wat = kSub == 2 ? place8(tid / 8, tid % 8) : place4(tid / 4, tid % 4), xat = place8(tid / 8, tid % 8);
-    uint32_t wso[kScalesW];
-#pragma unroll
-    for (int i = 0; i < kScalesW; ++i) wso[i] = weight_row(tid + i * kProductThreads) * a.nb;
-    const uint32_t xso = (uint32_t)min(tid % kRowsX, last) * a.nb;
     // a reader's pieces: of fragment 0, the others lie 16 rows apart
     const int lo = place8(r, g), hi = place8(r, 4 + g);
-    const int wfrag[2] = {wn * kOwn * kPw + (kSub == 2 ? lo : place4(r, g)), wn * kOwn * kPw + hi};
-    const int xfrag[2] = {wm * FR * 16 * kPx + lo, wm * FR * 16 * kPx + hi};
+    const int wfrag[2] = {wn * kOwn * kPw + (kPw == 8 ? lo : place4(r, g)), wn * kOwn * kPw + hi};
+    const int xfrag[2] = {wm * FR * 16 * kPx + (kPx == 8 ? lo : place4(r, g)), wm * FR * 16 * kPx + hi};
+    // the piece that this thread fetches of its rows (rows of its later pieces are a multiple of 8 on)
+    const int p8 = tid % 8 ^ (tid / 8 % 8), p4 = tid % 4 ^ (tid / 8 % 4);
+    const int pw = kPw == 8 ? p8 : p4, px = kPx == 8 ? p8 : p4;
 
-    f32x4 acc[FR][NF];
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+        const Tile tile = find_tile<kRowsX, kThreads>(a, plan, t / a.ntiles);
+        const int tile0 = t % a.ntiles * (WN * kOut * 16);
+        const uint8_t *wb = a.w + (size_t)tile.expert * a.n * wrow, *wsb = a.ws + (size_t)tile.expert * a.n * a.nb;
+        const uint8_t *xb = a.x + (size_t)tile.row * xrow, *xsb = a.xs + (size_t)tile.row * a.nb;
+        const int last = tile.end - 1 - tile.row;             // rows past the expert's last read the last one
+        // weight row of a place in the tile; columns past the last one read the last one's, and are not stored
+        auto weight_row = [&](int q) -> uint32_t {
+            const int c = GLU ? q / kOwn * (kOwn / 2) + q % (kOwn / 2) : q;
+            return (GLU && q % kOwn >= kOwn / 2 ? half : 0) + min(tile0 + c, a.fo - 1);
+        };
+        uint32_t wo[kLoadsW], xo[kLoadsX];
 #pragma unroll
-    for (int f = 0; f < FR; ++f)
+        for (int i = 0; i < kLoadsW; ++i) wo[i] = weight_row((tid + i * kThreads) / kPw) * wrow + 16 * pw;
 #pragma unroll
-        for (int j = 0; j < NF; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < kLoadsX; ++i) xo[i] = (uint32_t)min((tid + i * kThreads) / kPx, last) * xrow + 16 * px;
+        // scale rows: the weights', then the inputs'; threads past the last one carry it too (the same bytes)
+        const uint8_t *sp[kScales];
+        int sq[kScales];
+#pragma unroll
+        for (int i = 0; i < kScales; ++i) {
+            sq[i] = min(tid + i * kThreads, kRows - 1);
+            sp[i] = sq[i] < kRowsW ? wsb + (size_t)weight_row(sq[i]) * a.nb : xsb + (size_t)min(sq[i] - kRowsW, last) * a.nb;
+        }
 
-    const int supers = a.k / kSuper, stages = supers * kStages;
-    u32x4 piece[kLoads], wsr[kScalesW], xsr;
-    // Loads of whole stages. Beyond the last one the last one is read again, and not used: a branch here would make
-    // the compiler wait for the load at its end.
-    auto load = [&](int i, int stage) {
-        const uint32_t at = min(stage, stages - 1);
-        if (i < kLoadsW) piece[i] = *reinterpret_cast<const u32x4_a8 *>(wb + (wo[i] + at * (16 * kPw)));
-        else piece[i] = *reinterpret_cast<const u32x4_a8 *>(xb + (xo[i - kLoadsW] + at * (16 * kPx)));
-    };
-    auto keep = [&](int i, int buf) {
-        if (i < kLoadsW) wl[buf][wat + i * kProductThreads] = piece[i];
-        else xl[buf][xat + (i - kLoadsW) * kProductThreads] = piece[i];
-    };
-    auto load_scales = [&](int super) {
-        const uint32_t at = min(super, supers - 1) * 16;
+        f32x4 acc[FR][NF];
 #pragma unroll
-        for (int i = 0; i < kScalesW; ++i) wsr[i] = *reinterpret_cast<const u32x4_a1 *>(wsb + (wso[i] + at));
-        xsr = *reinterpret_cast<const u32x4_a1 *>(xsb + (xso + at));
-    };
-    auto keep_scales = [&](int buf) {
+        for (int f = 0; f < FR; ++f)
 #pragma unroll
-        for (int i = 0; i < kScalesW; ++i) wsl[buf][tid + i * kProductThreads] = by_group(wsr[i]);
-        xsl[buf][tid % kRowsX] = by_group(xsr);          // threads of the same row write the same bytes
-    };
-    const uint32_t *wsw = reinterpret_cast<const uint32_t *>(wsl) + (wn * kOwn + r) * 4 + g;
-    const uint32_t *xsw = reinterpret_cast<const uint32_t *>(xsl) + (wm * FR * 16 + r) * 4 + g;
-    i32x8 wf[2][NF], xf[FR];
-    uint32_t ws[NF], xs[FR];
-    // fragments of step i of 512 elements
-    auto read_w = [&](int i) {
-        const u32x4 *l = wl[i / kSub & 1] + wfrag[i % kSub];
+            for (int j = 0; j < NF; ++j) acc[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+        u32x4 raw[kScales];
+        // Fetches of whole stages. Beyond the last one the last one is fetched again, and not used: a branch here would
+        // part the steps that it stands between, and the waits count the fetches.
+        auto fetch = [&](int stage, int slot) {
+            const uint32_t at = min(stage, stages - 1);
+            u32x4 *wl = ring(slot), *xl = wl + kSizeW;
 #pragma unroll
-        for (int j = 0; j < NF; ++j) wf[i & 1][j] = join(l[j * 16 * kPw], l[j * 16 * kPw]);
-    };
-    auto read_x = [&](int i, int f) {
-        const u32x4 *l = xl[i / kSub & 1] + f * 16 * kPx;
-        xf[f] = XF == 4 ? join(l[xfrag[i % kSub]], l[xfrag[i % kSub]]) : join(l[xfrag[0]], l[xfrag[1]]);
-    };
-    auto read_scales = [&](int buf) {
+            for (int i = 0; i < kLoadsW; ++i) fetch_lds(wb + (wo[i] + at * (16 * kPw)), wl + i * kThreads + wave * kWave);
 #pragma unroll
-        for (int j = 0; j < NF; ++j) ws[j] = wsw[buf * kRowsW * 4 + j * 64];
+            for (int i = 0; i < kLoadsX; ++i) fetch_lds(xb + (xo[i] + at * (16 * kPx)), xl + i * kThreads + wave * kWave);
+        };
+        auto load_scales = [&](int super) {
+            const uint32_t at = min(super, supers - 1) * 16;
 #pragma unroll
-        for (int f = 0; f < FR; ++f) xs[f] = xsw[buf * kRowsX * 4 + f * 64];
-    };
-    if (supers > 0) {
-        load_scales(0);
+            for (int i = 0; i < kScales; ++i) raw[i] = *reinterpret_cast<const u32x4_a1 *>(sp[i] + at);
+        };
+        auto keep_scales = [&](u32x4 *to) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) load(i, 0);
-        keep_scales(0);
+            for (int i = 0; i < kScales; ++i) to[sq[i]] = by_group(raw[i]);
+        };
+        i32x8 wf[2][NF], xf[FR];
+        uint32_t ws[NF], xs[FR];
+        // fragments of step i of 512 elements
+        auto read_w = [&](int i) {
+            const u32x4 *l = ring(i / kSub) + wfrag[i % kSub];
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) keep(i, 0);
+            for (int j = 0; j < NF; ++j) wf[i & 1][j] = join(l[j * 16 * kPw], l[j * 16 * kPw]);
+        };
+        auto read_x = [&](int i, int f) {
+            const u32x4 *l = ring(i / kSub) + kSizeW + f * 16 * kPx;
+            xf[f] = XF == 4 ? join(l[xfrag[i % kSub]], l[xfrag[i % kSub]]) : join(l[xfrag[0]], l[xfrag[1]]);
+        };
+        auto read_scales = [&](const u32x4 *from) {
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(from) + g;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) load(i, 1);
-        __syncthreads();
-        read_w(0);
-        read_x(0, 0);
-        read_x(0, 1);
-        read_scales(0);
-    }
-    for (int super = 0; super < supers; ++super) {
+            for (int j = 0; j < NF; ++j) ws[j] = p[(wn * kOwn + j * 16 + r) * 4];
+#pragma unroll
+            for (int f = 0; f < FR; ++f) xs[f] = p[(kRowsW + (wm * FR + f) * 16 + r) * 4];
+        };
+        if (supers > 0) {
+            load_scales(0);
+#pragma unroll
+            for (int i = 0; i < RING - 1; ++i) fetch(i, i);
+            __builtin_amdgcn_sched_barrier(0);
+            keep_scales(s0);
+            barrier_fetched<(RING - 2) * kLoads>();
+            fetch(RING - 1, RING - 1);
+            read_w(0);
+            read_x(0, 0);
+            read_x(0, 1);
+            read_scales(s0);
+        }
+        for (int super = 0; super < supers; ++super) {
 #define MOE_WIDE_STEP(I)                                                                              \
-        {                                                                                             \
-            constexpr int kStage = I / kSub, kGroups = (FR - 2) * kSub;                               \
-            if (I == 1) load_scales(super + 1);                                                       \
-            if (I == 3) keep_scales((super + 1) & 1);                                                 \
-            _Pragma("unroll") for (int f = 0; f < FR - 2; ++f) {                                      \
-                const int group = I % kSub * (FR - 2) + f;                                            \
-                read_x(I, f + 2);                                                                     \
-                _Pragma("unroll") for (int i = group * kLoads / kGroups; i < (group + 1) * kLoads / kGroups; ++i) { \
-                    keep(i, (kStage + 1) & 1);                                                        \
-                    load(i, super * kStages + kStage + 2);                                            \
+            {                                                                                         \
+                constexpr bool kEnd = I % kSub == kSub - 1;                                           \
+                if (I == 0) load_scales(super + 1);                                                   \
+                if (I == 3) keep_scales(s1);                                                          \
+                _Pragma("unroll") for (int f = 0; f < FR - 2; ++f) {                                  \
+                    read_x(I, f + 2);                                                                 \
+                    _Pragma("unroll") for (int j = 0; j < NF; ++j)                                    \
+                        acc[f][j] = mma<XF, I>(wf[I & 1][j], xf[f], acc[f][j], ws[j], xs[f]);         \
+                    __builtin_amdgcn_sched_barrier(0);                                                \
                 }                                                                                     \
-                _Pragma("unroll") for (int j = 0; j < NF; ++j)                                        \
-                    acc[f][j] = mma<XF, I>(wf[I & 1][j], xf[f], acc[f][j], ws[j], xs[f]);             \
+                if (kEnd) {                                                                           \
+                    barrier_fetched<(RING - 2) * kLoads>();                                           \
+                    __builtin_amdgcn_sched_barrier(0);                                                \
+                    fetch(super * kStages + I / kSub + RING, I / kSub);                               \
+                    __builtin_amdgcn_sched_barrier(0);                                                \
+                }                                                                                     \
+                read_w((I + 1) & 3);                                                                  \
+                read_x((I + 1) & 3, 0);                                                               \
+                read_x((I + 1) & 3, 1);                                                               \
                 __builtin_amdgcn_sched_barrier(0);                                                    \
-            }                                                                                         \
-            if (I % kSub == kSub - 1) __syncthreads();                                                \
-            __builtin_amdgcn_sched_barrier(0);                                                        \
-            read_w((I + 1) & 3);                                                                      \
-            read_x((I + 1) & 3, 0);                                                                   \
-            read_x((I + 1) & 3, 1);                                                                   \
-            __builtin_amdgcn_sched_barrier(0);                                                        \
-            _Pragma("unroll") for (int f = FR - 2; f < FR; ++f)                                       \
-                _Pragma("unroll") for (int j = 0; j < NF; ++j)                                        \
-                    acc[f][j] = mma<XF, I>(wf[I & 1][j], xf[f], acc[f][j], ws[j], xs[f]);             \
-            if (I == 3) read_scales((super + 1) & 1);                                                 \
-            __builtin_amdgcn_sched_barrier(0);                                                        \
-        }
-        MOE_WIDE_STEP(0)
-        MOE_WIDE_STEP(1)
-        MOE_WIDE_STEP(2)
-        MOE_WIDE_STEP(3)
+                _Pragma("unroll") for (int f = FR - 2; f < FR; ++f)                                   \
+                    _Pragma("unroll") for (int j = 0; j < NF; ++j)                                    \
+                        acc[f][j] = mma<XF, I>(wf[I & 1][j], xf[f], acc[f][j], ws[j], xs[f]);         \
+                if (I == 3) read_scales(s1);                                                          \
+                __builtin_amdgcn_sched_barrier(0);                                                    \
+            }
+            MOE_WIDE_STEP(0)
+            MOE_WIDE_STEP(1)
+            MOE_WIDE_STEP(2)
+            MOE_WIDE_STEP(3)
 #undef MOE_WIDE_STEP
-    }
-    // the last k % 512 elements, a step at a time
-    for (int at = supers * kSuper; at < a.k; at += kStep) {
-        __syncthreads();
-        constexpr int kTx = XF == 4 ? 4 : 8;                  // pieces of an input row in one step
-#pragma unroll 1
-        for (int c = tid; c < kRowsW * 4; c += kProductThreads)
-            wl[0][kSub == 2 ? place8(c / 4, c % 4) : place4(c / 4, c % 4)] =
-                load_piece_or_zero<4>(wb + weight_row(c / 4) * wrow + 16 * (c % 4), at, c % 4, a.k);
-#pragma unroll 1
-        for (int c = tid; c < kRowsX * kTx; c += kProductThreads)
-            xl[0][place8(c / kTx, c % kTx)] =
-                load_piece_or_zero<XF>(xb + (uint32_t)min(c / kTx, last) * xrow + 16 * (c % kTx), at, c % kTx, a.k);
-        const int b = at / kBlock;
-        u32x4 v;
-#pragma unroll
-        for (int j = 0; j < kScalesW; ++j) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = b + i < a.nb ? wsb[wso[j] + b + i] : 127;
-            wsl[0][tid + j * kProductThreads] = v;
         }
+        barrier_fetched<0>();
+        // the last k % 512 elements, a step at a time
+        for (int at = supers * kSuper; at < a.k; at += kStep) {
+            constexpr int kTx = XF == 4 ? 4 : 8;              // pieces of an input row in one step
+#pragma unroll 1
+            for (int c = tid; c < kRowsW * 4; c += kThreads)
+                l0[kPw == 8 ? place8(c / 4, c % 4) : place4(c / 4, c % 4)] =
+                    load_piece_or_zero<4>(wb + weight_row(c / 4) * wrow + 16 * (c % 4), at, c % 4, a.k);
+#pragma unroll 1
+            for (int c = tid; c < kRowsX * kTx; c += kThreads)
+                l0[kSizeW + (kPx == 8 ? place8(c / kTx, c % kTx) : place4(c / kTx, c % kTx))] =
+                    load_piece_or_zero<XF>(xb + (uint32_t)min(c / kTx, last) * xrow + 16 * (c % kTx), at, c % kTx, a.k);
+            const int b = at / kBlock;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = b + i < a.nb ? xsb[xso + b + i] : 127;
-        xsl[0][tid % kRowsX] = v;
-        __syncthreads();
-        read_w(0);
-        read_scales(0);
+            for (int j = 0; j < kScales; ++j) {
+                u32x4 v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = b + i < a.nb ? sp[j][b + i] : 127;
+                s0[sq[j]] = v;
+            }
+            __syncthreads();
+            read_w(0);
+            read_scales(s0);
+#pragma unroll
+            for (int f = 0; f < FR; ++f) {
+                read_x(0, f);
+#pragma unroll
+                for (int j = 0; j < NF; ++j) acc[f][j] = mma<XF, 0>(wf[0][j], xf[f], acc[f][j], ws[j], xs[f]);
+            }
+            __syncthreads();
+        }
 #pragma unroll
         for (int f = 0; f < FR; ++f) {
-            read_x(0, f);
+            const int row = tile.row + (wm * FR + f) * 16 + r;
+            if (row >= tile.end) continue;
 #pragma unroll
-            for (int j = 0; j < NF; ++j) acc[f][j] = mma<XF, 0>(wf[0][j], xf[f], acc[f][j], ws[j], xs[f]);
-        }
-    }
+            for (int j = 0; j < kOut; ++j) {
+                f32x4 v = acc[f][j];
+                if (GLU) {
 #pragma unroll
-    for (int f = 0; f < FR; ++f) {
-        const int row = tile.row + (wm * FR + f) * 16 + r;
-        if (row >= tile.end) continue;
-#pragma unroll
-        for (int j = 0; j < kOut; ++j) {
-            f32x4 v = acc[f][j];
-            if (GLU) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = swiglu(v[i], acc[f][j + kOut][i]);
+                    for (int i = 0; i < 4; ++i) v[i] = swiglu(v[i], acc[f][j + kOut][i]);
+                }
+                const int col = tile0 + (wn * kOut + j) * 16 + 4 * g;
+                if (col < a.fo) store_out<T>(a, row, col, v);
             }
-            const int col = tile0 + (wn * kOut + j) * 16 + 4 * g;
-            if (col < a.fo) store_out<T>(a, row, col, v);
         }
-    }
-    __syncthreads();
     }
 }
 
@@ -845,8 +722,8 @@ int moe_expert_product(const void *x, const uint8_t *x_scales, int element, cons
     if ((long long)n * k > 4ll << 30 || k > 1 << 24) return MOE_ERR_SHAPE;
     const int each = rows / a.E;                // rows of an expert, were they even
     // rows and columns of a tile
-    const int tall = each <= 8 ? 16 : (each <= 40 ? 64 : (each <= 150 ? 128 : 192));
-    const int cols = (tall == 16 ? kFrags * 16 : 256) / (glu ? 2 : 1);
+    const int tall = each <= 40 ? 64 : (each <= 150 ? 128 : 256);
+    const int cols = (tall == 64 ? 128 : 256) / (glu ? 2 : 1);
     a.ntiles = (a.fo + cols - 1) / cols;
     // a tile starts at every expert's first row, so at most this many
     const long long mtiles = rows / tall + std::min(a.E, rows);
@@ -861,15 +738,14 @@ int moe_expert_product(const void *x, const uint8_t *x_scales, int element, cons
     a.ws = weight_scales;
     a.erc = ep_recv_count;
     a.out = out;
-    const dim3 g((unsigned)std::min<long long>(mtiles * a.ntiles, kWorkgroups)), b(kProductThreads);
+    const dim3 g((unsigned)std::min<long long>(mtiles * a.ntiles, kWorkgroups)), b(tall == 256 ? 512 : 256);
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
 #define MOE_PRODUCT_G(T, XF, G)                                                                       \
     do {                                                                                              \
-        if (tall == 16) hipLaunchKernelGGL((expert_product_kernel<T, XF, 1, G>), g, b, 0, st, a);     \
-        else if (tall == 64) hipLaunchKernelGGL((expert_product_wide_kernel<T, XF, 4, 4, 1, G>), g, b, 0, st, a); \
-        else if (tall == 128) hipLaunchKernelGGL((expert_product_wide_kernel<T, XF, 4, 8, 2, G>), g, b, 0, st, a); \
-        else hipLaunchKernelGGL((expert_product_wide_kernel<T, XF, 6, 8, 2, G>), g, b, 0, st, a);     \
+        if (tall == 64) hipLaunchKernelGGL((expert_product_kernel<T, XF, 4, 2, 1, 4, 1, 4, G>), g, b, 0, st, a); \
+        else if (tall == 128) hipLaunchKernelGGL((expert_product_kernel<T, XF, 8, 4, 1, 4, 1, 2, G>), g, b, 0, st, a); \
+        else hipLaunchKernelGGL((expert_product_kernel<T, XF, 8, 4, 2, 4, 2, 2, G>), g, b, 0, st, a); \
     } while (0)
 #define MOE_PRODUCT(T, XF)                                                                            \
     do {                                                                                              \
