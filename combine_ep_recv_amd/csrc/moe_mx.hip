@@ -360,11 +360,19 @@ __device__ __forceinline__ float swiglu(float gate, float up)
     return gate * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(gate * -1.44269504f)) * up;
 }
 
-// 16 bytes a lane from device memory into LDS, the wavefront's 1 KiB one after the other from `to`, past the registers.
-__device__ __forceinline__ void fetch_lds(const uint8_t *from, u32x4 *to)
+// A buffer of `bytes` from `base` on (the same in all lanes); reads past it give zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t *base, uint64_t bytes)
 {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
-                                     (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+    const int size = (int)(bytes < 0xffffffffull ? (uint32_t)bytes : 0xffffffffu);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), 0, size, 0x00027000);
+}
+// 16 bytes a lane from `buffer`, `lane` + `all` bytes in, to LDS, the wavefront's 1 KiB one after the other from `to`,
+// past the registers. (A buffer load: the compiler takes a global load of this kind for one that may count as an LDS
+// access too, and then waits for every LDS read at the first.)
+__device__ __forceinline__ void fetch_lds(__amdgpu_buffer_rsrc_t buffer, uint32_t lane, uint32_t all, u32x4 *to)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer, (__attribute__((address_space(3))) void *)to, 16, (int)lane, (int)all,
+                                             0, 0);
 }
 // A barrier behind which every wavefront's LDS reads and writes, and all but its youngest LEFT fetches into LDS, are
 // done. (The wait is the builtin: the compiler then knows which fetches are in and puts no wait of its own before the
@@ -436,6 +444,8 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
         const int tile0 = t % a.ntiles * (WN * kOut * 16);
         const uint8_t *wb = a.w + (size_t)tile.expert * a.n * wrow, *wsb = a.ws + (size_t)tile.expert * a.n * a.nb;
         const uint8_t *xb = a.x + (size_t)tile.row * xrow, *xsb = a.xs + (size_t)tile.row * a.nb;
+        const __amdgpu_buffer_rsrc_t wbuf = buffer_of(wb, (uint64_t)a.n * wrow);
+        const __amdgpu_buffer_rsrc_t xbuf = buffer_of(xb, (uint64_t)(tile.end - tile.row) * xrow);
         const int last = tile.end - 1 - tile.row;             // rows past the expert's last read the last one
         // weight row of a place in the tile; columns past the last one read the last one's, and are not stored
         auto weight_row = [&](int q) -> uint32_t {
@@ -469,9 +479,9 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
             const uint32_t at = min(stage, stages - 1);
             u32x4 *wl = ring(slot), *xl = wl + kSizeW;
 #pragma unroll
-            for (int i = 0; i < kLoadsW; ++i) fetch_lds(wb + (wo[i] + at * (16 * kPw)), wl + i * kThreads + wave * kWave);
+            for (int i = 0; i < kLoadsW; ++i) fetch_lds(wbuf, wo[i], at * (16 * kPw), wl + i * kThreads + wave * kWave);
 #pragma unroll
-            for (int i = 0; i < kLoadsX; ++i) fetch_lds(xb + (xo[i] + at * (16 * kPx)), xl + i * kThreads + wave * kWave);
+            for (int i = 0; i < kLoadsX; ++i) fetch_lds(xbuf, xo[i], at * (16 * kPx), xl + i * kThreads + wave * kWave);
         };
         auto load_scales = [&](int super) {
             const uint32_t at = min(super, supers - 1) * 16;
@@ -581,7 +591,8 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
         }
         // Results leave by way of LDS, 16 rows of the wavefront's columns at a time, so that neighbouring lanes store
         // neighbouring 16 bytes: a lane's own four columns are 8 bytes 16 lanes from the next ones, each a look-up of
-        // its own in the cache. (16 x 256 tokens, 2048 -> 7168: 530 us, 560 with 8-byte stores.)
+        // its own in the cache. (16 ranks of 256 tokens,
+        // 2048 -> 7168: 530 us, 560 with 8-byte stores; 515 since the stores pass the cache by.)
         constexpr int kPitch = kOut * 32 + 16;                // bytes; 16 more than the columns, to spread the banks
         constexpr int kLanes = kOut * 2;                      // lanes of a row
         char *own = reinterpret_cast<char *>(l0) + wave * 16 * kPitch;
@@ -609,7 +620,7 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
                 const u32x4 v = *reinterpret_cast<const u32x4 *>(own + q / kLanes * kPitch + q % kLanes * 16);
                 typename T::raw *out = static_cast<typename T::raw *>(a.out) + (size_t)row * a.fo + col;
                 if (col + 8 <= a.fo) {
-                    *reinterpret_cast<u32x4_a2 *>(out) = v;
+                    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2 *>(out));
                 } else {
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
@@ -618,6 +629,19 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
             }
         }
     }
+}
+
+// Rows of a tile, for `each` rows an expert. A tile of 64 rows keeps three stages of weights on their way and pads
+// few rows; above 48 rows an expert it would read the weights a second time, through the cache, and do too little on
+// what it read. Measured with 64 experts, 7168 -> 4096 with SwiGLU, 32 / 48 / 64 rows each: E4M3 225 / 256 / 301 us
+// with 64 rows, 279 / 287 / 292 with 128; E2M1 with 48 and 96 rows each 244 and 328 with 64, 227 and 240 with 128. Of
+// E2M1, 256 rows pay where the second half is more than an eighth full: 300 us and 312 with 128 rows each, 313 and 383
+// with 192, 684 and 769 with 512 (2048 -> 7168: 193 and 181, 209 and 243, 451 and 495). E4M3's fragments do not fit the
+// registers at that height (512 rows each: 1110 us, and 1090 with 128).
+int tile_rows(int each, int element)
+{
+    if (each <= 48) return 64;
+    return element == MOE_MX_E2M1 && each > 144 ? 256 : 128;
 }
 
 int check_mx(long long rows, int cols, int dtype, int element)
@@ -729,7 +753,7 @@ int moe_expert_product(const void *x, const uint8_t *x_scales, int element, cons
     if ((long long)n * k > 4ll << 30 || k > 1 << 24) return MOE_ERR_SHAPE;
     const int each = rows / a.E;                // rows of an expert, were they even
     // rows and columns of a tile
-    const int tall = each <= 40 ? 64 : (each <= 150 ? 128 : 256);
+    const int tall = tile_rows(each, element);
     const int cols = (tall == 64 ? 128 : 256) / (glu ? 2 : 1);
     a.ntiles = (a.fo + cols - 1) / cols;
     // a tile starts at every expert's first row, so at most this many
@@ -745,14 +769,15 @@ int moe_expert_product(const void *x, const uint8_t *x_scales, int element, cons
     a.ws = weight_scales;
     a.erc = ep_recv_count;
     a.out = out;
-    const dim3 g((unsigned)std::min<long long>(mtiles * a.ntiles, kWorkgroups)), b(tall == 256 ? 512 : 256);
+    const dim3 g((unsigned)std::min<long long>(mtiles * a.ntiles, kWorkgroups)), b(tall == 64 ? 256 : 512);
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
 #define MOE_PRODUCT_G(T, XF, G)                                                                       \
     do {                                                                                              \
         if (tall == 64) hipLaunchKernelGGL((expert_product_kernel<T, XF, 4, 2, 1, 4, 1, 4, G>), g, b, 0, st, a); \
-        else if (tall == 128) hipLaunchKernelGGL((expert_product_kernel<T, XF, 8, 4, 1, 4, 1, 2, G>), g, b, 0, st, a); \
-        else hipLaunchKernelGGL((expert_product_kernel<T, XF, 8, 4, 2, 4, 2, 2, G>), g, b, 0, st, a); \
+        else if (XF == 4 && tall == 256)                                                              \
+            hipLaunchKernelGGL((expert_product_kernel<T, 4, 8, 4, 2, 4, 2, 2, G>), g, b, 0, st, a);   \
+        else hipLaunchKernelGGL((expert_product_kernel<T, XF, 4, 4, 2, 4, 2, 2, G>), g, b, 0, st, a); \
     } while (0)
 #define MOE_PRODUCT(T, XF)                                                                            \
     do {                                                                                              \
