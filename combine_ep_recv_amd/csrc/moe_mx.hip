@@ -20,7 +20,7 @@ using namespace moe_detail;
 constexpr int kBlock = 32;                 // elements that share a scale byte
 constexpr int kPiece = 16;                 // elements a lane quantises: half a block
 constexpr int kMxThreads = 256;
-constexpr long long kMaxRows = (1ll << 31) - 1;
+constexpr long long kMaxBlocks = (1ll << 31) - kMxThreads / 2;      // two lanes a block: a launch has below 2^32 lanes
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -74,15 +74,15 @@ __device__ __forceinline__ void load_piece(const void *in, long long piece, floa
 template <class T, int E, bool RAGGED>
 __global__ __launch_bounds__(kMxThreads) void quantize_kernel(MxArgs a)
 {
-    const long long lane_piece = (long long)blockIdx.x * kMxThreads + threadIdx.x;
+    const uint32_t lane_piece = blockIdx.x * kMxThreads + threadIdx.x;
     // RAGGED: the grid counts two pieces for every block, and the half that a row's last block lacks is empty
     long long row = 0, piece = lane_piece;
     bool live;
     if (RAGGED) {
-        row = lane_piece / (2 * a.blocks);
-        const int q = (int)(lane_piece - row * (2 * a.blocks));
+        const uint32_t r = lane_piece / (2u * a.blocks), q = lane_piece - r * (2u * a.blocks);
+        row = r;
         piece = row * a.per_row + q;
-        live = piece < a.pieces && q < a.per_row;
+        live = piece < a.pieces && q < (uint32_t)a.per_row;
     } else {
         live = piece < a.pieces;
     }
@@ -145,12 +145,13 @@ __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_floa
 template <class T, int E, bool RAGGED>
 __global__ __launch_bounds__(kMxThreads) void dequantize_kernel(MxArgs a)
 {
-    const long long piece = (long long)blockIdx.x * kMxThreads + threadIdx.x;
+    const uint32_t lane_piece = blockIdx.x * kMxThreads + threadIdx.x;
+    const long long piece = lane_piece;
     if (piece >= a.pieces) return;
     long long block = piece / 2;
     if (RAGGED) {
-        const long long row = piece / a.per_row;
-        block = row * a.blocks + (piece - row * a.per_row) / 2;
+        const uint32_t row = lane_piece / (uint32_t)a.per_row;
+        block = (long long)row * a.blocks + (lane_piece - row * a.per_row) / 2;
     }
     const float s = scale_of(a.scales_in[block]);
     float x[kPiece];
@@ -646,11 +647,10 @@ int tile_rows(int each, int element)
 
 int check_mx(long long rows, int cols, int dtype, int element)
 {
-    if (rows < 0 || rows > kMaxRows || cols < kPiece || cols % kPiece) return MOE_ERR_SHAPE;
+    if (rows < 0 || cols < kPiece || cols % kPiece) return MOE_ERR_SHAPE;
     if (dtype != MOE_FP16 && dtype != MOE_BF16 && dtype != MOE_FP32) return MOE_ERR_DTYPE;
     if (element != MOE_MX_E2M1 && element != MOE_MX_E4M3) return MOE_ERR_QUANT;
-    // two pieces a block, one piece a thread
-    if (rows * ((cols + kBlock - 1) / kBlock) > (long long)INT_MAX * (kMxThreads / 2)) return MOE_ERR_SHAPE;
+    if (rows > kMaxBlocks / ((cols + kBlock - 1) / kBlock)) return MOE_ERR_SHAPE;
     return MOE_OK;
 }
 
@@ -758,7 +758,8 @@ int moe_expert_product(const void *x, const uint8_t *x_scales, int element, cons
     a.ntiles = (a.fo + cols - 1) / cols;
     // a tile starts at every expert's first row, so at most this many
     const long long mtiles = rows / tall + std::min(a.E, rows);
-    if (mtiles * a.ntiles > INT_MAX) return MOE_ERR_SHAPE;
+    // rows and tiles are counted past the last one by up to a tile's height and a stride of the grid
+    if (rows > INT_MAX - 256 || mtiles * a.ntiles > INT_MAX - kWorkgroups) return MOE_ERR_SHAPE;
     if (rows == 0) return MOE_OK;
     if (!x || !x_scales || !weights || !weight_scales || !ep_recv_count || !out) return MOE_ERR_NULLPTR;
     if (!aligned(x, 16) || !aligned(weights, 16) || !aligned(ep_recv_count, 4) || !aligned(out, 2))

@@ -388,7 +388,7 @@ enum moe_mx_element { MOE_MX_E2M1 = 0, MOE_MX_E4M3 = 1 };
  *  x       [rows, cols], 16-byte aligned
  *  codes   [rows, cols / 2] (E2M1) or [rows, cols] (E4M3) bytes, 16-byte aligned
  *  scales  uint8 [rows, ceil(cols / 32)], E8M0 bytes shared + 127
- * cols is a multiple of 16; rows * ceil(cols / 32) <= 2^38 - 128.
+ * cols is a multiple of 16; rows * ceil(cols / 32) <= 2^31 - 128.
  */
 int moe_mx_quantize(const void *x, int64_t rows, int cols, int dtype, int element, void *codes, uint8_t *scales,
                     void *stream);
@@ -413,7 +413,8 @@ enum moe_activation { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 };
  *  out           [rows, n], or [rows, n / 2] with MOE_ACT_SWIGLU, fp16 or bf16 (dtype). Rows behind the last that
  *                ep_recv_count counts are left as they were
  * A scale byte of 255 makes every result of its row NaN.
- * Ranges: ep_world and experts as in moe_dispatch, rows >= 0, k a multiple of 16, n >= 1 (even with SwiGLU). Counts
+ * Ranges: ep_world and experts as in moe_dispatch, 0 <= rows < 2^31 - 256, k a multiple of 16 up to 2^24, n >= 1
+ * (even with SwiGLU), n * k <= 2^32, (rows / 64 + E) * ceil(n / 64) < 2^31 - 1024 (MOE_ERR_SHAPE otherwise). Counts
  * that ep_recv_count should not hold (negative, descending, beyond rows) leave the kernel in bounds and the outputs
  * unspecified. Needs no workspace.
  */

@@ -110,7 +110,8 @@ def P(v):
 @pytest.mark.parametrize("kw,want", [
     (dict(rows=-1), moe.MOE_ERR_SHAPE), (dict(cols=8), moe.MOE_ERR_SHAPE), (dict(cols=40), moe.MOE_ERR_SHAPE),
     (dict(cols=0), moe.MOE_ERR_SHAPE), (dict(dtype=0), moe.MOE_ERR_DTYPE), (dict(element=2), moe.MOE_ERR_QUANT),
-    (dict(rows=(1 << 31) - 1, cols=1 << 13), moe.MOE_ERR_SHAPE),
+    (dict(rows=(1 << 31) - 1, cols=1 << 13), moe.MOE_ERR_SHAPE), (dict(rows=(1 << 31) - 127, cols=16), moe.MOE_ERR_SHAPE),
+    (dict(rows=(1 << 30) - 63, cols=48), moe.MOE_ERR_SHAPE), (dict(rows=(1 << 62), cols=64), moe.MOE_ERR_SHAPE),
     (dict(x=None), moe.MOE_ERR_NULLPTR), (dict(codes=None), moe.MOE_ERR_NULLPTR), (dict(scales=None), moe.MOE_ERR_NULLPTR),
     (dict(x=A + 8), moe.MOE_ERR_ALIGN), (dict(codes=A + 8), moe.MOE_ERR_ALIGN),
     (dict(rows=0, x=None, codes=None, scales=None), moe.MOE_OK),
@@ -131,6 +132,8 @@ def test_mx_calls_refuse_before_a_launch(kw, want):
     (dict(k=72), moe.MOE_ERR_SHAPE), (dict(n=0), moe.MOE_ERR_SHAPE), (dict(act=1, n=7), moe.MOE_ERR_SHAPE),
     (dict(act=2), moe.MOE_ERR_SHAPE), (dict(element=2), moe.MOE_ERR_QUANT), (dict(dtype=0), moe.MOE_ERR_DTYPE),
     (dict(dtype=3), moe.MOE_ERR_DTYPE), (dict(rows=1 << 30, n=1 << 20), moe.MOE_ERR_SHAPE),
+    (dict(rows=(1 << 31) - 200, n=2), moe.MOE_ERR_SHAPE), (dict(k=(1 << 24) + 16, n=1), moe.MOE_ERR_SHAPE),
+    (dict(k=1 << 20, n=(1 << 12) + 1), moe.MOE_ERR_SHAPE),
     (dict(x=None), moe.MOE_ERR_NULLPTR), (dict(xs=None), moe.MOE_ERR_NULLPTR), (dict(w=None), moe.MOE_ERR_NULLPTR),
     (dict(ws=None), moe.MOE_ERR_NULLPTR), (dict(erc=None), moe.MOE_ERR_NULLPTR), (dict(out=None), moe.MOE_ERR_NULLPTR),
     (dict(x=A + 8), moe.MOE_ERR_ALIGN), (dict(w=A + 4), moe.MOE_ERR_ALIGN), (dict(erc=A + 2), moe.MOE_ERR_ALIGN),
@@ -416,6 +419,16 @@ def test_product_shapes(element, act, k, n):
                          ids=lambda v: str(v) if isinstance(v, int) else "%d experts %d rows" % (len(v), sum(v)))
 def test_product_rows_per_expert(element, per_expert, W):
     check_product(per_expert, W, 160, 40, element, seed=len(per_expert), spare=1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("element", [E2M1, E4M3])
+@pytest.mark.parametrize("per_expert,n,act", [([(17 * e) % 90 for e in range(1024)], 34, SWIGLU), ([260, 0] * 120, 514, NONE),
+                                              ([50000, 44000], 514, NONE)],
+                         ids=["few rows", "some rows", "many rows"])
+def test_product_of_more_tiles_than_workgroups(element, per_expert, n, act):
+    """A workgroup that goes from tile to tile, of other experts and columns, with whole stages of k and a rest."""
+    check_product(per_expert, 2, 528, n, element, act, seed=n, spare=3, spread=2)
 
 
 @pytest.mark.gpu
