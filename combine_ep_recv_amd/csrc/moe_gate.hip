@@ -86,8 +86,8 @@ __device__ __attribute__((noinline)) double exponential(float x, float y) { retu
 
 // The choice for one token from binary64 scores, by a whole wavefront: lane k gets pair k's id. Rare (see
 // gate_kernel), so it trades time for registers: the scores lie in LDS (v[experts], this wavefront's), the logits are
-// read again (v holds them first). `bias` is LDS too, zeros where there is none. Not inlined: the constants of binary64's exponential would be kept in registers through gate_kernel's
-// loop. Every argument is the same in all lanes.
+// read again (v holds them first). `bias` is LDS too, zeros where there is none. Not inlined: the constants of binary64's
+// exponential would be kept in registers through gate_kernel's loop. Every argument is the same in all lanes.
 template <class T, int SCORE>
 __device__ __attribute__((noinline)) int choose_exactly(const typename T::raw *row_, lds_float *bias, int biased_, lds_double *v,
                                                         int experts_, int topk_, int groups_, int topk_groups_,
@@ -189,10 +189,22 @@ __device__ __attribute__((noinline)) int choose_exactly(const typename T::raw *r
 //
 // Two experts' order may hang on the last bits of their scores, and has to come out as in binary64, whose
 // exponentials cost about ten times fp32's. So the choice is made on fp32 scores, and made again on binary64 ones
-// only where two neighbours in it, or the last one and the best left out, are closer than the fp32 scores may be off:
-// exp2 of a rounded product (2 |x| 2^-24 relative, where x e^x <= 0.4, and an ulp), a sum of PER + 6 terms in a row,
-// a reciprocal, a product: below (PER + 20) 2^-24 of the largest score, and half an ulp of the choice for the bias.
+// only where two neighbours in it, or the last one and the best left out, are closer than the fp32 scores may be off
+// (u = 2^-24; the hardware's exp2 and reciprocal are off by 2 u). One such token costs 5.5 us, and the last one of a
+// launch is waited for, so the bound is worth its care.
+//   softmax  two exponentials, each off by 2.25 |x| u (a difference, a product, its constant) and 2 u, where
+//            |x| e^x <= 0.37: 5.7 u of the largest score. The sum is the same for both: the difference of two scores
+//            shares its error, PER / 4 + 7 u for adding, 2 u and 2.25 |x| u, |x| averaged over the sum and so
+//            at most 3.6 for 320 experts and 5.1 for 2048, and 2 u for its reciprocal. Below (PER / 4 + 32) u together.
+//   sigmoid  1.25 |x| s (1 - s) u <= 0.3 u, half of exp2's u (s (1 - s) <= 1/4), u of the sum and 2 u of the
+//            reciprocal: below 4 u each.
+// Either way half an ulp of each choice for its sum with the bias.
 // Without a bias the logits themselves are compared, which needs neither.
+//
+// What bounds it: vector instructions and their order, not memory. 65521 tokens of 304 experts (bf16, softmax, bias,
+// 8 picks, a quarter of the tokens masked) take 47 us, 40 without the last binary64 look, for 31 MB of logits (5 us);
+// the vector units are busy for 32 of them (1200 instructions for four tokens, with every list and pick). 4096 tokens
+// of 256 experts in 8 groups take 12, 8.5 without that look; 8 tokens take 8, 3.5 of them on the card.
 template <class T, int LANES, int PER, int WAVES, int SCORE>
 __global__ __launch_bounds__(WAVES *kWave, LANES == 16 ? 4 : (PER <= 5 ? 5 : 1)) void gate_kernel(GateArgs a)
 {
@@ -237,19 +249,19 @@ __global__ __launch_bounds__(WAVES *kWave, LANES == 16 ? 4 : (PER <= 5 ? 5 : 1))
         for (int j = 0; j < PER; ++j) c[j] = l[j];
         bool safe = true;
         if (SCORE == MOE_SCORE_SOFTMAX) {
-            float sum = 0.f;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};          // four sums: short ones are off by less
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 c[j] = __builtin_amdgcn_exp2f((l[j] - top) * log2e);
-                sum += c[j];
+                sum[j % 4] += c[j];
             }
-            inv = best = __builtin_amdgcn_rcpf(wave_sum<LANES>(sum));
+            inv = best = __builtin_amdgcn_rcpf(wave_sum<LANES>((sum[0] + sum[1]) + (sum[2] + sum[3])));
             safe = top < INFINITY;                        // logits of +infinity: NaN above
         } else if (by_score) {
 #pragma unroll
             for (int j = 0; j < PER; ++j) c[j] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l[j] * -log2e));
         }
-        const float room = (PER + 24) * 0x1p-23f * best + 0x1p-100f;
+        const float room = (SCORE == MOE_SCORE_SIGMOID ? 8 : PER / 4 + 32) * 0x1p-24f * best + 0x1p-100f;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
             const float b = bias[j * LANES + sub], s = by_score ? __builtin_fmaf(c[j], inv, b) : l[j];
@@ -416,6 +428,8 @@ struct GateGradArgs {
 // One wavefront per token. Lane k takes pair k; the pairs' gradients meet the experts in an LDS row, from which each lane
 // writes its experts', VEC neighbouring ones at a time (two where rows of 16-bit logits start at 4 bytes: half as many
 // loads and stores). The row of logits, where every expert needs its score, is on its way before anything else.
+// Memory bounds long calls: 65521 tokens of 304 experts in bf16 with a gradient for every logit take 18 us, 4.2 TB/s of
+// 76 MB; 4096 tokens of 256 experts in fp32 take 3.3 us on the card, and 9 with the call.
 template <class T, int PER, int VEC, int WAVES, int SCORE, bool RENORM>
 __global__ __launch_bounds__(WAVES *kWave) void gate_backward_kernel(GateGradArgs a)
 {
