@@ -499,3 +499,21 @@ def test_gate_of_long_batches_on_the_last_bits(score):
     ids, w = moe.gate(L.to(DEV), 8, score, bias=b.to(DEV))
     check(L[:40], ids[:40], w[:40], bias=b, score=score)
     assert (ids[1::2] == ids[1]).all() and (w[1::2] == w[1]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("N,E", [(300, 64), (2100, 64), (300, 300), (9700, 300), (200, 1500)])
+@pytest.mark.parametrize("spread", [3e-7, 3e-6, 3e-5])
+def test_gate_choices_about_as_far_apart_as_fp32_can_tell(score, N, E, spread):
+    """Tokens whose choices lie around the distance below which fp32 scores are not trusted, on either side of it, with
+    scores that differ much under biases that level them: the order is that of binary64 for every token."""
+    g = torch.Generator().manual_seed(E)
+    base = 2 * torch.randn(E, generator=g)
+    b = torch.from_numpy((0.5 - scores(base.numpy(), score)[0]).astype(np.float32))
+    L = base * (1 + spread * torch.randn((N, E), generator=g))
+    at = torch.randperm(N, generator=g)[:200]
+    for groups, kind in ((1, moe.MOE_GROUP_MAX), (4, moe.MOE_GROUP_MAX), (4, moe.MOE_GROUP_TOP2)):
+        kw = dict(score=score, groups=groups, topk_groups=(groups + 1) // 2, group_score=kind)
+        ids, w = moe.gate(L.to(DEV), 8, bias=b.to(DEV), **kw)
+        check(L[at], ids[at.to(DEV)], w[at.to(DEV)], bias=b, **kw)
