@@ -12,6 +12,7 @@
 #include <limits.h>
 
 #include <algorithm>
+#include <type_traits>
 
 namespace {
 
@@ -44,22 +45,24 @@ struct MxArgs {
     int per_row, blocks;       // pieces and blocks of a row
 };
 
-// 16 elements of T from `p` (16-byte aligned: a row is a multiple of 16 elements)
-template <class T>
+constexpr long long kOnceBytes = 256ll << 20;      // the Infinity Cache
+
+// 16 elements of T (16-byte aligned: a row is a multiple of 16 elements)
+template <class T, bool ONCE>
 __device__ __forceinline__ void load_piece(const void *in, long long piece, float (&x)[kPiece])
 {
     const u32x4 *p = reinterpret_cast<const u32x4 *>(static_cast<const typename T::raw *>(in) + piece * kPiece);
     if constexpr (sizeof(typename T::raw) == 4) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const u32x4 v = p[i];
+            const u32x4 v = ONCE ? __builtin_nontemporal_load(p + i) : p[i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) x[4 * i + j] = __uint_as_float(v[j]);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const u32x4 v = p[i];
+            const u32x4 v = ONCE ? __builtin_nontemporal_load(p + i) : p[i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 x[8 * i + 2 * j] = T::load((uint16_t)(v[j] & 0xffff));
@@ -70,13 +73,13 @@ __device__ __forceinline__ void load_piece(const void *in, long long piece, floa
 }
 
 // A lane takes 16 elements and its neighbour the block's other half; a row with a last block of 16 leaves that
-// block to one lane. E: MOE_MX_E2M1 or MOE_MX_E4M3.
+// block to one lane. E: MOE_MX_E2M1 or MOE_MX_E4M3. ONCE: the input passes the caches by.
 //
 // Memory bounds it: 2 bytes in and about half a byte (E2M1) or one (E4M3) out, an element, against some ten
 // instructions. Loads of 32 bytes a lane are whole lines between neighbours, the shared exponent is one exchange of
-// neighbours away, and nothing passes through LDS. bf16 [32768, 7168] to E2M1 and back to bf16 takes 219 us, 5.4 TB/s
+// neighbours away, and nothing passes through LDS. bf16 [32768, 7168] to E2M1 and back to bf16 takes 202 us, 5.9 TB/s
 // of its 1.19 GB (a large copy reaches 5.2); [256, 7168] is the two calls' launches, 18.7 us.
-template <class T, int E, bool RAGGED>
+template <class T, int E, bool RAGGED, bool ONCE>
 __global__ __launch_bounds__(kMxThreads) void quantize_kernel(MxArgs a)
 {
     const uint32_t lane_piece = blockIdx.x * kMxThreads + threadIdx.x;
@@ -94,7 +97,7 @@ __global__ __launch_bounds__(kMxThreads) void quantize_kernel(MxArgs a)
     float x[kPiece];
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) x[i] = 0.f;
-    if (live) load_piece<T>(a.in, piece, x);
+    if (live) load_piece<T, ONCE>(a.in, piece, x);
     // the largest magnitude as bits: ordered like the values, and infinity and NaN above them all
     uint32_t top = 0;
 #pragma unroll
@@ -701,16 +704,29 @@ int moe_mx_quantize(const void *x, int64_t rows, int cols, int dtype, int elemen
     a.per_row = cols / kPiece;
     a.blocks = (cols + kBlock - 1) / kBlock;
     a.pieces = rows * a.per_row;
+    // An input that fills the Infinity Cache passes it by, which leaves the cache to the codes: bf16 [32768, 7168]
+    // to E2M1 and back 202 us, 220 otherwise; [65536, 2048] to E4M3 64 us and 70. A smaller one may lie in it, fresh
+    // from the kernel before: [32768, 2048] to E2M1 30 us past the cache, 28 through it.
+    const bool once = rows * cols * (dtype == MOE_FP32 ? 4 : 2) >= kOnceBytes;
     const bool ragged = cols % kBlock != 0;
     const dim3 g((unsigned)((2 * rows * a.blocks + kMxThreads - 1) / kMxThreads)), b(kMxThreads);
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
     by_type(dtype, [&](auto type) {
         using T = decltype(type);
-        if (element == MOE_MX_E2M1 && ragged) hipLaunchKernelGGL((quantize_kernel<T, MOE_MX_E2M1, true>), g, b, 0, st, a);
-        else if (element == MOE_MX_E2M1) hipLaunchKernelGGL((quantize_kernel<T, MOE_MX_E2M1, false>), g, b, 0, st, a);
-        else if (ragged) hipLaunchKernelGGL((quantize_kernel<T, MOE_MX_E4M3, true>), g, b, 0, st, a);
-        else hipLaunchKernelGGL((quantize_kernel<T, MOE_MX_E4M3, false>), g, b, 0, st, a);
+        auto launch = [&](auto e, auto half) {
+            constexpr int kE = decltype(e)::value;
+            constexpr bool kRagged = decltype(half)::value;
+            if (once) hipLaunchKernelGGL((quantize_kernel<T, kE, kRagged, true>), g, b, 0, st, a);
+            else hipLaunchKernelGGL((quantize_kernel<T, kE, kRagged, false>), g, b, 0, st, a);
+        };
+        using std::integral_constant;
+        using Four = integral_constant<int, MOE_MX_E2M1>;
+        using Eight = integral_constant<int, MOE_MX_E4M3>;
+        if (element == MOE_MX_E2M1 && ragged) launch(Four(), std::true_type());
+        else if (element == MOE_MX_E2M1) launch(Four(), std::false_type());
+        else if (ragged) launch(Eight(), std::true_type());
+        else launch(Eight(), std::false_type());
     });
     return launched();
 }

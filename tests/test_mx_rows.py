@@ -317,6 +317,19 @@ def test_dequantize_takes_every_code_and_scale(element, cols):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("element", [E2M1, E4M3])
+@pytest.mark.parametrize("dtype,rows,cols", [(torch.float32, 65537, 1024), (torch.bfloat16, 70001, 1936)], ids=str)
+def test_quantize_of_more_than_the_caches_hold(element, dtype, rows, cols):
+    """Codes and scales of a long input are those of its parts."""
+    x = torch.randn(rows, cols, device=DEV, generator=torch.Generator(DEV).manual_seed(1)).to(dtype)
+    codes, scales = moe.quantize_mx(x, element)
+    for at in range(0, rows, 20000):
+        c, s = moe.quantize_mx(x[at:at + 20000], element)
+        assert torch.equal(codes[at:at + 20000].view(torch.uint8), c.view(torch.uint8))
+        assert torch.equal(scales[at:at + 20000], s)
+
+
+@pytest.mark.gpu
 def test_quantize_leaves_the_neighbours_alone():
     for element, per in ((E2M1, 2), (E4M3, 1)):
         for rows, cols in ((3, 16), (5, 80), (1, 48)):
