@@ -480,6 +480,37 @@ def test_product_is_exact_on_small_whole_numbers(element, k, rows):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("element", [E2M1, E4M3])
+@pytest.mark.parametrize("k", [48, 1040])
+def test_product_takes_every_scale(element, k):
+    """Every pair of a row's scale byte and one of a few weights': the powers add up, however far apart they are. Codes
+    are 1 and 2, so that results are whole numbers times one power."""
+    rng = np.random.default_rng(k)
+    rows, n, W = 255, 40, 2
+    one, two = (2, 4) if element == E2M1 else (56, 64)
+    x = np.where(rng.integers(0, 2, (rows, k)) > 0, one, two).astype(np.uint8)
+    w = np.where(rng.integers(0, 2, (2, n, k)) > 0, 2, 4).astype(np.uint8)
+    nb = -(-k // 32)
+    xs = np.repeat(np.arange(255)[:, None], nb, 1).astype(np.uint8)
+    ints = values(x, np.full((rows, nb), 127, np.uint8), element) @ values(w[1], np.full((n, nb), 127, np.uint8), E2M1).T
+    for byte in (0, 1, 40, 127, 200, 254):
+        ws = np.full((2, n, nb), byte, np.uint8)
+        counts = counts_for([0, rows], W, 3)
+        got = moe.expert_product(*on_gpu(x, xs, w, ws, counts, element)).cpu().double().numpy()
+        for r in range(rows):
+            power = r + byte - 254
+            want = torch.from_numpy(np.ldexp(ints[r], power)).to(torch.bfloat16).double().numpy()
+            if power >= -126:                          # products of normal size: one rounding, infinity past the top
+                assert np.array_equal(got[r], want), (byte, r, got[r][:3], want[:3])
+            else:
+                # What is smaller may be taken for zero. If it is not: bf16's step below 2^-126 is 2^-133, so that its
+                # rounding adds up to 2^-134 (and 2^-9 of what is larger); fp32's is 2^-149, and at most k half steps
+                # of it, below 2^-139, are added before.
+                limit = np.ldexp(ints[r], power) * (1 + 2.0 ** -8) + 1.1 * 2.0 ** -134
+                assert ((got[r] >= 0) & (got[r] <= limit)).all(), (byte, r)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("element", [E2M1, E4M3])
 def test_product_rows_do_not_touch_each_other(element):
     """A row's result does not depend on what the other rows hold: NaN rows spoil only themselves, a NaN weight row
     only its column, and rows behind the last one are never read into a result."""
