@@ -446,11 +446,14 @@ def combine(expand_x: torch.Tensor, assist_info: torch.Tensor, ep_recv_count: to
 
 # ---- the gate ----
 
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _launch(name: str, device, *args):
     """Call the library with `device` current (a launch on a device's default stream goes to the current
     device) and raise on an error status."""
     f = getattr(library(), name)
-    if device.index is None or device.index == torch.cuda.current_device():
+    if device.index is None or device.index == _raw_device():
         rc = f(*args)
     else:
         with torch.cuda.device(device):
@@ -475,7 +478,9 @@ def _address(t: Optional[torch.Tensor]):
 
 
 def _new(shape, dtype, device):
-    """torch.empty of one or two dimensions, at two thirds of its cost."""
+    """torch.empty, at three quarters of its cost for one or two dimensions."""
+    if len(shape) > 2:
+        return torch.empty(shape, dtype=dtype, device=device)
     return torch.empty_strided(shape, shape[1:] + (1,), dtype=dtype, device=device)
 
 
@@ -612,19 +617,17 @@ def _mx_rows(name, codes):
     raise MoeError(name, MOE_ERR_DTYPE, "microscaled codes are float8_e4m3fn or packed uint8, got %s" % codes.dtype)
 
 
-def _flat(shape):
-    n = 1
-    for v in shape:
-        n *= v
-    return n
-
-
-def _quantize(codes, scales, x, rows, cols, element):
-    """moe_mx_quantize of checked tensors."""
+def _quantize(codes, scales, x, cols, element):
+    """moe_mx_quantize of checked tensors; cols is not 0."""
     dev = x.device
-    _launch("moe_mx_quantize", dev, x.data_ptr(), rows, cols, _float_code("moe_mx_quantize", x.dtype), element,
-            codes.data_ptr(), scales.data_ptr(), _stream_ptr(dev))
+    _launch("moe_mx_quantize", dev, x.data_ptr(), x.numel() // cols, cols, _float_code("moe_mx_quantize", x.dtype),
+            element, codes.data_ptr(), scales.data_ptr(), _stream_ptr(dev))
     return codes, scales
+
+
+def _columns(fn, cols):
+    if cols < 1 or cols % 16:
+        raise MoeError(fn, MOE_ERR_SHAPE, "the last dimension must be a multiple of 16")
 
 
 def quantize_mx_into(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor):
@@ -635,11 +638,11 @@ def quantize_mx_into(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor)
     if x.dim() < 1 or codes.dim() < 1:
         raise MoeError("moe_mx_quantize", MOE_ERR_SHAPE, "x must have at least one dimension")
     element, shape = _mx_rows("codes", codes)
-    _float_code("moe_mx_quantize", x.dtype)
+    _columns("moe_mx_quantize", shape[-1])
     _check_tensor("x", x, x.dtype, shape, dev)
     _check_tensor("codes", codes, codes.dtype, codes.shape, dev)
     _check_tensor("scales", scales, torch.uint8, shape[:-1] + (-(-shape[-1] // MX_BLOCK),), dev)
-    return _quantize(codes, scales, x, _flat(shape[:-1]), shape[-1], element)
+    return _quantize(codes, scales, x, shape[-1], element)
 
 
 def quantize_mx(x: torch.Tensor, element: int = MOE_MX_E2M1):
@@ -649,23 +652,24 @@ def quantize_mx(x: torch.Tensor, element: int = MOE_MX_E2M1):
     power 2^(byte - 127) of a block of 32 elements. A block with an infinity or NaN gets byte 255 (NaN)."""
     dev = _gpu_device("x", x)
     dt, per = _mx_codes(element)
-    if x.dim() < 1 or x.shape[-1] < 1 or x.shape[-1] % 16:
-        raise MoeError("moe_mx_quantize", MOE_ERR_SHAPE, "the last dimension must be a multiple of 16")
-    _float_code("moe_mx_quantize", x.dtype)
-    _check_tensor("x", x, x.dtype, x.shape, dev)
     shape = tuple(x.shape)
-    lead, cols = shape[:-1], shape[-1]
-    codes = torch.empty(lead + (cols // per,), dtype=dt, device=dev)
-    scales = torch.empty(lead + (-(-cols // MX_BLOCK),), dtype=torch.uint8, device=dev)
-    return _quantize(codes, scales, x, _flat(lead), cols, element)
+    cols = shape[-1] if shape else 0
+    _columns("moe_mx_quantize", cols)
+    if x.dtype not in _FLOAT_CODES or not x.is_contiguous():
+        raise MoeError("moe_mx_quantize", MOE_ERR_DTYPE if x.dtype not in _FLOAT_CODES else MOE_ERR_SHAPE,
+                       "x must be a contiguous fp16, bf16 or fp32 tensor, got %s" % x.dtype)
+    lead = shape[:-1]
+    return _quantize(_new(lead + (cols // per,), dt, dev), _new(lead + (-(-cols // MX_BLOCK),), torch.uint8, dev), x,
+                     cols, element)
 
 
 def _dequantize(out, codes, scales, shape, element):
     """moe_mx_dequantize of a checked out."""
-    dev = out.device
+    dev, cols = out.device, shape[-1]
+    _columns("moe_mx_dequantize", cols)
     _check_tensor("codes", codes, codes.dtype, codes.shape, dev)
-    _check_tensor("scales", scales, torch.uint8, shape[:-1] + (-(-shape[-1] // MX_BLOCK),), dev)
-    _launch("moe_mx_dequantize", dev, codes.data_ptr(), scales.data_ptr(), _flat(shape[:-1]), shape[-1],
+    _check_tensor("scales", scales, torch.uint8, shape[:-1] + (-(-cols // MX_BLOCK),), dev)
+    _launch("moe_mx_dequantize", dev, codes.data_ptr(), scales.data_ptr(), out.numel() // cols, cols,
             _float_code("moe_mx_dequantize", out.dtype), element, out.data_ptr(), _stream_ptr(dev))
     return out
 
@@ -677,7 +681,6 @@ def dequantize_mx_into(out: torch.Tensor, codes: torch.Tensor, scales: torch.Ten
     if codes.dim() < 1:
         raise MoeError("moe_mx_dequantize", MOE_ERR_SHAPE, "codes must have at least one dimension")
     element, shape = _mx_rows("codes", codes)
-    _float_code("moe_mx_dequantize", out.dtype)
     _check_tensor("out", out, out.dtype, shape, dev)
     return _dequantize(out, codes, scales, shape, element)
 
@@ -689,7 +692,7 @@ def dequantize_mx(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype 
         raise MoeError("moe_mx_dequantize", MOE_ERR_SHAPE, "codes must have at least one dimension")
     _float_code("moe_mx_dequantize", dtype)
     element, shape = _mx_rows("codes", codes)
-    return _dequantize(torch.empty(shape, dtype=dtype, device=dev), codes, scales, shape, element)
+    return _dequantize(_new(shape, dtype, dev), codes, scales, shape, element)
 
 
 def expert_product_into(out: torch.Tensor, x: torch.Tensor, x_scales: torch.Tensor, weights: torch.Tensor,
@@ -736,5 +739,5 @@ def expert_product(x: torch.Tensor, x_scales: torch.Tensor, weights: torch.Tenso
     if x.dim() != 2 or not isinstance(weights, torch.Tensor) or weights.dim() != 3:
         raise MoeError("moe_expert_product", MOE_ERR_SHAPE, "x must be 2-D and weights 3-D")
     n = weights.shape[1]
-    out = torch.empty((x.shape[0], n // 2 if activation == MOE_ACT_SWIGLU else n), dtype=dtype, device=dev)
+    out = _new((x.shape[0], n // 2 if activation == MOE_ACT_SWIGLU else n), dtype, dev)
     return expert_product_into(out, x, x_scales, weights, weight_scales, ep_recv_count, activation)

@@ -222,6 +222,19 @@ def test_mx_wrappers_reject_before_the_call(rec):
     assert rec.calls == []
 
 
+def test_mx_wrappers_reject_rows_without_columns(rec):
+    none, byte = torch.zeros((4, 0), dtype=torch.uint8), torch.zeros((4, 0), dtype=torch.uint8)
+    for call in (lambda: moe.quantize_mx(torch.zeros(4, 0)), lambda: moe.quantize_mx(torch.tensor(1.0)),
+                 lambda: moe.quantize_mx_into(none, byte, torch.zeros(4, 0)), lambda: moe.dequantize_mx(none, byte),
+                 lambda: moe.dequantize_mx_into(torch.zeros(4, 0), none, byte),
+                 lambda: moe.dequantize_mx(torch.zeros((4, 20), dtype=torch.uint8), torch.zeros((4, 2), dtype=torch.uint8))):
+        with pytest.raises(moe.MoeError):
+            call()
+    assert rec.calls == []
+    codes, scales = moe.quantize_mx(torch.zeros(0, 48))
+    assert codes.shape == (0, 24) and scales.shape == (0, 2) and moe.dequantize_mx(codes, scales).shape == (0, 48)
+
+
 def test_cpu_tensors_are_rejected():
     with pytest.raises(moe.MoeError):
         moe.quantize_mx(torch.zeros(4, 64))
