@@ -77,8 +77,9 @@ __device__ __forceinline__ void load_piece(const void *in, long long piece, floa
 //
 // Memory bounds it: 2 bytes in and about half a byte (E2M1) or one (E4M3) out, an element, against some ten
 // instructions. Loads of 32 bytes a lane are whole lines between neighbours, the shared exponent is one exchange of
-// neighbours away, and nothing passes through LDS. bf16 [32768, 7168] to E2M1 and back to bf16 takes 202 us, 5.9 TB/s
-// of its 1.19 GB (a large copy reaches 5.2); [256, 7168] is the two calls' launches, 18.7 us.
+// neighbours away, and nothing passes through LDS. bf16 [32768, 7168] to E2M1 and back to bf16 takes 204 us, 5.8 TB/s
+// of its 1.19 GB (a large copy reaches 5.2); [256, 7168] is the two calls, 17 us, 6 of them
+// on the card.
 template <class T, int E, bool RAGGED, bool ONCE>
 __global__ __launch_bounds__(kMxThreads) void quantize_kernel(MxArgs a)
 {
@@ -427,7 +428,7 @@ __device__ __forceinline__ void barrier_fetched()
 // What bounds it, with 64 experts of 7168 -> 4096 with SwiGLU or 256 of 2048 -> 7168. Few rows: the weights' bytes,
 // 224 us for 1.0 GB with 32 rows each (5.9 TB/s of cache misses; a plain read reaches 6.2) and 512 us for 2.4 GB in
 // and out with 96 rows each. Many rows, skewed (1024 a rank, 8 ranks): power. The clock falls from 2.4 to 1.7 GHz, the
-// matrix units work 47 % of the cycles, 1190 us or 3.2 PFLOP/s, where the same instructions alone on random values
+// matrix units work half of the cycles, 1150 us or 3.4 PFLOP/s, where the same instructions alone on random values
 // reach 7.1 and on constant ones 9. Without fetches and results it takes 840 us, without fetches 930, with fetches that
 // hit the cache 1070. Four wavefronts of 128 x 128, which read a third less from LDS, need 1300: one wavefront a SIMD
 // leaves its waits open.
