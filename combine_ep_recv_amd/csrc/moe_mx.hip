@@ -429,7 +429,7 @@ __device__ __forceinline__ void barrier_fetched()
 // 224 us for 1.0 GB with 32 rows each (5.9 TB/s of cache misses; a plain read reaches 6.2) and 512 us for 2.4 GB in
 // and out with 96 rows each. Many rows, skewed (1024 a rank, 8 ranks): power. The clock falls from 2.4 to 1.7 GHz, the
 // matrix units work half of the cycles, 1150 us or 3.4 PFLOP/s, where the same instructions alone on random values
-// reach 7.1 and on constant ones 9. Without fetches and results it takes 840 us, without fetches 930, with fetches that
+// reach 7.1 and on constant ones 8.4. Without fetches and results it takes 840 us, without fetches 930, with fetches that
 // hit the cache 1070. Four wavefronts of 128 x 128, which read a third less from LDS, need 1300: one wavefront a SIMD
 // leaves its waits open.
 template <class T, int XF, int FR, int NF, int WM, int WN, int SUB, int RING, bool GLU>
