@@ -327,9 +327,9 @@ __device__ Tile find_tile(const ProductArgs &a, Plan &plan, int mt)
 }
 
 // The instruction adds its 128 products in fp32 when both sides are E2M1 (a sum of whole numbers below 2^24 comes out
-// exactly). With E4M3 it aligns neighbouring products to the largest of them and drops what lies 13 to 14 bits below
-// it: 1.5e-5 of the result on normal values, a 130th of the bf16 rounding behind it. That is the choice made here for
-// four times the rate of bf16 products, which would hold every product; between instructions the sum is fp32.
+// exactly). With E4M3 it aligns neighbouring products to the largest of them and drops what lies more than 13 bits
+// below it, which E4M3's 15 powers of two reach: where the large products cancel, nothing right would be left. So E4M3 rows
+// are multiplied in two parts (see split), between which and within which every product counts; sums are fp32 throughout.
 //
 // One 16 x 16 x 128 step: weights (E2M1) by rows of elements of format XF (0: E4M3, 4: E2M1), the scale bytes in
 // byte SEL of ws and xs. Lane (r, g), r = lane % 16, g = lane / 16, holds 32 elements of row r and the scale of
@@ -339,6 +339,19 @@ template <int XF, int SEL>
 __device__ __forceinline__ f32x4 mma(i32x8 w, i32x8 x, f32x4 c, uint32_t ws, uint32_t xs)
 {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, 4, XF, SEL, (int)ws, SEL, (int)xs);
+}
+
+// E4M3 codes in two parts: the magnitudes from 2 on (whose code has bit 6 set) and those below, zeros in each other's
+// places. The first are whole multiples of 2^-2 up to 448, the second of 2^-9 below 2: times E2M1 (multiples of 1/2 up
+// to 6) a part's products span 13 bits below the largest possible one's power of two, which is what the instruction
+// keeps. (A selector byte above 12 makes v_perm's byte 0xff, 0 picks a byte of the zeros.)
+__device__ __forceinline__ void split(i32x8 x, i32x8 &upper, i32x8 &lower)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        upper[i] = x[i] & (int)__builtin_amdgcn_perm(0u, 0u, (uint32_t)x[i] & 0x40404040u);
+        lower[i] = x[i] ^ upper[i];
+    }
 }
 
 __device__ __forceinline__ i32x8 join(u32x4 lo, u32x4 hi)
@@ -420,14 +433,16 @@ __device__ __forceinline__ void barrier_fetched()
 //
 // LDS holds RING stages. The barrier comes when the current one has been read, two fragments before its end; behind it
 // the stage RING ahead is fetched in its place, and the next one's first fragments are read while those two multiply.
+// E4M3 fragments are parted one ahead.
 // With two stages the next one is on its way while one is multiplied; with four, three are, for shapes that wait for
 // the weights from device memory. Input fragments are read two ahead. Scale bytes come 512 elements (four steps) at a
 // time, through registers, and become a word per (row, g) on the way. (Two groups at a time, so that neighbouring lanes
 // share a request: 1161 us for 1181 with many rows, but 23.0 for 21.7 with two tokens, whose code is then read once.)
 //
 // What bounds it, with 64 experts of 7168 -> 4096 with SwiGLU or 256 of 2048 -> 7168. Few rows: the weights' bytes,
-// 224 us for 1.0 GB with 32 rows each (5.9 TB/s of cache misses; a plain read reaches 6.2) and 512 us for 2.4 GB in
-// and out with 96 rows each. Many rows, skewed (1024 a rank, 8 ranks): power. The clock falls from 2.4 to 1.7 GHz, the
+// 212 us for 1.0 GB with 32 rows of E2M1 each (a plain read reaches 6.2 TB/s), 234 with E4M3, whose two parts
+// take twice the matrix instructions and 32 others a fragment, and 505 us for 2.4 GB in and out with 96 rows each. Many
+// E4M3 rows: the matrix units, 1505 us with 512 rows each where their instructions alone take 860. Many E2M1 rows, skewed (1024 a rank, 8 ranks): power. The clock falls from 2.4 to 1.7 GHz, the
 // matrix units work half of the cycles, 1150 us or 3.4 PFLOP/s, where the same instructions alone on random values
 // reach 7.1 and on constant ones 8.4. Without fetches and results it takes 840 us, without fetches 930, with fetches that
 // hit the cache 1070. Four wavefronts of 128 x 128, which read a third less from LDS, need 1300: one wavefront a SIMD
@@ -439,6 +454,10 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
     constexpr int kSub = XF == 4 ? SUB : 1, kStages = 4 / kSub;   // steps of a stage, stages of 512 elements
     constexpr int kPw = 4 * kSub, kPx = XF == 4 ? kPw : 8;    // 16-byte pieces of a row in a stage
     constexpr int kLoadsW = kRowsW * kPw / kThreads, kLoadsX = kRowsX * kPx / kThreads, kLoads = kLoadsW + kLoadsX;
+    // Whether a wavefront multiplies only the fragments that hold rows of the expert. E4M3's two parts make a fragment
+    // dear: 64 experts of 64 rows, 7168 -> 4096 with SwiGLU, 303 us, 380 with every fragment; two tokens 22 and 41.
+    constexpr bool kSkip = XF != 4;
+    static_assert(!kSkip || FR == 4, "the counts of fragments that the main loop is made for");
     constexpr int kRows = kRowsW + kRowsX, kScales = (kRows + kThreads - 1) / kThreads;   // scale rows of a thread
     static_assert(kRowsW * kPw % kThreads == 0 && kRowsX * kPx % kThreads == 0, "every thread carries as many pieces");
     static_assert(RING == 2 || (RING == 4 && kStages == 4), "a stage's place in the ring is known where it is used");
@@ -520,7 +539,7 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
 #pragma unroll
             for (int i = 0; i < kScales; ++i) to[sq[i]] = by_group(raw[i]);
         };
-        i32x8 wf[2][NF], xf[FR];
+        i32x8 wf[2][NF], xf[FR], upper[2], lower[2];
         uint32_t ws[NF], xs[FR];
         // fragments of step i of 512 elements
         auto read_w = [&](int i) {
@@ -532,6 +551,21 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
             const u32x4 *l = ring(i / kSub) + kSizeW + f * 16 * kPx;
             xf[f] = XF == 4 ? join(l[xfrag[i % kSub]], l[xfrag[i % kSub]]) : join(l[xfrag[0]], l[xfrag[1]]);
         };
+        // E4M3: the parts of fragment f, made while the one before multiplies
+        auto part = [&](int f) {
+            if constexpr (XF != 4) split(xf[f], upper[f & 1], lower[f & 1]);
+        };
+        auto multiply = [&](auto step, int f) {
+            constexpr int I = decltype(step)::value;
+#pragma unroll
+            for (int j = 0; j < NF; ++j)
+                acc[f][j] = mma<XF, I>(wf[I & 1][j], XF == 4 ? xf[f] : upper[f & 1], acc[f][j], ws[j], xs[f]);
+            if (XF != 4) {
+#pragma unroll
+                for (int j = 0; j < NF; ++j)
+                    acc[f][j] = mma<XF, I>(wf[I & 1][j], lower[f & 1], acc[f][j], ws[j], xs[f]);
+            }
+        };
         auto read_scales = [&](const u32x4 *from) {
             const uint32_t *p = reinterpret_cast<const uint32_t *>(from) + g;
 #pragma unroll
@@ -539,7 +573,10 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
 #pragma unroll
             for (int f = 0; f < FR; ++f) xs[f] = p[(kRowsW + (wm * FR + f) * 16 + r) * 4];
         };
-        if (supers > 0) {
+        // Whole groups of 512 elements, for the wavefront's first LIVE fragments. Every wavefront meets the same barriers
+        // and makes the same fetches whatever its LIVE.
+        auto whole = [&](auto count) {
+            constexpr int LIVE = decltype(count)::value, LAST = LIVE < 2 ? LIVE : 2;
             load_scales(0);
 #pragma unroll
             for (int i = 0; i < RING - 1; ++i) fetch(i, i);
@@ -548,43 +585,56 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
             barrier_fetched<(RING - 2) * kLoads>();
             fetch(RING - 1, RING - 1);
             read_w(0);
-            read_x(0, 0);
-            read_x(0, 1);
+#pragma unroll
+            for (int f = 0; f < LAST; ++f) read_x(0, f);
             read_scales(s0);
-        }
-        for (int super = 0; super < supers; ++super) {
+            part(0);
+            for (int super = 0; super < supers; ++super) {
 #define MOE_WIDE_STEP(I)                                                                              \
-            {                                                                                         \
-                constexpr bool kEnd = I % kSub == kSub - 1;                                           \
-                if (I == 0) load_scales(super + 1);                                                   \
-                if (I == 3) keep_scales(s1);                                                          \
-                _Pragma("unroll") for (int f = 0; f < FR - 2; ++f) {                                  \
-                    read_x(I, f + 2);                                                                 \
-                    _Pragma("unroll") for (int j = 0; j < NF; ++j)                                    \
-                        acc[f][j] = mma<XF, I>(wf[I & 1][j], xf[f], acc[f][j], ws[j], xs[f]);         \
+                {                                                                                     \
+                    constexpr bool kEnd = I % kSub == kSub - 1;                                       \
+                    if (I == 0) load_scales(super + 1);                                               \
+                    if (I == 3) keep_scales(s1);                                                      \
+                    _Pragma("unroll") for (int f = 0; f < LIVE - LAST; ++f) {                         \
+                        read_x(I, f + 2);                                                             \
+                        multiply(std::integral_constant<int, I>(), f);                                \
+                        if (f + 1 < LIVE - 1) part(f + 1);                                            \
+                        __builtin_amdgcn_sched_barrier(0);                                            \
+                    }                                                                                 \
+                    if (LIVE > 1) part(LIVE - 1);                                                     \
+                    if (kEnd) {                                                                       \
+                        barrier_fetched<(RING - 2) * kLoads>();                                       \
+                        __builtin_amdgcn_sched_barrier(0);                                            \
+                        fetch(super * kStages + I / kSub + RING, I / kSub);                           \
+                        __builtin_amdgcn_sched_barrier(0);                                            \
+                    }                                                                                 \
+                    read_w((I + 1) & 3);                                                              \
+                    _Pragma("unroll") for (int f = 0; f < LAST; ++f) read_x((I + 1) & 3, f);          \
                     __builtin_amdgcn_sched_barrier(0);                                                \
-                }                                                                                     \
-                if (kEnd) {                                                                           \
-                    barrier_fetched<(RING - 2) * kLoads>();                                           \
+                    _Pragma("unroll") for (int f = LIVE - LAST; f < LIVE; ++f)                        \
+                        multiply(std::integral_constant<int, I>(), f);                                \
+                    part(0);                                                                          \
+                    if (I == 3) read_scales(s1);                                                      \
                     __builtin_amdgcn_sched_barrier(0);                                                \
-                    fetch(super * kStages + I / kSub + RING, I / kSub);                               \
-                    __builtin_amdgcn_sched_barrier(0);                                                \
-                }                                                                                     \
-                read_w((I + 1) & 3);                                                                  \
-                read_x((I + 1) & 3, 0);                                                               \
-                read_x((I + 1) & 3, 1);                                                               \
-                __builtin_amdgcn_sched_barrier(0);                                                    \
-                _Pragma("unroll") for (int f = FR - 2; f < FR; ++f)                                   \
-                    _Pragma("unroll") for (int j = 0; j < NF; ++j)                                    \
-                        acc[f][j] = mma<XF, I>(wf[I & 1][j], xf[f], acc[f][j], ws[j], xs[f]);         \
-                if (I == 3) read_scales(s1);                                                          \
-                __builtin_amdgcn_sched_barrier(0);                                                    \
-            }
-            MOE_WIDE_STEP(0)
-            MOE_WIDE_STEP(1)
-            MOE_WIDE_STEP(2)
-            MOE_WIDE_STEP(3)
+                }
+                MOE_WIDE_STEP(0)
+                MOE_WIDE_STEP(1)
+                MOE_WIDE_STEP(2)
+                MOE_WIDE_STEP(3)
 #undef MOE_WIDE_STEP
+            }
+        };
+        if (supers > 0) {
+            using std::integral_constant;
+            if constexpr (kSkip) {
+                const int live = (last + 16 - wm * FR * 16) / 16;      // fragments of this wavefront that hold rows
+                if (live > 3) whole(integral_constant<int, 4>());
+                else if (live == 3) whole(integral_constant<int, 3>());
+                else if (live == 2) whole(integral_constant<int, 2>());
+                else whole(integral_constant<int, 1>());
+            } else {
+                whole(integral_constant<int, FR>());
+            }
         }
         barrier_fetched<0>();
         // the last k % 512 elements, a step at a time
@@ -612,8 +662,8 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
 #pragma unroll
             for (int f = 0; f < FR; ++f) {
                 read_x(0, f);
-#pragma unroll
-                for (int j = 0; j < NF; ++j) acc[f][j] = mma<XF, 0>(wf[0][j], xf[f], acc[f][j], ws[j], xs[f]);
+                part(f);
+                multiply(std::integral_constant<int, 0>(), f);
             }
             __syncthreads();
         }
@@ -659,13 +709,14 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
     }
 }
 
-// Rows of a tile, for `each` rows an expert. A tile of 64 rows keeps three stages of weights on their way and pads
-// few rows; above 48 rows an expert it would read the weights a second time, through the cache, and do too little on
-// what it read. Measured with 64 experts, 7168 -> 4096 with SwiGLU, 32 / 48 / 64 rows each: E4M3 225 / 256 / 301 us
-// with 64 rows, 279 / 287 / 292 with 128; E2M1 with 48 and 96 rows each 244 and 328 with 64, 227 and 240 with 128. Of
-// E2M1, 256 rows pay where the second half is more than an eighth full: 300 us and 312 with 128 rows each, 313 and 383
-// with 192, 684 and 769 with 512 (2048 -> 7168: 193 and 181, 209 and 243, 451 and 495). E4M3's fragments do not fit the
-// registers at that height (512 rows each: 1110 us, and 1090 with 128).
+// Rows of a tile, for `each` rows an expert (masked pairs' among them: no more is known here). A tile of 64 rows keeps
+// three stages of weights on their way and pads few rows; above 48 rows an expert it would read the weights a second
+// time, through the cache, and do too little on what it read. Measured with 64 experts, 7168 -> 4096 with SwiGLU, 32 / 48
+// / 64 rows each: E4M3 233 / 275 / 348 us with 64 rows, 277 / 292 / 302 with 128; E2M1 218 / 247 / 288 and 212 / 215 /
+// 218. Of E2M1, 256 rows pay where the second half is more than an eighth full, 160 and 512 rows each: 264 and 622 us,
+// 363 and 760 with 128 (2048 -> 7168, 144 and 512: 163 and 373, 210 and 451); at 128 each they do by a tenth where no
+// pair is masked (256 and 296 us) and lose where a quarter is (596 and 512). E4M3's fragments do not fit the registers at
+// that height.
 int tile_rows(int each, int element)
 {
     if (each <= 48) return 64;
