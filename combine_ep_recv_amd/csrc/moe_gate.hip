@@ -198,7 +198,7 @@ __device__ __attribute__((noinline)) int choose_exactly(const typename T::raw *r
 //            at most 3.6 for 320 experts and 5.1 for 2048, and 2 u for its reciprocal. Below (PER / 4 + 32) u together.
 //   sigmoid  1.25 |x| s (1 - s) u <= 0.3 u, half of exp2's u (s (1 - s) <= 1/4), u of the sum and 2 u of the
 //            reciprocal: below 4 u each.
-// Either way half an ulp of each choice for its sum with the bias.
+// Either way half an ulp of each choice for its sum with the bias; for a group's sum of two, of each term and of the sum.
 // Without a bias the logits themselves are compared, which needs neither.
 //
 // What bounds it: vector instructions and their order, not memory. 65521 tokens of 304 experts (bf16, softmax, bias,
@@ -278,6 +278,10 @@ __global__ __launch_bounds__(WAVES *kWave, LANES == 16 ? 4 : (PER <= 5 ? 5 : 1))
             float first, second;
             best_of_groups(v, a.groups, a.group_size, sub, share, first, second);
             float worth = a.group_top2 && second > low ? first + second : first;
+            // what the rounding of a sum's terms goes by: they may cancel, and those of any group bear on the order
+            float size = 0.f;
+            if (a.group_top2)
+                size = wave_max<LANES>(second > low ? fabsf(first) + fabsf(second) : (first > low ? fabsf(first) : 0.f));
             if (sub % share != 0) worth = low;
             unsigned long long kept = 0;
             int place = sub;
@@ -287,7 +291,8 @@ __global__ __launch_bounds__(WAVES *kWave, LANES == 16 ? 4 : (PER <= 5 ? 5 : 1))
                 const float m = wave_max<LANES>(worth);
                 if (i == a.topk_groups) {
                     // whether the last kept group lies clear of the best one left out
-                    if (by_score && m > low && !(above - m > 2.f * (room + 0x1.4p-23f * fabsf(above)))) safe = false;
+                    size = fmaxf(size, fabsf(above));
+                    if (by_score && m > low && !(above - m > 2.f * (room + 0x1.4p-23f * size))) safe = false;
                     break;
                 }
                 const uint32_t at = wave_min<LANES>(worth == m && m > low ? (uint32_t)sub : 64u);

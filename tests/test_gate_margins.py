@@ -1,0 +1,27 @@
+"""The gate where its fp32 choice has to know its own limits, and where one token's result could depend on others.
+
+Ids and weights are held to the definition as in test_gate.py; what must not depend on a token's neighbours or on the
+length of the batch must be equal bit for bit.
+"""
+import pytest
+import torch
+
+import combine_ep_recv_amd as moe
+from test_gate import DEV, MAX, SIGMOID, SOFTMAX, TOP2, check, draw
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("N", [300, 1100])
+@pytest.mark.parametrize("size", [1e2, 1e3, 1e4])
+def test_gate_groups_whose_two_best_cancel(score, N, size):
+    """A large bias and its negative in every group: a group's worth is near 1, the terms' rounding that of the bias.
+    Groups lie as far apart as that rounding, experts much further. Short batches, and those whose tokens share a
+    wavefront."""
+    g = torch.Generator().manual_seed(int(size))
+    L = torch.randn(1, 1, 2, generator=g).expand(N, 8, 2) + size * 2.0 ** -20 * torch.randn(N, 8, 2, generator=g)
+    L = L.reshape(N, 16).contiguous()
+    b = (size * (1 + torch.arange(8) / 8))[:, None].mul(torch.tensor([1.0, -1.0])).flatten().float()
+    kw = dict(score=score, groups=8, topk_groups=4, group_score=TOP2)
+    ids, w = moe.gate(L.to(DEV), 8, bias=b.to(DEV), **kw)
+    check(L, ids, w, bias=b, **kw)
