@@ -282,6 +282,7 @@ __global__ __launch_bounds__(WAVES *kWave, LANES == 16 ? 4 : (PER <= 5 ? 5 : 1))
             float size = 0.f;
             if (a.group_top2)
                 size = wave_max<LANES>(second > low ? fabsf(first) + fabsf(second) : (first > low ? fabsf(first) : 0.f));
+            if (!(size < INFINITY)) safe = false;         // a sum that fp32 does not hold, and binary64 does
             if (sub % share != 0) worth = low;
             unsigned long long kept = 0;
             int place = sub;

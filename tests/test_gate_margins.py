@@ -25,3 +25,20 @@ def test_gate_groups_whose_two_best_cancel(score, N, size):
     kw = dict(score=score, groups=8, topk_groups=4, group_score=TOP2)
     ids, w = moe.gate(L.to(DEV), 8, bias=b.to(DEV), **kw)
     check(L, ids, w, bias=b, **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("N", [40, 1100])
+def test_gate_groups_whose_sum_passes_fp32(score, N):
+    """Biases near the largest finite ones, both signs: sums of two that are finite in binary64 and infinite in fp32."""
+    top = torch.finfo(torch.float32).max
+    L = draw(N, 16, torch.float32, 5)
+    for b in (torch.tensor([-top] * 12 + [0.0, 0.5, 1.0, 1.5]),
+              torch.tensor([-top, 0.75 * -top] * 6 + [0.5 * -top, -top] * 2),
+              torch.tensor([top, 0.5 * top] * 4 + [top, 0.75 * top] * 4),
+              torch.tensor([0.0, 1.0] * 3 + [float("inf"), 0.0] + [-top] * 8)):
+        for keep in (1, 3, 5):
+            kw = dict(score=score, groups=8, topk_groups=keep, group_score=TOP2)
+            ids, w = moe.gate(L.to(DEV), 2 * keep, bias=b.to(DEV), **kw)
+            check(L, ids, w, bias=b, **kw)
