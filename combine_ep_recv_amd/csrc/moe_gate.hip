@@ -400,17 +400,18 @@ __global__ __launch_bounds__(WAVES *kWave, LANES == 16 ? 4 : (PER <= 5 ? 5 : 1))
         }
         if (!any) w = 0.f;
         const float total = a.renorm ? wave_sum<LANES>(w) : 0.f;
-        // scores below e^-80, whose sum fp32 may not hold: those weights in binary64
-        if (__ballot(any && (SCORE == MOE_SCORE_SOFTMAX ? x - top : x) < -80.f)) {
+        w = a.renorm ? (total > 0.f ? w / total : 0.f) : w * inv;
+        // scores below e^-80, whose sum fp32 may not hold: the weights of such a token in binary64
+        const unsigned long long tiny = __ballot(any && (SCORE == MOE_SCORE_SOFTMAX ? x - top : x) < -80.f);
+        if (tiny) {
             double d = SCORE == MOE_SCORE_SOFTMAX ? exponential(x == top ? 0.f : x, x == top ? 0.f : top)
                                                   : 1.0 / (1.0 + exponential(-x, 0.f));
             if (!any) d = 0.0;
             double all = d;
 #pragma unroll
             for (int i = 1; i < LANES; i *= 2) all += __shfl_xor(all, i);
-            w = (float)(a.renorm ? (all > 0.0 ? d / all : 0.0) : d * (double)inv);
-        } else {
-            w = a.renorm ? (total > 0.f ? w / total : 0.f) : w * inv;
+            const bool here = LANES == kWave || (tiny >> (lane / LANES * LANES) & 0xffff);
+            if (here) w = (float)(a.renorm ? (all > 0.0 ? d / all : 0.0) : d * (double)inv);
         }
         w = any ? w * a.scale : 0.f;
         if (sub < a.topk && t < a.tokens) {

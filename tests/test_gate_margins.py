@@ -42,3 +42,20 @@ def test_gate_groups_whose_sum_passes_fp32(score, N):
             kw = dict(score=score, groups=8, topk_groups=keep, group_score=TOP2)
             ids, w = moe.gate(L.to(DEV), 2 * keep, bias=b.to(DEV), **kw)
             check(L, ids, w, bias=b, **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_gate_weights_do_not_depend_on_the_neighbours(score, renormalize):
+    """Tokens that share a wavefront with one whose chosen scores lie below e^-80, and without."""
+    N, E = 1100, 32
+    L = draw(N, E, torch.float32, 7)
+    low = L.clone()
+    low[1::4, 3:] = -150.0 - torch.arange(E - 3)
+    kw = dict(score=score, renormalize=renormalize)
+    ids, w = moe.gate(L.to(DEV), 8, **kw)
+    ids2, w2 = moe.gate(low.to(DEV), 8, **kw)
+    same = torch.arange(N) % 4 != 1
+    assert torch.equal(ids[same], ids2[same]) and torch.equal(w[same], w2[same])
+    check(low[:60], ids2[:60], w2[:60], **kw)
