@@ -194,8 +194,8 @@ __device__ __attribute__((noinline)) int choose_exactly(const typename T::raw *r
 // launch is waited for, so the bound is worth its care.
 //   softmax  two exponentials, each off by 2.25 |x| u (a difference, a product, its constant) and 2 u, where
 //            |x| e^x <= 0.37: 5.7 u of the largest score. The sum is the same for both: the difference of two scores
-//            shares its error, PER / 4 + 7 u for adding, 2 u and 2.25 |x| u, |x| averaged over the sum and so
-//            at most 3.6 for 320 experts and 5.1 for 2048, and 2 u for its reciprocal. Below (PER / 4 + 32) u together.
+//            shares its error, E / 64 + 7 u for adding, 2 u and 2.25 |x| u, |x| averaged over the sum and so
+//            at most 3.6 for 320 experts and 5.1 for 2048, and 2 u for its reciprocal. Below (E / 64 + 32) u together.
 //   sigmoid  1.25 |x| s (1 - s) u <= 0.3 u, half of exp2's u (s (1 - s) <= 1/4), u of the sum and 2 u of the
 //            reciprocal: below 4 u each.
 // Either way half an ulp of each choice for its sum with the bias; for a group's sum of two, of each term and of the sum.
@@ -249,19 +249,23 @@ __global__ __launch_bounds__(WAVES *kWave, LANES == 16 ? 4 : (PER <= 5 ? 5 : 1))
         for (int j = 0; j < PER; ++j) c[j] = l[j];
         bool safe = true;
         if (SCORE == MOE_SCORE_SOFTMAX) {
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};          // four sums: short ones are off by less
+            // Experts that are 64 apart add up first, then the four of those sums that are 16 apart, then 16 such: one
+            // order, whatever the lanes, so that a token's weights do not change with the length of its batch.
+            constexpr int kSums = kWave / LANES;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 c[j] = __builtin_amdgcn_exp2f((l[j] - top) * log2e);
-                sum[j % 4] += c[j];
+                sum[j % kSums] += c[j];
             }
-            inv = best = __builtin_amdgcn_rcpf(wave_sum<LANES>((sum[0] + sum[1]) + (sum[2] + sum[3])));
+            const float four = LANES == 16 ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : sum_of_rows(sum[0]);
+            inv = best = __builtin_amdgcn_rcpf(wave_sum<16>(four));
             safe = top < INFINITY;                        // logits of +infinity: NaN above
         } else if (by_score) {
 #pragma unroll
             for (int j = 0; j < PER; ++j) c[j] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l[j] * -log2e));
         }
-        const float room = (SCORE == MOE_SCORE_SIGMOID ? 8 : PER / 4 + 32) * 0x1p-24f * best + 0x1p-100f;
+        const float room = (SCORE == MOE_SCORE_SIGMOID ? 8 : LANES * PER / kWave + 32) * 0x1p-24f * best + 0x1p-100f;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
             const float b = bias[j * LANES + sub], s = by_score ? __builtin_fmaf(c[j], inv, b) : l[j];

@@ -107,6 +107,14 @@ __device__ __forceinline__ float wave_sum(float v)
 }
 #undef MOE_REDUCE_64
 #undef MOE_REDUCE_16
+// (row 0 + row 1) + (row 2 + row 3) of the wavefront's rows of 16 lanes, in every row
+__device__ __forceinline__ float sum_of_rows(float v)
+{
+    const auto odd = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(odd[0]) + __uint_as_float(odd[1]);
+    const auto half = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(half[0]) + __uint_as_float(half[1]);
+}
 __device__ __forceinline__ double wave_max(double v)
 {
     v = max_of(v, dpp<0x111, 0xf>(v, v));

@@ -352,7 +352,8 @@ enum moe_group_score { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
  *  pair_mask     uint8 [N, K] or NULL: 1 where the pair has an expert
  * Ranges: 0 <= tokens < 2^24, 1 <= experts <= 2048 (special experts' ids may be among them), 1 <= topk <= 64,
  * 1 <= groups <= 64, groups divides experts, topk <= topk_groups * experts / groups, scale finite and not 0; a value
- * outside them, or an unknown score or group score, is MOE_ERR_SHAPE. Outputs are bitwise deterministic.
+ * outside them, or an unknown score or group score, is MOE_ERR_SHAPE. Outputs are bitwise deterministic, and a
+ * token's do not depend on the other tokens or on how many there are.
  */
 int moe_gate(const void *logits, const float *bias, const uint8_t *token_mask, int tokens, int experts, int topk,
              int dtype, int score, int groups, int topk_groups, int group_score, int renormalize, float scale,

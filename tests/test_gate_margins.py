@@ -59,3 +59,18 @@ def test_gate_weights_do_not_depend_on_the_neighbours(score, renormalize):
     same = torch.arange(N) % 4 != 1
     assert torch.equal(ids[same], ids2[same]) and torch.equal(w[same], w2[same])
     check(low[:60], ids2[:60], w2[:60], **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("E,K", [(20, 4), (64, 8), (100, 8), (200, 16), (256, 8), (300, 3), (320, 16)])
+def test_gate_weights_do_not_depend_on_the_length_of_the_batch(score, E, K):
+    """Tokens alone, in a short batch and in one long enough for several to share a wavefront."""
+    N = 33 * E
+    L = draw(N, E, torch.float32, E).to(DEV)
+    for renormalize in (True, False):
+        kw = dict(score=score, renormalize=renormalize)
+        ids, w = moe.gate(L, K, **kw)
+        for rows in (slice(0, 1), slice(5, 30), slice(N - 200, N)):
+            part, pw = moe.gate(L[rows].contiguous(), K, **kw)
+            assert torch.equal(part, ids[rows]) and torch.equal(pw, w[rows])
