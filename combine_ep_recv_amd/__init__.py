@@ -484,6 +484,12 @@ def _new(shape, dtype, device):
     return torch.empty_strided(shape, shape[1:] + (1,), dtype=dtype, device=device)
 
 
+def _check_int(fn, bits):
+    """Refuse sizes that a C int does not hold, which ctypes would cut off without a word; bits: all of them, or-ed."""
+    if bits >> 31:
+        raise MoeError(fn, MOE_ERR_SHAPE, "a size or option is negative or above 2^31 - 1")
+
+
 def _logits(fn, logits):
     """(device, tokens, experts, dtype code) of a gate's logits, checked."""
     dev = _gpu_device("logits", logits)
@@ -509,8 +515,10 @@ def _gate(head, ids, w, logits, topk, score, bias, groups, topk_groups, group_sc
         _check_tensor("bias", bias, torch.float32, (E,), dev)
     if token_mask is not None:
         _byte_mask("token_mask", token_mask, (N,), dev)
-    _launch("moe_gate", dev, logits.data_ptr(), _address(bias), _address(token_mask), N, E, topk, dt, int(score),
-            int(groups), int(topk_groups), int(group_score), 1 if renormalize else 0, float(scale), ids.data_ptr(),
+    score, groups, topk_groups, group_score = int(score), int(groups), int(topk_groups), int(group_score)
+    _check_int("moe_gate", N | E | topk | score | groups | topk_groups | group_score)
+    _launch("moe_gate", dev, logits.data_ptr(), _address(bias), _address(token_mask), N, E, topk, dt, score,
+            groups, topk_groups, group_score, 1 if renormalize else 0, float(scale), ids.data_ptr(),
             w.data_ptr(), _address(pair_mask), _stream_ptr(dev))
 
 
@@ -568,6 +576,7 @@ def _gate_backward(head, out, logits, ids, w, grad, score, renormalize, scale):
     _check_tensor("expert_ids", ids, torch.int32, (N, K), dev)
     _check_tensor("expert_scales", w, torch.float32, (N, K), dev)
     _check_tensor("grad_scales", grad, torch.float32, (N, K), dev)
+    _check_int("moe_gate_backward", N | E | K | int(score))
     _launch("moe_gate_backward", dev, logits.data_ptr(), ids.data_ptr(), w.data_ptr(), grad.data_ptr(), N, E, K, dt,
             int(score), 1 if renormalize else 0, float(scale), out.data_ptr(), _stream_ptr(dev))
     return out
@@ -628,6 +637,7 @@ def _quantize(codes, scales, x, cols, element):
 def _columns(fn, cols):
     if cols < 1 or cols % 16:
         raise MoeError(fn, MOE_ERR_SHAPE, "the last dimension must be a multiple of 16")
+    _check_int(fn, cols)
 
 
 def quantize_mx_into(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor):
@@ -719,6 +729,7 @@ def expert_product_into(out: torch.Tensor, x: torch.Tensor, x_scales: torch.Tens
     _check_tensor("weight_scales", weight_scales, torch.uint8, (E, n, nb), dev)
     _check_tensor("ep_recv_count", ep_recv_count, torch.int32, (W, E), dev)
     _check_tensor("out", out, out.dtype, (rows, n // 2 if activation == MOE_ACT_SWIGLU else n), dev)
+    _check_int("moe_expert_product", W | E | rows | k | n | int(activation))
     _launch("moe_expert_product", dev, x.data_ptr(), x_scales.data_ptr(), element, weights.data_ptr(),
             weight_scales.data_ptr(), ep_recv_count.data_ptr(), W, E // W, rows, k, n, int(activation),
             dtype_code(out.dtype), out.data_ptr(), _stream_ptr(dev))
