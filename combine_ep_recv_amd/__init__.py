@@ -558,8 +558,8 @@ def gate(logits: torch.Tensor, topk: int, score: int = MOE_SCORE_SOFTMAX, bias: 
     """
     head = _logits("moe_gate", logits)
     topk = int(topk)
-    if topk < 1:
-        raise MoeError("moe_gate", MOE_ERR_SHAPE, "topk must be at least 1")
+    if not 1 <= topk <= head[2]:
+        raise MoeError("moe_gate", MOE_ERR_SHAPE, "topk must be between 1 and the number of experts")
     dev, shape = head[0], (head[1], topk)
     ids, w = _new(shape, torch.int32, dev), _new(shape, torch.float32, dev)
     on = _new(shape, torch.bool, dev) if with_pair_mask else None

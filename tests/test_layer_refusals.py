@@ -53,3 +53,10 @@ def test_sizes_beyond_a_c_int_are_refused_not_cut_off(rec, call):  # noqa: F811
     with pytest.raises(moe.MoeError) as e:
         call()
     assert e.value.status == moe.MOE_ERR_SHAPE and rec.calls == []
+
+
+@pytest.mark.parametrize("topk", [0, -3, 17, 10 ** 12, BIG + 2])
+def test_gate_refuses_a_topk_before_it_makes_room_for_it(rec, topk):  # noqa: F811
+    with pytest.raises(moe.MoeError) as e:
+        moe.gate(torch.zeros(4, 16), topk)
+    assert e.value.status == moe.MOE_ERR_SHAPE and rec.calls == []
