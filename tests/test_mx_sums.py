@@ -76,3 +76,14 @@ def test_product_counts_every_product_of_e4m3_rows(k, rows):
 @pytest.mark.parametrize("k", [112, 512, 1168])
 def test_product_sums_in_fp32(element, act, per_expert, k):
     check_sums(per_expert, 2, k, 150, element, act, seed=k, spare=2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("element", [E2M1, E4M3])
+@pytest.mark.parametrize("per_expert,k", [([100, 90, 130, 70], 528), ([100, 90, 130, 70], 1040), ([300, 250, 17, 400], 528),
+                                          ([300, 250, 17, 400], 1040), ([300, 200] * 24, 528)],
+                         ids=["128 rows, 528", "128 rows, 1040", "256 rows, 528", "256 rows, 1040", "many tiles"])
+def test_swiglu_of_tall_tiles_and_several_columns(element, per_expert, k):
+    """SwiGLU where a tile has 128 or 256 rows: three tiles of columns, the last one ragged and of an odd width, and a
+    rest of k behind the whole groups; with more tiles than workgroups a workgroup goes from column tile to column tile."""
+    check_sums(per_expert, 2, k, 2 * (2 * 128 + 37), element, SWIGLU, seed=k, spare=2)
