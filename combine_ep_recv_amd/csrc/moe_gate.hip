@@ -84,8 +84,8 @@ __device__ __forceinline__ P uniform(P v)
 // exp(x - y) in binary64
 __device__ __attribute__((noinline)) double exponential(float x, float y) { return exp((double)x - (double)y); }
 
-// The choice for one token from binary64 scores, by a whole wavefront: lane k gets pair k's id. Rare (see
-// gate_kernel), so it trades time for registers: the scores lie in LDS (v[experts], this wavefront's), the logits are
+// The choice for one token from binary64 scores, by a whole wavefront: lane k gets pair k's id. Rare but for equal sums
+// (see gate_kernel), so it trades time for registers: the scores lie in LDS (v[experts], this wavefront's), the logits are
 // read again (v holds them first). `bias` is LDS too, zeros where there is none. Not inlined: the constants of binary64's
 // exponential would be kept in registers through gate_kernel's loop. Every argument is the same in all lanes.
 template <class T, int SCORE>
@@ -200,11 +200,14 @@ __device__ __attribute__((noinline)) int choose_exactly(const typename T::raw *r
 //            reciprocal: below 4 u each.
 // Either way half an ulp of each choice for its sum with the bias; for a group's sum of two, of each term and of the sum.
 // Without a bias the logits themselves are compared, which needs neither.
+// Of the tokens of a random bias one in two thousand is decided again. Equal sums always are: under a bias of zeros, or
+// any constant one, every tie of logits among the picks. A third of 65536 tokens of 256 bf16 logits have one, and take 96
+// us (fp16 logits 53), 37 and 35 with a random bias; 4096 tokens 14.5 and 11.0.
 //
 // What bounds it: vector instructions and their order, not memory. 65521 tokens of 304 experts (bf16, softmax, bias,
-// 8 picks, a quarter of the tokens masked) take 47 us, 40 without the last binary64 look, for 31 MB of logits (5 us);
+// 8 picks, a quarter of the tokens masked) take 47 us, 40 without the last binary64 look, for 30 MB of logits (6 us);
 // the vector units are busy for 32 of them (1200 instructions for four tokens, with every list and pick). 4096 tokens
-// of 256 experts in 8 groups take 12, 8.5 without that look; 8 tokens take 8, 3.5 of them on the card.
+// of 256 experts in 8 groups take 11 to 14, 8.5 without that look; 8 tokens take 11, 3.5 of them on the card.
 template <class T, int LANES, int PER, int WAVES, int SCORE>
 __global__ __launch_bounds__(WAVES *kWave, LANES == 16 ? 4 : (PER <= 5 ? 5 : 1)) void gate_kernel(GateArgs a)
 {

@@ -338,7 +338,9 @@ enum moe_group_score { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
  *   the topk_groups best of `groups` equal groups of consecutive experts; the topk largest c in them, descending
  *   expert_scales[t, k] = scale * s[id_k] / (renormalize ? sum over the chosen s : 1)
  * Ties go to the lower id (group). c is compared as in binary64; without a bias the logits are compared, whose order
- * is that of the scores. A chosen sum of 0 gives weights 0.
+ * is that of the scores. A chosen sum of 0 gives weights 0. Choices too close for fp32 to tell, equal sums among them,
+ * are made again in binary64, some microseconds a token: a constant bias over 16-bit logits, which have many ties, is
+ * slower than no bias.
  * A logit of -infinity or NaN is an expert that is not there: never chosen, score 0. Logits of +infinity share the
  * softmax equally. A bias of -infinity or NaN keeps its expert from being chosen and leaves the scores as they are.
  * Where fewer than topk experts can be chosen, and in the rows that token_mask leaves out, the pairs that are missing
@@ -415,7 +417,8 @@ enum moe_activation { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 };
  *                ep_recv_count counts are left as they were
  * A scale byte of 255 makes every result of its row NaN.
  * Ranges: ep_world and experts as in moe_dispatch, 0 <= rows < 2^31 - 256, k a multiple of 16 up to 2^24, n >= 1
- * (even with SwiGLU), n * k <= 2^32, (rows / 64 + E) * ceil(n / 64) < 2^31 - 1024 (MOE_ERR_SHAPE otherwise). Counts
+ * (even with SwiGLU), n * k <= 2^32 (MOE_ERR_SHAPE otherwise). Tiles are counted in 31 bits: every call with
+ * (rows / 64 + E) * ceil(n / 64) < 2^31 - 1024 is taken, larger ones as far as their tiles allow. Counts
  * that ep_recv_count should not hold (negative, descending, beyond rows) leave the kernel in bounds and the outputs
  * unspecified. Needs no workspace.
  */
