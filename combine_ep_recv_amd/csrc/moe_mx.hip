@@ -386,7 +386,8 @@ __device__ __forceinline__ u32x4 by_group(u32x4 d)
 }
 
 // silu(gate) * up by the hardware's exponential and reciprocal (an ulp each; the exponent's argument is off by |gate|
-// half steps): far below the 16-bit rounding behind it
+// half steps): far below the 16-bit rounding behind it. Below a gate of about -87 the reciprocal underflows, where fp32's
+// exponential overflows below -88, and the result is 0 instead of less than 2e-36 |up|.
 __device__ __forceinline__ float swiglu(float gate, float up)
 {
     return gate * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(gate * -1.44269504f)) * up;

@@ -87,3 +87,32 @@ def test_swiglu_of_tall_tiles_and_several_columns(element, per_expert, k):
     """SwiGLU where a tile has 128 or 256 rows: three tiles of columns, the last one ragged and of an odd width, and a
     rest of k behind the whole groups; with more tiles than workgroups a workgroup goes from column tile to column tile."""
     check_sums(per_expert, 2, k, 2 * (2 * 128 + 37), element, SWIGLU, seed=k, spare=2)
+
+
+@pytest.mark.gpu
+def test_product_of_e4m3_rows_replayed_with_other_row_counts():
+    """One captured call, replayed as the experts' row counts change under it: tiles with one to four fragments of rows,
+    whole tiles and none."""
+    per, W, k, n = [64, 64, 64, 64], 2, 656, 96
+    x, xs, w, ws, counts = draw_product(per, W, k, n, E4M3, 4, spread=2)
+    dev = on_gpu(x, xs, w, ws, counts, E4M3)
+    out = torch.empty((256, n // 2), dtype=torch.bfloat16, device=DEV)
+    moe.expert_product_into(out, *dev, activation=SWIGLU)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.expert_product_into(out, *dev, activation=SWIGLU)
+    for i, now in enumerate(([64, 64, 64, 64], [1, 16, 17, 222], [0, 256, 0, 0], [33, 48, 49, 126], [5, 0, 130, 65])):
+        dev[4].copy_(counts_for(now, W, i))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        want = torch.full_like(out, 7.0)
+        moe.expert_product_into(want, *dev, activation=SWIGLU)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        if i == 0:
+            first = got
+    # expert 0's first five rows are the same in every call that gives them to it
+    assert torch.equal(got[:5], first[:5])
