@@ -43,7 +43,8 @@ MOE_MX_E2M1, MOE_MX_E4M3 = 0, 1
 MOE_ACT_NONE, MOE_ACT_SWIGLU = 0, 1
 
 EXPORTS = ("moe_dispatch_workspace_size", "moe_dispatch", "moe_dispatch_noalloc", "moe_combine_workspace_size",
-           "moe_combine", "moe_gate", "moe_gate_backward", "moe_mx_quantize", "moe_mx_dequantize",
+           "moe_combine", "moe_combine_backward_workspace_size", "moe_combine_backward", "moe_dispatch_backward",
+           "moe_gate", "moe_gate_backward", "moe_mx_quantize", "moe_mx_dequantize",
            "moe_expert_product", "moe_status_str")
 NOALLOC_SCRATCH_BYTES = 32 << 20      # MOE_NOALLOC_SCRATCH_BYTES
 
@@ -107,6 +108,13 @@ def library() -> ctypes.CDLL:
     lib.moe_combine.argtypes = [P, P, P, P, P, P, I, ctypes.POINTER(MoeSpecialExperts), I, I, I, I, I, I, P, P,
                                 SZ, P]
     lib.moe_combine.restype = I
+    lib.moe_combine_backward_workspace_size.argtypes = [I, I, I, I, I, I, I, ctypes.POINTER(SZ)]
+    lib.moe_combine_backward_workspace_size.restype = I
+    lib.moe_combine_backward.argtypes = [P, P, P, P, P, P, P, I, ctypes.POINTER(MoeSpecialExperts), I, I, I, I, I, I,
+                                         P, P, P, P, P, SZ, P]
+    lib.moe_combine_backward.restype = I
+    lib.moe_dispatch_backward.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, P, P]
+    lib.moe_dispatch_backward.restype = I
     F, L = ctypes.c_float, ctypes.c_int64
     lib.moe_gate.argtypes = [P, P, P, I, I, I, I, I, I, I, I, I, F, P, P, P, P]
     lib.moe_gate.restype = I
@@ -444,7 +452,7 @@ def combine(expand_x: torch.Tensor, assist_info: torch.Tensor, ep_recv_count: to
                         copy_experts=copy_experts, ori_x=ori_x, const_experts=const_experts, const_x=const_x)
 
 
-# ---- the gate ----
+# ---- launches of what stands around dispatch and combine ----
 
 _raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
@@ -489,6 +497,169 @@ def _check_int(fn, bits):
     if bits >> 31:
         raise MoeError(fn, MOE_ERR_SHAPE, "a size or option is negative or above 2^31 - 1")
 
+
+# ---- the gradients of combine and dispatch ----
+
+def combine_backward_workspace_size(ep_world, bs, experts_per_rank, h, topk, dtype, const_experts=0) -> int:
+    _check_int("moe_combine_backward", ep_world | bs | experts_per_rank | h | topk | const_experts)
+    n = ctypes.c_size_t(0)
+    _check("moe_combine_backward_workspace_size",
+           library().moe_combine_backward_workspace_size(ep_world, bs, experts_per_rank, h, topk, dtype, const_experts,
+                                                         ctypes.byref(n)))
+    return n.value
+
+
+def combine_backward_workspace(ep_world, bs, experts_per_rank, h, topk, dtype: torch.dtype, const_experts=0,
+                               device="cuda"):
+    """Workspace tensor for moe_combine_backward of this shape, or None where it needs none."""
+    n = combine_backward_workspace_size(ep_world, bs, experts_per_rank, h, topk, dtype_code(dtype), const_experts)
+    return torch.empty((n,), dtype=torch.uint8, device=device) if n else None
+
+
+def _row_call(fn, rows, expert_ids, ep_world, experts_per_rank):
+    """(device, tokens, topk, h, dtype code) of a gradient call on dispatch's rows, its sizes checked."""
+    dev = _gpu_device("expert_ids", expert_ids)
+    _gpu_device("the rows", rows)
+    if rows.dim() != 2 or expert_ids.dim() != 2:
+        raise MoeError(fn, MOE_ERR_SHAPE, "the rows and expert_ids must be 2-D")
+    if rows.dtype not in (torch.float16, torch.bfloat16):
+        raise MoeError(fn, MOE_ERR_DTYPE, "gradients are fp16 or bf16, got %s" % rows.dtype)
+    N, K = expert_ids.shape
+    _check_int(fn, N | K | rows.shape[1] | ep_world | experts_per_rank)
+    if ep_world < 1 or N % ep_world or rows.shape[0] != N * K:
+        raise MoeError(fn, MOE_ERR_SHAPE, "there must be ep_world*bs*topk rows")
+    return dev, N, K, rows.shape[1], _FLOAT_CODES[rows.dtype]
+
+
+def _check_routing(assist_info, ep_recv_count, expert_ids, N, K, ep_world, experts_per_rank, device):
+    _check_tensor("assist_info", assist_info, torch.int32, (N * K, 3), device)
+    _check_tensor("ep_recv_count", ep_recv_count, torch.int32, (ep_world, experts_per_rank * ep_world), device)
+    _check_tensor("expert_ids", expert_ids, torch.int32, (N, K), device)
+
+
+def combine_backward_into(grad_expand_x: torch.Tensor, grad_scales: torch.Tensor, grad_out: torch.Tensor,
+                          expand_x: torch.Tensor, assist_info: torch.Tensor, ep_recv_count: torch.Tensor,
+                          expert_ids: torch.Tensor, expert_scales: torch.Tensor, ep_world: int, experts_per_rank: int,
+                          workspace: Optional[torch.Tensor] = None, x_active_mask: Optional[torch.Tensor] = None,
+                          zero_experts: int = 0, copy_experts: int = 0, ori_x: Optional[torch.Tensor] = None,
+                          grad_ori_x: Optional[torch.Tensor] = None, const_experts: int = 0,
+                          const_x: Optional[torch.Tensor] = None, grad_const_x: Optional[torch.Tensor] = None):
+    """moe_combine_backward into preallocated grad_expand_x [rows, h] (rows behind the last counted one are left as
+    they were), grad_scales fp32 [N, topk] and, when given, grad_ori_x [N, h] and grad_const_x [const_experts, h], on
+    the current stream. See combine_backward for the rest."""
+    fn = "moe_combine_backward"
+    dev, N, K, h, dt = _row_call(fn, expand_x, expert_ids, ep_world, experts_per_rank)
+    _check_routing(assist_info, ep_recv_count, expert_ids, N, K, ep_world, experts_per_rank, dev)
+    _check_tensor("expand_x", expand_x, expand_x.dtype, (N * K, h), dev)
+    _check_tensor("grad_out", grad_out, expand_x.dtype, (N, h), dev)
+    _check_tensor("expert_scales", expert_scales, torch.float32, (N, K), dev)
+    _check_tensor("grad_expand_x", grad_expand_x, expand_x.dtype, (N * K, h), dev)
+    _check_tensor("grad_scales", grad_scales, torch.float32, (N, K), dev)
+    mp, mk = _mask_args(x_active_mask, N, K, dev)
+    special = None
+    if zero_experts or copy_experts or const_experts:
+        zero_experts, copy_experts, const_experts = int(zero_experts), int(copy_experts), int(const_experts)
+        _check_int(fn, zero_experts | copy_experts | const_experts)
+        for name, count, t, shape in (("ori_x", copy_experts, ori_x, (N, h)),
+                                      ("const_x", const_experts, const_x, (const_experts, h))):
+            if count and t is None:
+                raise MoeError(fn, MOE_ERR_NULLPTR, "%s is needed: it was combine's" % name)
+            if count:
+                _check_tensor(name, t, expand_x.dtype, shape, dev)
+        special = _special(zero_experts, copy_experts, ori_x, const_experts, const_x)
+    for name, count, t, shape in (("grad_ori_x", copy_experts, grad_ori_x, (N, h)),
+                                  ("grad_const_x", const_experts, grad_const_x, (const_experts, h))):
+        if t is None:
+            continue
+        if not count:
+            raise MoeError(fn, MOE_ERR_NULLPTR, "%s without such experts" % name)
+        _check_tensor(name, t, expand_x.dtype, shape, dev)
+    if grad_const_x is not None and workspace is None:
+        workspace = combine_backward_workspace(ep_world, N // ep_world, experts_per_rank, h, K, expand_x.dtype,
+                                               const_experts, dev)
+    elif workspace is not None:
+        _check_tensor("workspace", workspace, torch.uint8, (workspace.numel(),), dev)
+    _launch(fn, dev, grad_out.data_ptr(), expand_x.data_ptr(), assist_info.data_ptr(), ep_recv_count.data_ptr(),
+            expert_ids.data_ptr(), expert_scales.data_ptr(), mp, mk, special, ep_world, N // ep_world, experts_per_rank, h,
+            K, dt, grad_expand_x.data_ptr(), grad_scales.data_ptr(), _address(grad_ori_x), _address(grad_const_x),
+            _address(workspace), 0 if workspace is None else workspace.numel(), _stream_ptr(dev))
+    return grad_expand_x, grad_scales
+
+
+def combine_backward(grad_out: torch.Tensor, expand_x: torch.Tensor, assist_info: torch.Tensor,
+                     ep_recv_count: torch.Tensor, expert_ids: torch.Tensor, expert_scales: torch.Tensor, ep_world: int,
+                     experts_per_rank: int, x_active_mask: Optional[torch.Tensor] = None, zero_experts: int = 0,
+                     copy_experts: int = 0, ori_x: Optional[torch.Tensor] = None, const_experts: int = 0,
+                     const_x: Optional[torch.Tensor] = None):
+    """Gradients of combine's inputs from grad_out [N, h], the gradient of its x_out; the other arguments are the
+    combine's (fp16 or bf16 rows).
+
+    Returns (grad_expand_x [rows, h], grad_scales fp32 [N, topk]), then grad_ori_x [N, h] with copy experts and
+    grad_const_x [const_experts, h] with const experts. grad_expand_x[row(t, k)] = expert_scales[t, k] * grad_out[t], rows
+    behind the last counted one uninitialised; grad_scales[t, k] is the product of the pair's row (ori_x[t], const_x[j])
+    with grad_out[t], and 0 for a zero expert's or an inactive pair: gate_backward takes it.
+    """
+    _gpu_device("expand_x", expand_x)
+    _gpu_device("expert_ids", expert_ids)
+    dev = expand_x.device
+    made = (torch.empty_like(expand_x), _new(tuple(expert_ids.shape), torch.float32, dev))
+    ori = torch.empty_like(ori_x) if copy_experts and ori_x is not None else None
+    const = torch.empty_like(const_x) if const_experts and const_x is not None else None
+    combine_backward_into(*made, grad_out, expand_x, assist_info, ep_recv_count, expert_ids, expert_scales, ep_world,
+                          experts_per_rank, None, x_active_mask, zero_experts, copy_experts, ori_x, ori, const_experts,
+                          const_x, const)
+    return made + tuple(t for t in (ori, const) if t is not None)
+
+
+def dispatch_backward_into(grad_x: torch.Tensor, grad_expand_x: torch.Tensor, assist_info: torch.Tensor,
+                           ep_recv_count: torch.Tensor, expert_ids: torch.Tensor, ep_world: int, experts_per_rank: int,
+                           x_active_mask: Optional[torch.Tensor] = None, add: Optional[torch.Tensor] = None,
+                           grad_expand_scales: Optional[torch.Tensor] = None,
+                           grad_scales: Optional[torch.Tensor] = None):
+    """moe_dispatch_backward into a preallocated grad_x [N, h] (which may be add itself) and, with grad_expand_scales,
+    grad_scales fp32 [N, topk], on the current stream. See dispatch_backward for the rest."""
+    fn = "moe_dispatch_backward"
+    dev, N, K, h, dt = _row_call(fn, grad_expand_x, expert_ids, ep_world, experts_per_rank)
+    _check_routing(assist_info, ep_recv_count, expert_ids, N, K, ep_world, experts_per_rank, dev)
+    dtype = grad_expand_x.dtype
+    _check_tensor("grad_expand_x", grad_expand_x, dtype, (N * K, h), dev)
+    _check_tensor("grad_x", grad_x, dtype, (N, h), dev)
+    if add is not None:
+        _check_tensor("add", add, dtype, (N, h), dev)
+    if (grad_expand_scales is None) != (grad_scales is None):
+        raise MoeError(fn, MOE_ERR_NULLPTR, "grad_expand_scales and grad_scales go together")
+    if grad_scales is not None:
+        _check_tensor("grad_expand_scales", grad_expand_scales, torch.float32, (N * K,), dev)
+        _check_tensor("grad_scales", grad_scales, torch.float32, (N, K), dev)
+    mp, mk = _mask_args(x_active_mask, N, K, dev)
+    _launch(fn, dev, grad_expand_x.data_ptr(), assist_info.data_ptr(), ep_recv_count.data_ptr(), expert_ids.data_ptr(),
+            _address(grad_expand_scales), _address(add), mp, mk, ep_world, N // ep_world, experts_per_rank, h, K, dt,
+            grad_x.data_ptr(), _address(grad_scales), _stream_ptr(dev))
+    return grad_x
+
+
+def dispatch_backward(grad_expand_x: torch.Tensor, assist_info: torch.Tensor, ep_recv_count: torch.Tensor,
+                      expert_ids: torch.Tensor, ep_world: int, experts_per_rank: int,
+                      x_active_mask: Optional[torch.Tensor] = None, add: Optional[torch.Tensor] = None,
+                      grad_expand_scales: Optional[torch.Tensor] = None):
+    """Gradient of dispatch's tokens from grad_expand_x [rows, h] (fp16 or bf16), the gradient of its expand_x (or of
+    what its codes stand for): grad_x[t] is the sum of the rows of t's pairs, plus add[t], in fp32, rounded once. add
+    [N, h] is what else flows back to the tokens, combine_backward's grad_ori_x among it. With grad_expand_scales
+    fp32 [rows], the gradient of dispatch's expand_scales, returns (grad_x, grad_scales fp32 [N, topk]), else
+    grad_x [N, h]. Pairs of special experts and inactive ones have no row and get 0."""
+    _gpu_device("grad_expand_x", grad_expand_x)
+    _gpu_device("expert_ids", expert_ids)
+    if grad_expand_x.dim() != 2 or expert_ids.dim() != 2:
+        raise MoeError("moe_dispatch_backward", MOE_ERR_SHAPE, "grad_expand_x and expert_ids must be 2-D")
+    dev, (N, K) = grad_expand_x.device, expert_ids.shape
+    out = _new((N, grad_expand_x.shape[1]), grad_expand_x.dtype, dev)
+    scales = _new((N, K), torch.float32, dev) if grad_expand_scales is not None else None
+    dispatch_backward_into(out, grad_expand_x, assist_info, ep_recv_count, expert_ids, ep_world, experts_per_rank,
+                           x_active_mask, add, grad_expand_scales, scales)
+    return out if scales is None else (out, scales)
+
+
+# ---- the gate ----
 
 def _logits(fn, logits):
     """(device, tokens, experts, dtype code) of a gate's logits, checked."""

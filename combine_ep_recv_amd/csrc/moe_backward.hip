@@ -1,0 +1,568 @@
+// moe_backward.hip -- the gradients of combine and dispatch (gfx950, wave64).
+//
+// With g the gradient of x_out, y the experts' rows and w the weights (row(t, k) is the row that dispatch gave to pair
+// (t, k)):
+//   combine   grad_y[row(t, k)] = w[t, k] * g[t]
+//             grad_w[t, k] = sum over the columns of y[row(t, k)] * g[t]; 0 for a pair without a row, except that a copy
+//             expert's row is ori_x[t] and const expert j's const_x[j]
+//             grad_ori_x[t] = (sum over copy pairs of w[t, k]) * g[t]
+//             grad_const_x[j] = sum over const expert j's pairs of w[t, k] * g[t]
+//   dispatch  grad_x[t] = add[t] + sum over k of grad_expand_x[row(t, k)]
+// Everything is held in fp32 and rounded once, and every sum has a fixed order.
+
+#include "moe_types.h"
+
+#include <limits.h>
+
+#include <algorithm>
+
+namespace {
+
+using namespace moe_detail;
+
+constexpr int kMaxExperts = 1024, kMinWorld = 2, kMaxWorld = 768;      // dispatch's limits
+constexpr long long kMaxTokens = (1ll << 24) - 1;
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kPiece = 8;                  // elements of 16 bytes
+constexpr int kNone = -1, kCopy = -2, kConst = -3;      // a pair without a row, of a copy expert, of const expert kConst - j
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));      // rows start at any element
+
+struct Routing {
+    const int32_t *assist, *erc, *ids;
+    const uint8_t *mask;
+    int mask_kind;
+    int W, bs, K, epr, E, S, R;
+    int zero_end, copy_end, const_end;     // special ids: [zero_end, copy_end) copy, [copy_end, const_end) const
+};
+
+// Tokens' rows in LDS: where each rank's rows begin, and the row (or kNone, kCopy, kConst - j) of each of a token's pairs.
+struct Rows {
+    uint32_t before[kMaxWorld];
+    int row[kMaxExperts];
+};
+
+// Finds the rows of token t's pairs: pair (t, k) lies in segment (local expert, source rank) of its expert's rank, whose
+// rows are in order of their tokens, so that assist_info's token column is searched by halves. (No pass over all
+// rows first, as combine's slots: a segment has few rows, and the search's loads hit the L2.) The first wavefront calls it;
+// the caller puts a barrier behind it. Whatever the arrays hold, rows stay in [0, R).
+__device__ __forceinline__ void find_rows(const Routing &a, int t, Rows &rows)
+{
+    const int lane = threadIdx.x;
+    const int s = t / a.bs, tok = t - s * a.bs;
+    uint32_t carry = 0;
+    for (int q = 0; q < a.W; q += kWave) {
+        const int rank = q + lane;
+        const int total = rank < a.W ? a.erc[(size_t)rank * a.S + a.S - 1] : 0;
+        const uint32_t inc = min((uint32_t)a.R, wave_scan((uint32_t)min(max(total, 0), a.R), (uint32_t)a.R) + carry);
+        // the sums before this rank: one lane up
+        const uint32_t before = (uint32_t)__builtin_amdgcn_update_dpp((int)carry, (int)inc, 0x138, 0xf, 0xf, false);
+        if (rank < a.W) rows.before[rank] = before;
+        carry = (uint32_t)__builtin_amdgcn_readlane((int)inc, kWave - 1);
+    }
+    wave_fence();
+    for (int k = lane; k < a.K; k += kWave) {
+        const size_t p = (size_t)t * a.K + k;
+        const int e = a.ids[p];
+        bool on = true;
+        if (a.mask_kind != MOE_MASK_NONE) on = a.mask[a.mask_kind == MOE_MASK_TOKEN ? (size_t)t : p] != 0;
+        int row = kNone;
+        if (on && (unsigned)e < (unsigned)a.E) {
+            const int r = e / a.epr, seg = (e - r * a.epr) * a.W + s;
+            const int32_t *c = a.erc + (size_t)r * a.S + seg;
+            const uint32_t base = rows.before[r];
+            uint32_t lo = seg ? (uint32_t)min(max(c[-1], 0), a.R) : 0u, hi = (uint32_t)min(max(c[0], 0), a.R);
+            lo = min((uint32_t)a.R, base + lo);
+            hi = min((uint32_t)a.R, base + hi);
+            const uint32_t end = hi;
+            while (lo < hi) {
+                const uint32_t mid = (lo + hi) >> 1;
+                if (a.assist[(size_t)mid * 3 + 1] < tok) lo = mid + 1;
+                else hi = mid;
+            }
+            if (lo < end && a.assist[(size_t)lo * 3 + 1] == tok) row = (int)lo;
+        } else if (on && e >= a.zero_end && e < a.const_end) {
+            row = e < a.copy_end ? kCopy : kConst - (e - a.copy_end);
+        }
+        rows.row[k] = row;
+    }
+}
+
+__device__ __forceinline__ u32x4 load16(const void *p)
+{
+    return __builtin_nontemporal_load(static_cast<const u32x4_a2 *>(p));
+}
+__device__ __forceinline__ void store16(void *p, u32x4 v)
+{
+    __builtin_nontemporal_store(v, static_cast<u32x4_a2 *>(p));
+}
+template <class T>
+__device__ __forceinline__ void unpack(u32x4 v, float (&x)[kPiece])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = T::load((uint16_t)(v[i] & 0xffff));
+        x[2 * i + 1] = T::load((uint16_t)(v[i] >> 16));
+    }
+}
+template <class T>
+__device__ __forceinline__ u32x4 pack(const float (&x)[kPiece])
+{
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (uint32_t)T::store(x[2 * i]) | ((uint32_t)T::store(x[2 * i + 1]) << 16);
+    return v;
+}
+
+// a * b as binary32, also on its way to 16 bits. (The compiler folds the product and fp16's rounding into a fused
+// multiply-add to +0, which turns -0 into +0.)
+__device__ __forceinline__ float product(float a, float b)
+{
+    float p = a * b;
+    asm("" : "+v"(p));
+    return p;
+}
+
+// --------------------------------------------------------------------------
+// combine
+// --------------------------------------------------------------------------
+
+struct CombineBackwardArgs {
+    Routing r;
+    const uint16_t *grad, *y, *ori_x, *const_x;
+    const float *w;
+    uint16_t *grad_y, *grad_ori;
+    float *grad_w;
+    int h, parts;
+};
+
+// A workgroup takes token t and every `parts`th block of KB of its pairs. Rows in pieces of 16 bytes a lane, the h % 8 last
+// elements one a lane.
+template <class T, int KB>
+__global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineBackwardArgs a)
+{
+    __shared__ Rows rows;
+    __shared__ float part[kWaves][KB];
+    const int t = blockIdx.x / a.parts, first = blockIdx.x - t * a.parts;
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    const int K = a.r.K, pieces = a.h / kPiece, tail = a.h - pieces * kPiece, rest = pieces * kPiece + min(tid, tail);
+    if (wave == 0) find_rows(a.r, t, rows);
+    __syncthreads();
+    const uint16_t *g = a.grad + (size_t)t * a.h;
+    for (int kb = first * KB; kb < K; kb += a.parts * KB) {
+        const uint16_t *src[KB];
+        int row[KB];
+        float w[KB], acc[KB];
+#pragma unroll
+        for (int i = 0; i < KB; ++i) {
+            row[i] = __builtin_amdgcn_readfirstlane(kb + i < K ? rows.row[kb + i] : kNone);
+            w[i] = kb + i < K ? a.w[(size_t)t * K + kb + i] : 0.f;
+            // a pair without a row reads the gradient's again, which is in the cache: a load that hangs on the pair would
+            // have the others waited for
+            src[i] = row[i] >= 0       ? a.y + (size_t)row[i] * a.h
+                     : row[i] == kNone ? g
+                     : row[i] == kCopy ? a.ori_x + (size_t)t * a.h
+                                       : a.const_x + (size_t)(kConst - row[i]) * a.h;
+            acc[i] = 0.f;
+        }
+        for (int c = tid; c < pieces; c += kThreads) {
+            u32x4 v[KB];
+            const u32x4 gv = *reinterpret_cast<const u32x4_a2 *>(g + c * kPiece);
+#pragma unroll
+            for (int i = 0; i < KB; ++i)
+                v[i] = load16(src[i] + c * kPiece);
+            float gx[kPiece];
+            unpack<T>(gv, gx);
+#pragma unroll
+            for (int i = 0; i < KB; ++i) {
+                float x[kPiece], o[kPiece];
+                unpack<T>(v[i], x);
+#pragma unroll
+                for (int j = 0; j < kPiece; ++j) {
+                    acc[i] = __builtin_fmaf(x[j], gx[j], acc[i]);
+                    o[j] = product(w[i], gx[j]);
+                }
+                if (row[i] >= 0) store16(a.grad_y + (size_t)row[i] * a.h + c * kPiece, pack<T>(o));
+            }
+        }
+        if (tid < tail) {
+            const float gx = T::load(g[rest]);
+#pragma unroll
+            for (int i = 0; i < KB; ++i) {
+                acc[i] = __builtin_fmaf(T::load(src[i][rest]), gx, acc[i]);
+                if (row[i] >= 0) a.grad_y[(size_t)row[i] * a.h + rest] = T::store(product(w[i], gx));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < KB; ++i) {
+            const float v = wave_sum(acc[i]);
+            if (lane == 0) part[wave][i] = v;
+        }
+        __syncthreads();
+        if (tid < KB && kb + tid < K) {
+            float v = part[0][tid];
+#pragma unroll
+            for (int i = 1; i < kWaves; ++i) v += part[i][tid];
+            a.grad_w[(size_t)t * K + kb + tid] = rows.row[kb + tid] == kNone ? 0.f : v;
+        }
+        __syncthreads();
+    }
+    if (a.grad_ori && first == 0) {
+        float w = 0.f;
+        for (int k = lane; k < K; k += kWave)
+            if (rows.row[k] == kCopy) w += a.w[(size_t)t * K + k];
+        w = wave_sum(w);
+        uint16_t *o = a.grad_ori + (size_t)t * a.h;
+        for (int c = tid; c < pieces; c += kThreads) {
+            float x[kPiece];
+            unpack<T>(*reinterpret_cast<const u32x4_a2 *>(g + c * kPiece), x);
+#pragma unroll
+            for (int j = 0; j < kPiece; ++j) x[j] = product(w, x[j]);
+            store16(o + c * kPiece, pack<T>(x));
+        }
+        if (tid < tail) o[rest] = T::store(product(w, T::load(g[rest])));
+    }
+}
+
+// The const experts' table: every pair adds to one row of it. A workgroup takes expert j, a slice of columns and a part of
+// the tokens: it lists the part's pairs of expert j in order, then adds their rows, and a second kernel joins the parts.
+constexpr int kScan = 4 * kThreads;        // pairs looked at between two lists
+constexpr int kSliceCols = kThreads * kPiece;
+constexpr int kMostSplits = 64, kSplitTokens = 256;
+
+struct ConstArgs {
+    const uint16_t *grad;
+    const float *w;
+    const int32_t *ids;
+    const uint8_t *mask;
+    float *sums;                           // [const experts, splits, h], or NULL where one part is all
+    uint16_t *out;
+    int mask_kind, N, K, h, first_id, slices, splits, per, join_slices;
+};
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void const_backward_kernel(ConstArgs a)
+{
+    __shared__ int list[kScan];
+    __shared__ int count[4][kWaves];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    const int j = blockIdx.x / (a.slices * a.splits), q = blockIdx.x - j * (a.slices * a.splits);
+    const int split = q / a.slices;
+    const long long col = (long long)(q - split * a.slices) * kSliceCols + tid * kPiece;
+    const int id = a.first_id + j;
+    const int live = (int)min(max(a.h - col, 0ll), (long long)kPiece);              // columns of this lane
+    const long long from = (long long)split * a.per * a.K, to = min((long long)a.N, (long long)(split + 1) * a.per) * a.K;
+    float acc[kPiece];
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) acc[i] = 0.f;
+    for (long long base = from; base < to; base += kScan) {
+        uint64_t hit[4];
+        bool mine[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const long long p = base + u * kThreads + tid;
+            mine[u] = p < to && a.ids[p] == id;
+            if (mine[u] && a.mask_kind != MOE_MASK_NONE)
+                mine[u] = a.mask[a.mask_kind == MOE_MASK_TOKEN ? p / a.K : p] != 0;
+            hit[u] = __builtin_amdgcn_ballot_w64(mine[u]);
+            if (lane == 0) count[u][wave] = __popcll(hit[u]);
+        }
+        __syncthreads();
+        int total = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            int at = total;
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) {
+                if (i < wave) at += count[u][i];
+                total += count[u][i];
+            }
+            if (mine[u]) list[at + __popcll(hit[u] & ((1ull << lane) - 1))] = (int)(base + u * kThreads + tid);
+        }
+        __syncthreads();
+        for (int i = 0; i < total; ++i) {
+            const int p = list[i];
+            const float w = a.w[p];
+            const uint16_t *g = a.grad + (size_t)(p / a.K) * a.h + col;
+            if (live == kPiece) {
+                float x[kPiece];
+                unpack<T>(*reinterpret_cast<const u32x4_a2 *>(g), x);
+#pragma unroll
+                for (int c = 0; c < kPiece; ++c) acc[c] = __builtin_fmaf(w, x[c], acc[c]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < kPiece; ++c)
+                    if (c < live) acc[c] = __builtin_fmaf(w, T::load(g[c]), acc[c]);
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int c = 0; c < kPiece; ++c) {
+        if (c >= live) continue;
+        if (a.sums) a.sums[((size_t)j * a.splits + split) * a.h + col + c] = acc[c];
+        else a.out[(size_t)j * a.h + col + c] = T::store(acc[c]);
+    }
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void const_join_kernel(ConstArgs a)
+{
+    const int j = blockIdx.x / a.join_slices;
+    const long long col = (long long)(blockIdx.x - j * a.join_slices) * kThreads + threadIdx.x;
+    if (col >= a.h) return;
+    float v = 0.f;
+    for (int i = 0; i < a.splits; ++i) v += a.sums[((size_t)j * a.splits + i) * a.h + col];
+    a.out[(size_t)j * a.h + col] = T::store(v);
+}
+
+// --------------------------------------------------------------------------
+// dispatch
+// --------------------------------------------------------------------------
+
+struct DispatchBackwardArgs {
+    Routing r;
+    const uint16_t *grad, *add;
+    const float *grad_scales_in;
+    uint16_t *out;
+    float *grad_scales;
+    int h, slices;
+};
+
+// A workgroup takes token t and every `slices`th 256 pieces of its row.
+template <class T>
+__global__ __launch_bounds__(kThreads) void dispatch_backward_kernel(DispatchBackwardArgs a)
+{
+    __shared__ Rows rows;
+    const int t = blockIdx.x / a.slices, slice = blockIdx.x - t * a.slices;
+    const int tid = threadIdx.x, K = a.r.K, pieces = a.h / kPiece, tail = a.h - pieces * kPiece;
+    if (tid < kWave) find_rows(a.r, t, rows);
+    __syncthreads();
+    constexpr int KB = 8;
+    for (int c = slice * kThreads + tid; c < pieces; c += a.slices * kThreads) {
+        float acc[kPiece];
+        u32x4 v[KB];
+        if (a.add) {
+            unpack<T>(load16(a.add + (size_t)t * a.h + c * kPiece), acc);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) acc[i] = 0.f;
+        }
+        for (int kb = 0; kb < K; kb += KB) {
+            int row[KB];
+#pragma unroll
+            for (int i = 0; i < KB; ++i) {
+                row[i] = __builtin_amdgcn_readfirstlane(kb + i < K ? rows.row[kb + i] : kNone);
+                v[i] = load16(a.grad + (size_t)max(row[i], 0) * a.h + c * kPiece);        // without a row: see above
+            }
+#pragma unroll
+            for (int i = 0; i < KB; ++i) {
+                if (row[i] < 0) continue;
+                float x[kPiece];
+                unpack<T>(v[i], x);
+#pragma unroll
+                for (int j = 0; j < kPiece; ++j) acc[j] += x[j];
+            }
+        }
+        store16(a.out + (size_t)t * a.h + c * kPiece, pack<T>(acc));
+    }
+    if (slice == 0 && tid < tail) {
+        const int rest = pieces * kPiece + tid;
+        float v = a.add ? T::load(a.add[(size_t)t * a.h + rest]) : 0.f;
+        for (int k = 0; k < K; ++k)
+            if (rows.row[k] >= 0) v += T::load(a.grad[(size_t)rows.row[k] * a.h + rest]);
+        a.out[(size_t)t * a.h + rest] = T::store(v);
+    }
+    if (slice == 0 && a.grad_scales)
+        for (int k = tid; k < K; k += kThreads)
+            a.grad_scales[(size_t)t * K + k] = rows.row[k] >= 0 ? a.grad_scales_in[rows.row[k]] : 0.f;
+}
+
+// --------------------------------------------------------------------------
+// host side
+// --------------------------------------------------------------------------
+
+int check_call(int W, int bs, int epr, int h, int K, int dtype)
+{
+    if (dtype != MOE_FP16 && dtype != MOE_BF16) return MOE_ERR_DTYPE;
+    if (W < kMinWorld || W > kMaxWorld || epr < 1 || bs < 0 || h < 1 || K < 1) return MOE_ERR_SHAPE;
+    const long long E = (long long)W * epr, N = (long long)W * bs;
+    if (E > kMaxExperts || K > E || N > kMaxTokens || N * K > INT_MAX) return MOE_ERR_SHAPE;
+    // dispatch's bound on a token's slices of 128 elements
+    if (N * ((h + 127ll) / 128) >= 1ll << 25) return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+int check_mask(const uint8_t *mask, int kind, long long N)
+{
+    if (kind < MOE_MASK_NONE || kind > MOE_MASK_PAIR) return MOE_ERR_MASK;
+    if ((kind != MOE_MASK_NONE) != (mask != nullptr) && N > 0) return MOE_ERR_MASK;
+    return kind == MOE_MASK_NONE && mask ? MOE_ERR_MASK : MOE_OK;
+}
+
+Routing routing_of(const int32_t *assist, const int32_t *erc, const int32_t *ids, const uint8_t *mask, int mask_kind, int W,
+                   int bs, int epr, int K)
+{
+    Routing r;
+    r.assist = assist;
+    r.erc = erc;
+    r.ids = ids;
+    r.mask = mask;
+    r.mask_kind = mask_kind;
+    r.W = W;
+    r.bs = bs;
+    r.K = K;
+    r.epr = epr;
+    r.E = r.S = W * epr;
+    r.R = (int)((long long)W * bs * K);
+    r.zero_end = r.copy_end = r.const_end = r.E;
+    return r;
+}
+
+// Parts of the tokens for the const experts' sums: by the tokens alone, so that a sum's order does not change with h.
+int splits_of(long long N) { return (int)std::min<long long>(kMostSplits, (N + kSplitTokens - 1) / kSplitTokens); }
+
+}  // namespace
+
+extern "C" {
+
+int moe_combine_backward_workspace_size(int ep_world, int bs, int experts_per_rank, int h, int topk, int dtype,
+                                        int const_expert_num, size_t *bytes)
+{
+    if (!bytes) return MOE_ERR_NULLPTR;
+    const int rc = check_call(ep_world, bs, experts_per_rank, h, topk, dtype);
+    if (rc) return rc;
+    const int splits = splits_of((long long)ep_world * bs);
+    // workgroups of both kernels of the const experts' gradient are counted in 24 bits, their threads in 32
+    const long long most = std::max((h + kSliceCols - 1ll) / kSliceCols * std::max(splits, 1), (h + kThreads - 1ll) / kThreads);
+    if (const_expert_num < 0 || const_expert_num * most >= 1ll << 24) return MOE_ERR_SHAPE;
+    *bytes = splits > 1 ? (size_t)const_expert_num * splits * h * sizeof(float) : 0;
+    return MOE_OK;
+}
+
+int moe_combine_backward(const void *grad_out, const void *expand_x, const int32_t *assist_info, const int32_t *ep_recv_count,
+                         const int32_t *expert_ids, const float *expert_scales, const uint8_t *x_active_mask, int mask_kind,
+                         const moe_special_experts *special, int ep_world, int bs, int experts_per_rank, int h, int topk,
+                         int dtype, void *grad_expand_x, float *grad_scales, void *grad_ori_x, void *grad_const_x,
+                         void *workspace, size_t workspace_bytes, void *stream)
+{
+    const int zero_n = special ? special->zero_expert_num : 0, copy_n = special ? special->copy_expert_num : 0;
+    const int const_n = special ? special->const_expert_num : 0;
+    size_t need = 0;
+    int rc = check_call(ep_world, bs, experts_per_rank, h, topk, dtype);
+    if (rc) return rc;
+    if (zero_n < 0 || copy_n < 0 || const_n < 0) return MOE_ERR_SHAPE;
+    const long long N = (long long)ep_world * bs, E = (long long)ep_world * experts_per_rank;
+    if (E + zero_n + copy_n + const_n > INT_MAX) return MOE_ERR_SHAPE;
+    const int table = const_n > 0 && grad_const_x ? const_n : 0;
+    if ((rc = moe_combine_backward_workspace_size(ep_world, bs, experts_per_rank, h, topk, dtype, table, &need))) return rc;
+    if (!ep_recv_count) return MOE_ERR_NULLPTR;
+    if (N > 0 && (!grad_out || !expand_x || !assist_info || !expert_ids || !expert_scales || !grad_expand_x || !grad_scales))
+        return MOE_ERR_NULLPTR;
+    if ((rc = check_mask(x_active_mask, mask_kind, N))) return rc;
+    const void *ori_x = copy_n > 0 ? special->ori_x : nullptr, *const_x = const_n > 0 ? special->const_x : nullptr;
+    if (N > 0 && ((copy_n > 0 && !ori_x) || (const_n > 0 && !const_x))) return MOE_ERR_NULLPTR;
+    if ((grad_ori_x && copy_n == 0) || (grad_const_x && const_n == 0)) return MOE_ERR_NULLPTR;
+    if (need > 0 && !workspace) return MOE_ERR_NULLPTR;
+    if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    if (!aligned(grad_out, 2) || !aligned(expand_x, 2) || !aligned(assist_info, 4) || !aligned(ep_recv_count, 4) ||
+        !aligned(expert_ids, 4) || !aligned(expert_scales, 4) || !aligned(grad_expand_x, 2) || !aligned(grad_scales, 4) ||
+        !aligned(ori_x, 2) || !aligned(const_x, 2) || !aligned(grad_ori_x, 2) || !aligned(grad_const_x, 2) ||
+        (need > 0 && !aligned(workspace, 16)))
+        return MOE_ERR_ALIGN;
+    if (N == 0 && table == 0) return MOE_OK;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    (void)hipGetLastError();
+    if (N > 0) {
+        CombineBackwardArgs a;
+        a.r = routing_of(assist_info, ep_recv_count, expert_ids, x_active_mask, mask_kind, ep_world, bs, experts_per_rank, topk);
+        a.r.zero_end = a.r.E + zero_n;
+        a.r.copy_end = a.r.zero_end + copy_n;
+        a.r.const_end = a.r.copy_end + const_n;
+        a.grad = static_cast<const uint16_t *>(grad_out);
+        a.y = static_cast<const uint16_t *>(expand_x);
+        a.ori_x = static_cast<const uint16_t *>(ori_x);
+        a.const_x = static_cast<const uint16_t *>(const_x);
+        a.w = expert_scales;
+        a.grad_y = static_cast<uint16_t *>(grad_expand_x);
+        a.grad_ori = static_cast<uint16_t *>(grad_ori_x);
+        a.grad_w = grad_scales;
+        a.h = h;
+        a.parts = 1;
+        const dim3 b(kThreads);
+        if (N * topk <= 4096) {
+            a.parts = topk;
+            const dim3 g((unsigned)(N * a.parts));
+            if (dtype == MOE_FP16) hipLaunchKernelGGL((combine_backward_kernel<F16, 1>), g, b, 0, st, a);
+            else hipLaunchKernelGGL((combine_backward_kernel<BF16, 1>), g, b, 0, st, a);
+        } else {
+            const dim3 g((unsigned)N);
+            if (dtype == MOE_FP16) hipLaunchKernelGGL((combine_backward_kernel<F16, 8>), g, b, 0, st, a);
+            else hipLaunchKernelGGL((combine_backward_kernel<BF16, 8>), g, b, 0, st, a);
+        }
+    }
+    if (table) {
+        ConstArgs c;
+        c.grad = static_cast<const uint16_t *>(grad_out);
+        c.w = expert_scales;
+        c.ids = expert_ids;
+        c.mask = x_active_mask;
+        c.mask_kind = mask_kind;
+        c.N = (int)N;
+        c.K = topk;
+        c.h = h;
+        c.first_id = (int)(E + zero_n + copy_n);
+        c.splits = std::max(1, splits_of(N));
+        c.per = (int)((N + c.splits - 1) / c.splits);
+        c.slices = (int)((h + kSliceCols - 1ll) / kSliceCols);
+        c.join_slices = (int)((h + kThreads - 1ll) / kThreads);
+        c.sums = c.splits > 1 ? static_cast<float *>(workspace) : nullptr;
+        c.out = static_cast<uint16_t *>(grad_const_x);
+        const dim3 g((unsigned)((long long)table * c.slices * c.splits)), b(kThreads);
+        const dim3 join((unsigned)((long long)table * c.join_slices));
+        if (dtype == MOE_FP16) {
+            hipLaunchKernelGGL(const_backward_kernel<F16>, g, b, 0, st, c);
+            if (c.sums) hipLaunchKernelGGL(const_join_kernel<F16>, join, b, 0, st, c);
+        } else {
+            hipLaunchKernelGGL(const_backward_kernel<BF16>, g, b, 0, st, c);
+            if (c.sums) hipLaunchKernelGGL(const_join_kernel<BF16>, join, b, 0, st, c);
+        }
+    }
+    return launched();
+}
+
+int moe_dispatch_backward(const void *grad_expand_x, const int32_t *assist_info, const int32_t *ep_recv_count,
+                          const int32_t *expert_ids, const float *grad_expand_scales, const void *add,
+                          const uint8_t *x_active_mask, int mask_kind, int ep_world, int bs, int experts_per_rank, int h,
+                          int topk, int dtype, void *grad_x, float *grad_scales, void *stream)
+{
+    int rc = check_call(ep_world, bs, experts_per_rank, h, topk, dtype);
+    if (rc) return rc;
+    const long long N = (long long)ep_world * bs;
+    if (!ep_recv_count || (N > 0 && (!grad_expand_x || !assist_info || !expert_ids || !grad_x))) return MOE_ERR_NULLPTR;
+    if (N > 0 && !grad_expand_scales != !grad_scales) return MOE_ERR_NULLPTR;
+    if ((rc = check_mask(x_active_mask, mask_kind, N))) return rc;
+    if (!aligned(grad_expand_x, 2) || !aligned(assist_info, 4) || !aligned(ep_recv_count, 4) || !aligned(expert_ids, 4) ||
+        !aligned(grad_expand_scales, 4) || !aligned(add, 2) || !aligned(grad_x, 2) || !aligned(grad_scales, 4))
+        return MOE_ERR_ALIGN;
+    if (N == 0) return MOE_OK;
+    DispatchBackwardArgs a;
+    a.r = routing_of(assist_info, ep_recv_count, expert_ids, x_active_mask, mask_kind, ep_world, bs, experts_per_rank, topk);
+    a.grad = static_cast<const uint16_t *>(grad_expand_x);
+    a.add = static_cast<const uint16_t *>(add);
+    a.grad_scales_in = grad_expand_scales;
+    a.out = static_cast<uint16_t *>(grad_x);
+    a.grad_scales = grad_scales;
+    a.h = h;
+    a.slices = N < 4096 ? (int)std::min(16ll, (h + kSliceCols - 1ll) / kSliceCols) : 1;
+    const dim3 g((unsigned)(N * a.slices)), b(kThreads);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    (void)hipGetLastError();
+    if (dtype == MOE_FP16) hipLaunchKernelGGL(dispatch_backward_kernel<F16>, g, b, 0, st, a);
+    else hipLaunchKernelGGL(dispatch_backward_kernel<BF16>, g, b, 0, st, a);
+    return launched();
+}
+
+}  // extern "C"

@@ -246,21 +246,6 @@ struct Plan {
     int expert;
 };
 
-// Inclusive sums over the 64 lanes that stop at `most` (which keeps them in 32 bits and in order; sums that never
-// reach it are plain ones).
-__device__ __forceinline__ uint32_t wave_scan(uint32_t v, uint32_t most)
-{
-#define MOE_SCAN_STEP(CTRL, ROWS) v = min(most, v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false));
-    MOE_SCAN_STEP(0x111, 0xf)          // row shifts by 1, 2, 4 and 8
-    MOE_SCAN_STEP(0x112, 0xf)
-    MOE_SCAN_STEP(0x114, 0xf)
-    MOE_SCAN_STEP(0x118, 0xf)
-    MOE_SCAN_STEP(0x142, 0xa)          // the last lane of a row to the next row, of the lower half to the upper one
-    MOE_SCAN_STEP(0x143, 0xc)
-#undef MOE_SCAN_STEP
-    return v;
-}
-
 // Fills the plan for tiles of BM rows and returns their number. The counts are ep_recv_count's differences, held
 // within [0, rows] whatever the array holds. All threads call it.
 template <int BM, int THREADS>

@@ -323,6 +323,62 @@ int moe_combine(const void *expand_x, const int32_t *assist_info, const int32_t 
                 int experts_per_rank, int h, int topk, int dtype, void *x_out,
                 void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- the gradients of combine and dispatch ---- */
+
+/* Phase one of moe_combine_backward: validates the scalars and writes the workspace size (0 without const experts, or
+ * where grad_const_x is not asked for: pass 0 then). */
+int moe_combine_backward_workspace_size(int ep_world, int bs, int experts_per_rank, int h, int topk, int dtype,
+                                        int const_expert_num, size_t *bytes);
+
+/*
+ * Gradient of combine, with g = grad_out, the gradient of x_out:
+ *   grad_expand_x[row(t, k)] = expert_scales[t, k] * g[t]
+ *   grad_scales[t, k]        = sum over the columns of expand_x[row(t, k)] * g[t]; for a copy expert's pair of
+ *                              ori_x[t] * g[t], for const expert j's of const_x[j] * g[t]; 0 for a zero expert's and for an
+ *                              inactive pair, whatever their weights hold
+ *   grad_ori_x[t]            = (sum over t's copy pairs of expert_scales[t, k]) * g[t]
+ *   grad_const_x[j]          = sum over const expert j's pairs of expert_scales[t, k] * g[t]
+ * fp32 throughout, each result rounded once. Where the combined rows were quantised on the way, the gradient is that of the
+ * values that they stood for.
+ *
+ *  grad_out       [N, h] dtype (fp16 or bf16)
+ *  expand_x, assist_info, ep_recv_count, expert_ids, expert_scales, x_active_mask, mask_kind, special: the combine's
+ *  grad_expand_x  [ROWS, h] dtype; rows behind the last that ep_recv_count counts are left as they were
+ *  grad_scales    [N, K] fp32, every element written
+ *  grad_ori_x     [N, h] dtype, every element written, or NULL (not wanted); NULL without copy experts
+ *  grad_const_x   [const_expert_num, h] dtype, every element written, or NULL; NULL without const experts
+ *  workspace      device scratch of at least the queried size, 16-byte aligned; NULL where that is 0
+ * Outputs overlap no input. Any alignment to the elements' size is taken. Ranges as in moe_dispatch, and const experts times
+ * slices of 2048 columns times parts of the tokens (at most 64) below 2^24. Rows are found from ep_recv_count and the tokens in
+ * assist_info, which are dispatch's, unchanged; otherwise the kernels stay in bounds and the outputs are unspecified.
+ * Bitwise deterministic, and the first three outputs' rows do not depend on how many tokens there are.
+ */
+int moe_combine_backward(const void *grad_out, const void *expand_x, const int32_t *assist_info,
+                         const int32_t *ep_recv_count, const int32_t *expert_ids, const float *expert_scales,
+                         const uint8_t *x_active_mask, int mask_kind, const moe_special_experts *special, int ep_world,
+                         int bs, int experts_per_rank, int h, int topk, int dtype, void *grad_expand_x, float *grad_scales,
+                         void *grad_ori_x, void *grad_const_x, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of dispatch: grad_x[t] = add[t] + sum over t's pairs that have a row of grad_expand_x[row(t, k)], in fp32 with k
+ * ascending, rounded once. Special experts' and inactive pairs have no row (so no counts of special experts are needed here:
+ * an id outside [0, E) has none). A copy expert's part of the tokens' gradient is moe_combine_backward's grad_ori_x, which
+ * goes into add. Of a dispatch that quantised, this is the gradient of the values that the codes stand for.
+ *
+ *  grad_expand_x       [ROWS, h] dtype (fp16 or bf16); rows behind the last counted one are not used
+ *  assist_info, ep_recv_count, expert_ids, x_active_mask, mask_kind: the dispatch's, as in moe_combine_backward
+ *  grad_expand_scales  fp32 [ROWS] or NULL: the gradient of dispatch's expand_scales; goes with grad_scales
+ *  add                 [N, h] dtype or NULL: what else flows back to the tokens
+ *  grad_x              [N, h] dtype
+ *  grad_scales         [N, K] fp32 or NULL: grad_expand_scales[row(t, k)], 0 for a pair without a row
+ * Outputs overlap no input (grad_x may be add itself). Ranges as in moe_dispatch; any alignment to the elements' size. Needs no
+ * workspace. A token's results do not depend on the others.
+ */
+int moe_dispatch_backward(const void *grad_expand_x, const int32_t *assist_info, const int32_t *ep_recv_count,
+                          const int32_t *expert_ids, const float *grad_expand_scales, const void *add,
+                          const uint8_t *x_active_mask, int mask_kind, int ep_world, int bs, int experts_per_rank, int h,
+                          int topk, int dtype, void *grad_x, float *grad_scales, void *stream);
+
 /* ---- the gate: the routing that dispatch and combine take ---- */
 
 /* Scores of a token's experts: their softmax, or the sigmoid of each. */
