@@ -45,7 +45,7 @@ MOE_ACT_NONE, MOE_ACT_SWIGLU = 0, 1
 EXPORTS = ("moe_dispatch_workspace_size", "moe_dispatch", "moe_dispatch_noalloc", "moe_combine_workspace_size",
            "moe_combine", "moe_combine_backward_workspace_size", "moe_combine_backward", "moe_dispatch_backward",
            "moe_gate", "moe_gate_backward", "moe_mx_quantize", "moe_mx_dequantize",
-           "moe_expert_product", "moe_status_str")
+           "moe_expert_product", "moe_int8_quantize", "moe_int8_dequantize", "moe_expert_product_int8", "moe_status_str")
 NOALLOC_SCRATCH_BYTES = 32 << 20      # MOE_NOALLOC_SCRATCH_BYTES
 
 
@@ -126,6 +126,12 @@ def library() -> ctypes.CDLL:
     lib.moe_mx_dequantize.restype = I
     lib.moe_expert_product.argtypes = [P, P, I, P, P, P, I, I, I, I, I, I, I, P, P]
     lib.moe_expert_product.restype = I
+    lib.moe_int8_quantize.argtypes = [P, L, I, I, P, P, P]
+    lib.moe_int8_quantize.restype = I
+    lib.moe_int8_dequantize.argtypes = [P, P, L, I, I, P, P]
+    lib.moe_int8_dequantize.restype = I
+    lib.moe_expert_product_int8.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, P, P]
+    lib.moe_expert_product_int8.restype = I
     lib.moe_status_str.argtypes = [I]
     lib.moe_status_str.restype = ctypes.c_char_p
     _lib = lib
@@ -876,10 +882,94 @@ def dequantize_mx(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype 
     return _dequantize(_new(shape, dtype, dev), codes, scales, shape, element)
 
 
-def expert_product_into(out: torch.Tensor, x: torch.Tensor, x_scales: torch.Tensor, weights: torch.Tensor,
+# ---- rows of 8-bit integers ----
+
+def quantize_int8_into(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor):
+    """moe_int8_quantize of x [..., cols] into preallocated codes (int8 [..., cols]) and scales (fp32 [...]), on the
+    current stream."""
+    fn = "moe_int8_quantize"
+    dev = _gpu_device("x", x)
+    shape = tuple(x.shape)
+    if not shape or shape[-1] < 1:
+        raise MoeError(fn, MOE_ERR_SHAPE, "x must have columns")
+    dt = _float_code(fn, x.dtype)
+    _check_int(fn, shape[-1])
+    _check_tensor("x", x, x.dtype, shape, dev)
+    _check_tensor("codes", codes, torch.int8, shape, dev)
+    _check_tensor("scales", scales, torch.float32, shape[:-1], dev)
+    _launch(fn, dev, x.data_ptr(), x.numel() // shape[-1], shape[-1], dt, codes.data_ptr(), scales.data_ptr(),
+            _stream_ptr(dev))
+    return codes, scales
+
+
+def quantize_int8(x: torch.Tensor):
+    """Rows of x [..., cols] (fp16, bf16 or fp32) as int8 codes with one scale each: (codes int8 [..., cols], scales
+    fp32 [...]), scale = max|x| / 127 and code = x / scale rounded to the nearest, ties to even: what dispatch writes
+    under MOE_QUANT_DYN_TOKEN. A row of zeros has scale 0; one with an infinity or NaN has scale NaN and codes 0."""
+    dev = _gpu_device("x", x)
+    shape = tuple(x.shape)
+    if not shape or shape[-1] < 1:
+        raise MoeError("moe_int8_quantize", MOE_ERR_SHAPE, "x must have columns")
+    return quantize_int8_into(_new(shape, torch.int8, dev), torch.empty(shape[:-1], dtype=torch.float32, device=dev), x)
+
+
+def dequantize_int8_into(out: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
+    """moe_int8_dequantize into a preallocated out [..., cols] (fp16, bf16 or fp32) on the current stream."""
+    fn = "moe_int8_dequantize"
+    dev = _gpu_device("codes", codes)
+    _gpu_device("out", out)
+    shape = tuple(codes.shape)
+    if not shape or shape[-1] < 1:
+        raise MoeError(fn, MOE_ERR_SHAPE, "codes must have columns")
+    dt = _float_code(fn, out.dtype)
+    _check_int(fn, shape[-1])
+    _check_tensor("codes", codes, torch.int8, shape, dev)
+    _check_tensor("scales", scales, torch.float32, shape[:-1], dev)
+    _check_tensor("out", out, out.dtype, shape, dev)
+    _launch(fn, dev, codes.data_ptr(), scales.data_ptr(), codes.numel() // shape[-1], shape[-1], dt, out.data_ptr(),
+            _stream_ptr(dev))
+    return out
+
+
+def dequantize_int8(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """What int8 codes [..., cols] and scales fp32 [...] stand for, code * scale, in dtype: quantize_int8's rows, or
+    dispatch's under MOE_QUANT_DYN_TOKEN."""
+    dev = _gpu_device("codes", codes)
+    _float_code("moe_int8_dequantize", dtype)
+    if codes.dim() < 1:
+        raise MoeError("moe_int8_dequantize", MOE_ERR_SHAPE, "codes must have columns")
+    return dequantize_int8_into(_new(tuple(codes.shape), dtype, dev), codes, scales)
+
+
+# ---- the experts' product ----
+
+def _product_int8(out, x, x_scales, weights, weight_scales, ep_recv_count, activation):
+    """moe_expert_product_int8 of tensors on GPUs with the right numbers of dimensions."""
+    fn = "moe_expert_product_int8"
+    dev, (rows, k), (E, n), W = x.device, x.shape, weights.shape[:2], ep_recv_count.shape[0]
+    if W < 1 or E % W:
+        raise MoeError(fn, MOE_ERR_SHAPE, "%d experts are not a multiple of %d ranks" % (E, W))
+    if out.dtype not in (torch.float16, torch.bfloat16):
+        raise MoeError(fn, MOE_ERR_DTYPE, "out must be fp16 or bf16, got %s" % out.dtype)
+    _check_tensor("x", x, torch.int8, (rows, k), dev)
+    if x_scales is not None:
+        _check_tensor("x_scales", x_scales, torch.float32, (rows,), dev)
+    _check_tensor("weights", weights, torch.int8, (E, n, k), dev)
+    _check_tensor("weight_scales", weight_scales, torch.float32, (E, n), dev)
+    _check_tensor("ep_recv_count", ep_recv_count, torch.int32, (W, E), dev)
+    _check_tensor("out", out, out.dtype, (rows, n // 2 if activation == MOE_ACT_SWIGLU else n), dev)
+    _check_int(fn, W | E | rows | k | n | int(activation))
+    _launch(fn, dev, x.data_ptr(), _address(x_scales), weights.data_ptr(), weight_scales.data_ptr(),
+            ep_recv_count.data_ptr(), W, E // W, rows, k, n, int(activation), dtype_code(out.dtype), out.data_ptr(),
+            _stream_ptr(dev))
+    return out
+
+
+def expert_product_into(out: torch.Tensor, x: torch.Tensor, x_scales: Optional[torch.Tensor], weights: torch.Tensor,
                         weight_scales: torch.Tensor, ep_recv_count: torch.Tensor, activation: int = MOE_ACT_NONE):
-    """moe_expert_product into a preallocated out [rows, n] ([rows, n / 2] with MOE_ACT_SWIGLU) in fp16
-    or bf16, on the current stream. Rows behind the last that ep_recv_count counts are left as they were."""
+    """moe_expert_product (or, with int8 rows, moe_expert_product_int8) into a preallocated out [rows, n] ([rows, n / 2]
+    with MOE_ACT_SWIGLU) in fp16 or bf16, on the current stream. Rows behind the last that ep_recv_count counts are left as
+    they were."""
     dev = _gpu_device("x", x)
     _gpu_device("weights", weights)
     _gpu_device("ep_recv_count", ep_recv_count)
@@ -887,6 +977,8 @@ def expert_product_into(out: torch.Tensor, x: torch.Tensor, x_scales: torch.Tens
     if x.dim() != 2 or weights.dim() != 3 or ep_recv_count.dim() != 2 or out.dim() != 2:
         raise MoeError("moe_expert_product", MOE_ERR_SHAPE,
                        "x, weights, ep_recv_count and out must have 2, 3, 2 and 2 dimensions")
+    if x.dtype == torch.int8:
+        return _product_int8(out, x, x_scales, weights, weight_scales, ep_recv_count, activation)
     element, (rows, k) = _mx_rows("x", x)
     E, n = weights.shape[:2]
     W, nb = ep_recv_count.shape[0], -(-k // MX_BLOCK)
@@ -907,15 +999,17 @@ def expert_product_into(out: torch.Tensor, x: torch.Tensor, x_scales: torch.Tens
     return out
 
 
-def expert_product(x: torch.Tensor, x_scales: torch.Tensor, weights: torch.Tensor, weight_scales: torch.Tensor,
+def expert_product(x: torch.Tensor, x_scales: Optional[torch.Tensor], weights: torch.Tensor, weight_scales: torch.Tensor,
                    ep_recv_count: torch.Tensor, activation: int = MOE_ACT_NONE,
                    dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """Each row of dispatch's order times its expert's weights.
 
-    x, x_scales: microscaled rows [rows, k], from dispatch under MOE_QUANT_MX or from quantize_mx;
-    weights, weight_scales: quantize_mx of [E, n, k] in E2M1; ep_recv_count: dispatch's. Returns
-    [rows, n], or with MOE_ACT_SWIGLU [rows, n / 2]: silu(first n / 2 weight rows) * the others. Rows
-    behind the last counted one are uninitialised.
+    Either x, x_scales: microscaled rows [rows, k], from dispatch under MOE_QUANT_MX or from quantize_mx;
+    weights, weight_scales: quantize_mx of [E, n, k] in E2M1. Or x int8 [rows, k] and x_scales fp32 [rows],
+    from dispatch under MOE_QUANT_DYN_TOKEN or from quantize_int8 (x_scales None: 1, for dispatch's rows under
+    MOE_QUANT_STATIC); weights, weight_scales: quantize_int8 of [E, n, k], int8 and fp32 [E, n].
+    ep_recv_count: dispatch's. Returns [rows, n], or with MOE_ACT_SWIGLU [rows, n / 2]: silu(first n / 2
+    weight rows) * the others. Rows behind the last counted one are uninitialised.
     """
     dev = _gpu_device("x", x)
     if x.dim() != 2 or not isinstance(weights, torch.Tensor) or weights.dim() != 3:

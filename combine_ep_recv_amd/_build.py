@@ -8,7 +8,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SRC = os.path.join(CSRC, "moe_ep.hip")
-SRCS = [SRC] + [os.path.join(CSRC, n) for n in ("moe_gate.hip", "moe_mx.hip", "moe_backward.hip")]
+SRCS = [SRC] + [os.path.join(CSRC, n) for n in ("moe_gate.hip", "moe_mx.hip", "moe_int8.hip", "moe_backward.hip")]
 HDR = os.path.join(ROOT, "include", "moe_ep.h")
 LIB = os.path.join(PKG, "libmoe_ep.so")
 

@@ -20,7 +20,6 @@ namespace {
 
 using namespace moe_detail;
 
-constexpr int kMaxExperts = 1024, kMinWorld = 2, kMaxWorld = 768;      // dispatch's limits
 constexpr long long kMaxTokens = (1ll << 24) - 1;
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
@@ -114,15 +113,6 @@ __device__ __forceinline__ u32x4 pack(const float (&x)[kPiece])
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = (uint32_t)T::store(x[2 * i]) | ((uint32_t)T::store(x[2 * i + 1]) << 16);
     return v;
-}
-
-// a * b as binary32, also on its way to 16 bits. (The compiler folds the product and fp16's rounding into a fused
-// multiply-add to +0, which turns -0 into +0.)
-__device__ __forceinline__ float product(float a, float b)
-{
-    float p = a * b;
-    asm("" : "+v"(p));
-    return p;
 }
 
 // --------------------------------------------------------------------------

@@ -1,5 +1,5 @@
-// moe_types.h -- element types, wavefront reductions and pointer checks shared by the gate and the
-// microscaled kernels (gfx950, wave64).
+// moe_types.h -- element types, wavefront reductions and pointer checks shared by the gate, the gradients and the
+// experts' kernels (gfx950, wave64).
 #ifndef MOE_TYPES_H
 #define MOE_TYPES_H
 
@@ -13,6 +13,8 @@
 namespace moe_detail {
 
 constexpr int kWave = 64;
+constexpr int kMaxExperts = 1024;          // dispatch's limits
+constexpr int kMinWorld = 2, kMaxWorld = 768;
 
 // 16- and 32-bit element types: their raw bits, and conversion to and from fp32 (round to nearest, ties to even)
 struct F16 {
@@ -30,6 +32,15 @@ struct F32 {
     static __device__ __forceinline__ float load(raw b) { return __uint_as_float(b); }
     static __device__ __forceinline__ raw store(float f) { return __float_as_uint(f); }
 };
+
+// a * b as binary32, also on its way to 16 bits. (The compiler folds the product and fp16's rounding into a fused
+// multiply-add to +0, which turns -0 into +0.)
+__device__ __forceinline__ float product(float a, float b)
+{
+    float p = a * b;
+    asm("" : "+v"(p));
+    return p;
+}
 
 // One DPP move (row shift or broadcast); lanes without a source get `old`.
 template <int CTRL, int ROWS>

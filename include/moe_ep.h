@@ -483,6 +483,46 @@ int moe_expert_product(const void *x, const uint8_t *x_scales, int element, cons
                        int experts_per_rank, int rows, int k, int n, int activation, int dtype, void *out,
                        void *stream);
 
+/* ---- rows of 8-bit integers and the experts' product on them ---- */
+
+/*
+ * Quantise rows [rows, cols] of fp16, bf16 or fp32 to int8 with one fp32 scale each, as MOE_QUANT_DYN_TOKEN does:
+ * scale = max|x| / 127, code = rint(x / scale) of the correctly rounded quotient, ties to even, in [-127, 127]. A row of zeros
+ * (or one whose scale rounds to 0) has scale 0 and codes 0; a row that holds an infinity or a NaN has scale NaN and codes 0, so
+ * that it comes back as NaN.
+ *  x       [rows, cols], aligned to its elements
+ *  codes   int8 [rows, cols], any alignment
+ *  scales  fp32 [rows]
+ * cols <= 2^30, rows * ceil(cols / 16) <= 2^31 - 256.
+ */
+int moe_int8_quantize(const void *x, int64_t rows, int cols, int dtype, int8_t *codes, float *scales, void *stream);
+
+/* The values that such rows stand for, code * scale in fp32, rounded once to out's dtype (fp16, bf16 or fp32): of
+ * moe_int8_quantize's rows, or of dispatch's under MOE_QUANT_DYN_TOKEN. Layouts and ranges as in moe_int8_quantize. */
+int moe_int8_dequantize(const int8_t *codes, const float *scales, int64_t rows, int cols, int dtype, void *out, void *stream);
+
+/*
+ * Experts' product on rows of 8-bit integers in dispatch's order: with e the expert that ep_recv_count gives `row`,
+ *   out[row, i] = act(x_scales[row] * weight_scales[e, i] * sum over k of x[row, k] * weights[e, i, k])
+ * The sum is exact (32-bit integers); the scales, the activation (moe_activation, as in moe_expert_product) and the products
+ * are fp32, rounded once.
+ *  x              int8 [rows, k], 16-byte aligned: dispatch's expand_x under MOE_QUANT_DYN_TOKEN or MOE_QUANT_STATIC, or
+ *                 moe_int8_quantize's codes
+ *  x_scales       fp32 [rows], or NULL for 1 (static rows, whose coefficient goes into the weights' scales)
+ *  weights        int8 [E, n, k], 16-byte aligned; weight_scales fp32 [E, n]: moe_int8_quantize of the E * n weight rows
+ *  ep_recv_count  [W, S] int32: dispatch's, unchanged
+ *  out            [rows, n], or [rows, n / 2] with MOE_ACT_SWIGLU, fp16 or bf16 (dtype). Rows behind the last that
+ *                 ep_recv_count counts are left as they were
+ * Ranges: ep_world and experts as in moe_dispatch, 0 <= rows < 2^31 - 256, k a multiple of 16 up to 131056 (the sums fit 31 bits
+ * and a sign), n >= 1 (even with SwiGLU), n * k <= 2^31 (MOE_ERR_SHAPE otherwise). Tiles are counted in 31 bits: every call
+ * with (rows / 64 + E) * ceil(n / 64) < 2^31 - 1024 is taken, larger ones as far as their tiles allow. Counts that
+ * ep_recv_count should not hold leave the kernel in bounds and the outputs unspecified. A row's results do not depend on the
+ * other rows. Needs no workspace.
+ */
+int moe_expert_product_int8(const int8_t *x, const float *x_scales, const int8_t *weights, const float *weight_scales,
+                            const int32_t *ep_recv_count, int ep_world, int experts_per_rank, int rows, int k, int n,
+                            int activation, int dtype, void *out, void *stream);
+
 /* A static, human-readable name for a status code. */
 const char *moe_status_str(int status);
 
