@@ -233,12 +233,11 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
 {
     constexpr int kThreads = WM * WN * kWave, kRowsW = WN * NF * 16, kRowsX = WM * FR * 16;
     constexpr int kP = 4 * SUB;                               // 16-byte pieces of a row in a stage
-    constexpr int kLoadsW = kRowsW * kP / kThreads, kLoadsX = kRowsX * kP / kThreads, kLoads = kLoadsW + kLoadsX;
+    constexpr int kLoadsW = kRowsW * kP / kThreads, kLoadsX = kRowsX * kP / kThreads;
     constexpr int kSizeW = kRowsW * kP, kSize = kSizeW + kRowsX * kP;
     constexpr int kBytes = kP * 16;                           // of a row in a stage
     static_assert(kRowsW * kP % kThreads == 0 && kRowsX * kP % kThreads == 0, "every thread carries as many pieces");
     static_assert(RING >= 2 && RING <= 4 && RING * SUB % 2 == 0, "a fragment's registers are known where it is used");
-    constexpr int LAST = FR < 2 ? FR : 2;
     // a stage's weights, then its inputs; an array a stage, so that the compiler tells them apart
     __shared__ u32x4 l0[kSize], l1[kSize], l2[RING > 2 ? kSize : 1], l3[RING > 3 ? kSize : 1];
     __shared__ float sw[kRowsW], sx[kRowsX];
@@ -252,15 +251,20 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
     const int half = a.n / 2, stages = a.k / kBytes;
     // piece p of row q in LDS
     auto place = [](int q, int p) { return kP == 8 ? q * 8 + (p ^ (q & 7)) : q * 4 + (p ^ ((q >> 1) & 3)); };
-    // a reader's pieces in each step: of fragment 0, the others lie 16 rows apart
+    // a reader's pieces in each step: of fragment 0; the weights' others lie 16 rows apart, the inputs' 16 * WM (so that a
+    // tile with few rows has as many for each wavefront)
     int wfrag[SUB], xfrag[SUB];
 #pragma unroll
     for (int u = 0; u < SUB; ++u) {
         wfrag[u] = wn * kOwn * kP + place(r, 4 * u + g);
-        xfrag[u] = kSizeW + wm * FR * 16 * kP + place(r, 4 * u + g);
+        xfrag[u] = kSizeW + wm * 16 * kP + place(r, 4 * u + g);
     }
     // the piece that this thread fetches of its rows (rows of its later pieces are a multiple of 8 on)
     const int piece = kP == 8 ? tid % 8 ^ (tid / 8 % 8) : tid % 4 ^ (tid / 8 % 4);
+
+    // Each XCD (workgroups go to the eight in turn) begins an eighth of the stages further on, and after the last one comes
+    // the first: the sums are whole numbers, whose order does not matter, and the XCDs read different memory at a time.
+    const int turn = (int)(blockIdx.x % 8) * stages / 8;
 
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
         const Tile tile = find_tile<kRowsX, kThreads>(a, plan, t / a.ntiles);
@@ -287,15 +291,20 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
         for (int f = 0; f < FR; ++f)
 #pragma unroll
             for (int j = 0; j < NF; ++j) acc[f][j] = i32x4{0, 0, 0, 0};
-        // Fetches of whole stages. Beyond the last one the last one is fetched again, and not used: a branch here would
-        // part the steps that it stands between, and the waits count the fetches.
-        auto fetch = [&](int stage, int slot) {
-            const uint32_t at = min(stage, stages - 1) * kBytes;
+        // Fetches FROM..TO-1 of a whole stage's: the weights', then `loads` of the inputs'. Beyond the last stage the last
+        // one is fetched again, and not used: a branch here would part the steps that it stands between, and the waits
+        // count the fetches.
+        auto fetch = [&](auto loads, int stage, int slot, int from, int to) {
+            int at = min(stage, stages - 1) + turn;
+            at -= at >= stages ? stages : 0;
             u32x4 *wl = ring(slot), *xl = wl + kSizeW;
 #pragma unroll
-            for (int i = 0; i < kLoadsW; ++i) fetch_lds(wbuf, wo[i], at, wl + i * kThreads + wave * kWave);
-#pragma unroll
-            for (int i = 0; i < kLoadsX; ++i) fetch_lds(xbuf, xo[i], at, xl + i * kThreads + wave * kWave);
+            for (int i = from; i < to; ++i) {
+                if (i < kLoadsW)
+                    fetch_lds(wbuf, wo[i], at * kBytes, wl + i * kThreads + wave * kWave);
+                else if (i - kLoadsW < decltype(loads)::value)
+                    fetch_lds(xbuf, xo[i - kLoadsW], at * kBytes, xl + (i - kLoadsW) * kThreads + wave * kWave);
+            }
         };
         u32x4 wf[2][NF], xf[2][FR];
         // fragments of step i, counted over the ring
@@ -304,18 +313,22 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
 #pragma unroll
             for (int j = 0; j < NF; ++j) wf[i & 1][j] = l[j * 16 * kP];
         };
-        auto read_x = [&](int i, int f) { xf[i & 1][f] = (ring(i / SUB) + xfrag[i % SUB])[f * 16 * kP]; };
+        auto read_x = [&](int i, int f) { xf[i & 1][f] = (ring(i / SUB) + xfrag[i % SUB])[f * WM * 16 * kP]; };
         auto multiply = [&](int i, int f) {
 #pragma unroll
             for (int j = 0; j < NF; ++j)
                 acc[f][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, wf[i & 1][j]),
                                                                   __builtin_bit_cast(i32x4, xf[i & 1][f]), acc[f][j], 0, 0, 0);
         };
-        if (stages > 0) {
+        // Whole stages, for the first LIVE fragments of every wavefront: the others have no rows.
+        auto whole = [&](auto count) {
+            constexpr int LIVE = decltype(count)::value, LAST = 2;
+            using Loads = std::integral_constant<int, (kLoadsX * LIVE + FR - 1) / FR>;
+            constexpr int kAll = kLoadsW + Loads::value, kLeft = (RING - 2) * kAll;
+            static_assert(Loads::value * kThreads >= LIVE * WM * 16 * kP, "the rows of LIVE fragments are fetched");
 #pragma unroll
-            for (int i = 0; i < RING - 1; ++i) fetch(i, i);
-            barrier_fetched<(RING - 2) * kLoads>();
-            fetch(RING - 1, RING - 1);
+            for (int i = 0; i < RING - 1; ++i) fetch(Loads(), i, i, 0, kAll);
+            barrier_fetched<kLeft>();
             read_w(0);
 #pragma unroll
             for (int f = 0; f < LAST; ++f) read_x(0, f);
@@ -327,25 +340,36 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
                     for (int u = 0; u < SUB; ++u) {
                         const int i = s * SUB + u, next = (i + 1) % (RING * SUB);
 #pragma unroll
-                        for (int f = 0; f < FR - LAST; ++f) {
+                        for (int f = 0; f < LIVE - LAST; ++f) {
                             read_x(i, f + LAST);
                             multiply(i, f);
+                            if (u == 0) fetch(Loads(), s0 + s + RING - 1, (s + RING - 1) % RING, 2 * f, f == LIVE - LAST - 1 ? kAll : 2 * f + 2);
                             __builtin_amdgcn_sched_barrier(0);
                         }
-                        if (u == SUB - 1) {
-                            barrier_fetched<(RING - 2) * kLoads>();
-                            fetch(s0 + s + RING, s);
-                            __builtin_amdgcn_sched_barrier(0);
-                        }
+                        if (LIVE == LAST && u == 0) fetch(Loads(), s0 + s + RING - 1, (s + RING - 1) % RING, 0, kAll);
+                        if (u == SUB - 1) barrier_fetched<kLeft>();
                         read_w(next);
 #pragma unroll
                         for (int f = 0; f < LAST; ++f) read_x(next, f);
                         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                        for (int f = FR - LAST; f < FR; ++f) multiply(i, f);
+                        for (int f = LIVE - LAST; f < LIVE; ++f) multiply(i, f);
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 }
+            }
+        };
+        if (stages > 0) {
+            const int live = last / (WM * 16) + 1;            // fragments that hold rows of the expert
+            if constexpr (FR == 8) {
+                if (live > 6) whole(std::integral_constant<int, 8>());
+                else if (live > 4) whole(std::integral_constant<int, 6>());
+                else if (live > 2) whole(std::integral_constant<int, 4>());
+                else whole(std::integral_constant<int, 2>());
+            } else {
+                static_assert(FR == 2 || FR == 4, "the counts of fragments that the main loop is made for");
+                if (FR > 2 && live > 2) whole(std::integral_constant<int, FR>());
+                else whole(std::integral_constant<int, 2>());
             }
         }
         barrier_fetched<0>();
@@ -382,7 +406,7 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
 #pragma unroll
         for (int f = 0; f < FR; ++f) {
             wave_fence();
-            const float xs = sx[(wm * FR + f) * 16 + r];
+            const float xs = sx[(f * WM + wm) * 16 + r];
 #pragma unroll
             for (int j = 0; j < kOut; ++j) {
                 float v[4];
@@ -400,7 +424,7 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
             wave_fence();
 #pragma unroll
             for (int i = 0; i < kOut * 32; i += kWave) {      // pieces of 16 bytes
-                const int q = i + lane, row = tile.row + (wm * FR + f) * 16 + q / kLanes;
+                const int q = i + lane, row = tile.row + (f * WM + wm) * 16 + q / kLanes;
                 const int col = tile0 + wn * kOut * 16 + q % kLanes * 8;
                 if (q / kLanes >= 16 || row >= tile.end || col >= a.fo) continue;
                 const u32x4 v = *reinterpret_cast<const u32x4 *>(own + q / kLanes * kPitch + q % kLanes * 16);
@@ -416,6 +440,14 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
         }
     }
 }
+
+// Rows of a tile, for `each` rows an expert (masked pairs' among them: no more is known here): 32 (two workgroups on a CU,
+// the most weights on their way and the most tiles), 128 (three stages) or 256 (two; the fewest bytes for a product).
+// Measured with 64 experts, 7168 -> 4096 with SwiGLU, 1 / 16 / 32 / 64 / 128 / 160 / 256 rows each: 238, 347, 372, 517, 794, 949
+// and 1407 us with 32 rows; 236, 348, 344, 356, 458, 514 and 701 with 128; 286, 408, 428, 437, 482, 505 and 699 with 256.
+// 8 experts of 1 row: 28, 33 and 53. 256 experts, 2048 -> 7168, 96 / 128 / 192 / 256 rows: 841, 1049, 1408 and 1635 with 128, 992,
+// 1050, 1180 and 1483 with 256.
+int tile_rows(int each) { return each <= 20 ? 32 : each <= 144 ? 128 : 256; }
 
 int check_rows(long long rows, int cols, int dtype)
 {
@@ -527,8 +559,8 @@ int moe_expert_product_int8(const int8_t *x, const float *x_scales, const int8_t
     a.fo = glu ? n / 2 : n;
     const int each = rows / a.E;                // rows of an expert, were they even
     // rows and columns of a tile, and workgroups at a time
-    const int tall = each <= 48 ? 64 : each <= 144 ? 128 : 256;
-    const int cols = (tall == 64 ? 128 : 256) / (glu ? 2 : 1), groups = tall == 64 ? 512 : 256;
+    const int tall = tile_rows(each);
+    const int cols = (tall == 32 ? 128 : 256) / (glu ? 2 : 1), groups = tall == 32 ? 512 : 256;
     a.ntiles = (a.fo + cols - 1) / cols;
     // a tile starts at every expert's first row, so at most this many
     const long long mtiles = rows / tall + std::min(a.E, rows);
@@ -545,14 +577,14 @@ int moe_expert_product_int8(const int8_t *x, const float *x_scales, const int8_t
     a.ws = weight_scales;
     a.erc = ep_recv_count;
     a.out = out;
-    const dim3 g((unsigned)std::min<long long>(mtiles * a.ntiles, groups)), b(tall == 64 ? 256 : 512);
+    const dim3 g((unsigned)std::min<long long>(mtiles * a.ntiles, groups)), b(tall == 32 ? 256 : 512);
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
     auto launch = [&](auto type, auto act) {
         using T = decltype(type);
         constexpr bool kGlu = decltype(act)::value;
-        if (tall == 64) hipLaunchKernelGGL((expert_product_kernel<T, 4, 2, 1, 4, 1, 4, kGlu>), g, b, 0, st, a);
-        else if (tall == 128) hipLaunchKernelGGL((expert_product_kernel<T, 4, 4, 2, 4, 2, 2, kGlu>), g, b, 0, st, a);
+        if (tall == 32) hipLaunchKernelGGL((expert_product_kernel<T, 2, 2, 1, 4, 2, 3, kGlu>), g, b, 0, st, a);
+        else if (tall == 128) hipLaunchKernelGGL((expert_product_kernel<T, 4, 4, 2, 4, 2, 3, kGlu>), g, b, 0, st, a);
         else hipLaunchKernelGGL((expert_product_kernel<T, 8, 4, 2, 4, 2, 2, kGlu>), g, b, 0, st, a);
     };
     if (dtype == MOE_FP16 && glu) launch(F16(), std::true_type());

@@ -515,7 +515,7 @@ int moe_int8_dequantize(const int8_t *codes, const float *scales, int64_t rows, 
  *                 ep_recv_count counts are left as they were
  * Ranges: ep_world and experts as in moe_dispatch, 0 <= rows < 2^31 - 256, k a multiple of 16 up to 131056 (the sums fit 31 bits
  * and a sign), n >= 1 (even with SwiGLU), n * k <= 2^31 (MOE_ERR_SHAPE otherwise). Tiles are counted in 31 bits: every call
- * with (rows / 64 + E) * ceil(n / 64) < 2^31 - 1024 is taken, larger ones as far as their tiles allow. Counts that
+ * with (rows / 32 + E) * ceil(n / 64) < 2^31 - 1024 is taken, larger ones as far as their tiles allow. Counts that
  * ep_recv_count should not hold leave the kernel in bounds and the outputs unspecified. A row's results do not depend on the
  * other rows. Needs no workspace.
  */
