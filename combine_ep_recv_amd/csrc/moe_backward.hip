@@ -15,6 +15,7 @@
 #include <limits.h>
 
 #include <algorithm>
+#include <type_traits>
 
 namespace {
 
@@ -24,6 +25,7 @@ constexpr long long kMaxTokens = (1ll << 24) - 1;
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kPiece = 8;                  // elements of 16 bytes
+constexpr long long kOnceBytes = 256ll << 20;      // the Infinity Cache
 constexpr int kNone = -1, kCopy = -2, kConst = -3;      // a pair without a row, of a copy expert, of const expert kConst - j
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -89,9 +91,12 @@ __device__ __forceinline__ void find_rows(const Routing &a, int t, Rows &rows)
     }
 }
 
+// 16 bytes of a row; ONCE: past the caches
+template <bool ONCE>
 __device__ __forceinline__ u32x4 load16(const void *p)
 {
-    return __builtin_nontemporal_load(static_cast<const u32x4_a2 *>(p));
+    const u32x4_a2 *q = static_cast<const u32x4_a2 *>(p);
+    return ONCE ? __builtin_nontemporal_load(q) : *q;
 }
 __device__ __forceinline__ void store16(void *p, u32x4 v)
 {
@@ -119,6 +124,113 @@ __device__ __forceinline__ u32x4 pack(const float (&x)[kPiece])
 // combine
 // --------------------------------------------------------------------------
 
+// The const experts' table: every pair adds to one row of it. A workgroup takes expert j, a slice of columns and a part of
+// the tokens: it lists the part's pairs of expert j in order, then adds their rows, and a second kernel joins the parts. These
+// workgroups come first in combine's launch (a launch of their own is 8 us more with 4 ranks of 515 tokens).
+constexpr int kScan = 4 * kThreads;        // pairs looked at between two lists
+constexpr int kSliceCols = kThreads * kPiece;
+constexpr long long kFewPairs = 4096;
+constexpr int kMostSplits = 64, kSplitTokens = 32, kAhead = 8;
+
+struct ConstArgs {
+    const uint16_t *grad;
+    const float *w;
+    const int32_t *ids;
+    const uint8_t *mask;
+    float *sums;                           // [const experts, splits, h], or NULL where one part is all
+    uint16_t *out;
+    int mask_kind, N, K, h, first_id, slices, splits, per, join_slices;
+};
+
+struct ConstList {
+    int pair[kScan];
+    int count[4][kWaves];
+};
+
+template <class T>
+__device__ __forceinline__ void const_backward(const ConstArgs &a, int block, ConstList &found)
+{
+    int(&list)[kScan] = found.pair;
+    int(&count)[4][kWaves] = found.count;
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    const int j = block / (a.slices * a.splits), q = block - j * (a.slices * a.splits);
+    const int split = q / a.slices;
+    const long long at = (long long)(q - split * a.slices) * kSliceCols + tid * kPiece;
+    const int id = a.first_id + j;
+    // columns of this lane, the last eight where it has fewer (those of its neighbour among them, which both store)
+    const int live = at >= a.h ? 0 : min(a.h, kPiece);
+    const long long col = max(min(at, (long long)a.h - kPiece), 0ll);
+    const long long from = (long long)split * a.per * a.K, to = min((long long)a.N, (long long)(split + 1) * a.per) * a.K;
+    float acc[kPiece];
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) acc[i] = 0.f;
+    for (long long base = from; base < to; base += kScan) {
+        uint64_t hit[4];
+        bool mine[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const long long p = base + u * kThreads + tid;
+            mine[u] = p < to && a.ids[p] == id;
+            if (mine[u] && a.mask_kind != MOE_MASK_NONE)
+                mine[u] = a.mask[a.mask_kind == MOE_MASK_TOKEN ? p / a.K : p] != 0;
+            hit[u] = __builtin_amdgcn_ballot_w64(mine[u]);
+            if (lane == 0) count[u][wave] = __popcll(hit[u]);
+        }
+        __syncthreads();
+        int total = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            int at = total;
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) {
+                if (i < wave) at += count[u][i];
+                total += count[u][i];
+            }
+            if (mine[u]) list[at + __popcll(hit[u] & ((1ull << lane) - 1))] = (int)(base + u * kThreads + tid);
+        }
+        __syncthreads();
+        // kAhead rows on their way at a time; the list's last pair stands in for those past its end
+        for (int i = 0; i < total; i += kAhead) {
+            const uint16_t *g[kAhead];
+            float w[kAhead];
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                const int p = __builtin_amdgcn_readfirstlane(list[min(i + q, total - 1)]);
+                g[q] = a.grad + (size_t)(p / a.K) * a.h + col;
+                w[q] = a.w[p];
+            }
+            if (live == kPiece) {
+                u32x4 v[kAhead];
+#pragma unroll
+                for (int q = 0; q < kAhead; ++q) v[q] = *reinterpret_cast<const u32x4_a2 *>(g[q]);
+#pragma unroll
+                for (int q = 0; q < kAhead; ++q) {
+                    if (i + q >= total) break;
+                    float x[kPiece];
+                    unpack<T>(v[q], x);
+#pragma unroll
+                    for (int c = 0; c < kPiece; ++c) acc[c] = __builtin_fmaf(w[q], x[c], acc[c]);
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < kAhead; ++q) {
+                    if (i + q >= total) break;
+#pragma unroll
+                    for (int c = 0; c < kPiece; ++c)
+                        if (c < live) acc[c] = __builtin_fmaf(w[q], T::load(g[q][c]), acc[c]);
+                }
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int c = 0; c < kPiece; ++c) {
+        if (c >= live) continue;
+        if (a.sums) a.sums[((size_t)j * a.splits + split) * a.h + col + c] = acc[c];
+        else a.out[(size_t)j * a.h + col + c] = T::store(acc[c]);
+    }
+}
+
 struct CombineBackwardArgs {
     Routing r;
     const uint16_t *grad, *y, *ori_x, *const_x;
@@ -126,16 +238,24 @@ struct CombineBackwardArgs {
     uint16_t *grad_y, *grad_ori;
     float *grad_w;
     int h, parts;
+    ConstArgs table;
+    int table_blocks;                      // workgroups of the const experts' gradient, before the tokens'
 };
 
 // A workgroup takes token t and every `parts`th block of KB of its pairs. Rows in pieces of 16 bytes a lane, the h % 8 last
 // elements one a lane.
-template <class T, int KB>
+template <class T, int KB, bool ONCE, bool TABLE>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineBackwardArgs a)
 {
     __shared__ Rows rows;
     __shared__ float part[kWaves][KB];
-    const int t = blockIdx.x / a.parts, first = blockIdx.x - t * a.parts;
+    int block = blockIdx.x;
+    if constexpr (TABLE) {
+        __shared__ ConstList found;
+        if (block < a.table_blocks) return const_backward<T>(a.table, block, found);
+        block -= a.table_blocks;
+    }
+    const int t = block / a.parts, first = block - t * a.parts;
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const int K = a.r.K, pieces = a.h / kPiece, tail = a.h - pieces * kPiece, rest = pieces * kPiece + min(tid, tail);
     if (wave == 0) find_rows(a.r, t, rows);
@@ -162,7 +282,7 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineBackw
             const u32x4 gv = *reinterpret_cast<const u32x4_a2 *>(g + c * kPiece);
 #pragma unroll
             for (int i = 0; i < KB; ++i)
-                v[i] = load16(src[i] + c * kPiece);
+                v[i] = load16<ONCE>(src[i] + c * kPiece);
             float gx[kPiece];
             unpack<T>(gv, gx);
 #pragma unroll
@@ -216,87 +336,6 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineBackw
     }
 }
 
-// The const experts' table: every pair adds to one row of it. A workgroup takes expert j, a slice of columns and a part of
-// the tokens: it lists the part's pairs of expert j in order, then adds their rows, and a second kernel joins the parts.
-constexpr int kScan = 4 * kThreads;        // pairs looked at between two lists
-constexpr int kSliceCols = kThreads * kPiece;
-constexpr int kMostSplits = 64, kSplitTokens = 256;
-
-struct ConstArgs {
-    const uint16_t *grad;
-    const float *w;
-    const int32_t *ids;
-    const uint8_t *mask;
-    float *sums;                           // [const experts, splits, h], or NULL where one part is all
-    uint16_t *out;
-    int mask_kind, N, K, h, first_id, slices, splits, per, join_slices;
-};
-
-template <class T>
-__global__ __launch_bounds__(kThreads) void const_backward_kernel(ConstArgs a)
-{
-    __shared__ int list[kScan];
-    __shared__ int count[4][kWaves];
-    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-    const int j = blockIdx.x / (a.slices * a.splits), q = blockIdx.x - j * (a.slices * a.splits);
-    const int split = q / a.slices;
-    const long long col = (long long)(q - split * a.slices) * kSliceCols + tid * kPiece;
-    const int id = a.first_id + j;
-    const int live = (int)min(max(a.h - col, 0ll), (long long)kPiece);              // columns of this lane
-    const long long from = (long long)split * a.per * a.K, to = min((long long)a.N, (long long)(split + 1) * a.per) * a.K;
-    float acc[kPiece];
-#pragma unroll
-    for (int i = 0; i < kPiece; ++i) acc[i] = 0.f;
-    for (long long base = from; base < to; base += kScan) {
-        uint64_t hit[4];
-        bool mine[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const long long p = base + u * kThreads + tid;
-            mine[u] = p < to && a.ids[p] == id;
-            if (mine[u] && a.mask_kind != MOE_MASK_NONE)
-                mine[u] = a.mask[a.mask_kind == MOE_MASK_TOKEN ? p / a.K : p] != 0;
-            hit[u] = __builtin_amdgcn_ballot_w64(mine[u]);
-            if (lane == 0) count[u][wave] = __popcll(hit[u]);
-        }
-        __syncthreads();
-        int total = 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            int at = total;
-#pragma unroll
-            for (int i = 0; i < kWaves; ++i) {
-                if (i < wave) at += count[u][i];
-                total += count[u][i];
-            }
-            if (mine[u]) list[at + __popcll(hit[u] & ((1ull << lane) - 1))] = (int)(base + u * kThreads + tid);
-        }
-        __syncthreads();
-        for (int i = 0; i < total; ++i) {
-            const int p = list[i];
-            const float w = a.w[p];
-            const uint16_t *g = a.grad + (size_t)(p / a.K) * a.h + col;
-            if (live == kPiece) {
-                float x[kPiece];
-                unpack<T>(*reinterpret_cast<const u32x4_a2 *>(g), x);
-#pragma unroll
-                for (int c = 0; c < kPiece; ++c) acc[c] = __builtin_fmaf(w, x[c], acc[c]);
-            } else {
-#pragma unroll
-                for (int c = 0; c < kPiece; ++c)
-                    if (c < live) acc[c] = __builtin_fmaf(w, T::load(g[c]), acc[c]);
-            }
-        }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int c = 0; c < kPiece; ++c) {
-        if (c >= live) continue;
-        if (a.sums) a.sums[((size_t)j * a.splits + split) * a.h + col + c] = acc[c];
-        else a.out[(size_t)j * a.h + col + c] = T::store(acc[c]);
-    }
-}
-
 template <class T>
 __global__ __launch_bounds__(kThreads) void const_join_kernel(ConstArgs a)
 {
@@ -304,6 +343,7 @@ __global__ __launch_bounds__(kThreads) void const_join_kernel(ConstArgs a)
     const long long col = (long long)(blockIdx.x - j * a.join_slices) * kThreads + threadIdx.x;
     if (col >= a.h) return;
     float v = 0.f;
+#pragma unroll 8
     for (int i = 0; i < a.splits; ++i) v += a.sums[((size_t)j * a.splits + i) * a.h + col];
     a.out[(size_t)j * a.h + col] = T::store(v);
 }
@@ -322,7 +362,7 @@ struct DispatchBackwardArgs {
 };
 
 // A workgroup takes token t and every `slices`th 256 pieces of its row.
-template <class T>
+template <class T, bool ONCE>
 __global__ __launch_bounds__(kThreads) void dispatch_backward_kernel(DispatchBackwardArgs a)
 {
     __shared__ Rows rows;
@@ -335,7 +375,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_backward_kernel(DispatchBac
         float acc[kPiece];
         u32x4 v[KB];
         if (a.add) {
-            unpack<T>(load16(a.add + (size_t)t * a.h + c * kPiece), acc);
+            unpack<T>(load16<ONCE>(a.add + (size_t)t * a.h + c * kPiece), acc);
         } else {
 #pragma unroll
             for (int i = 0; i < kPiece; ++i) acc[i] = 0.f;
@@ -345,7 +385,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_backward_kernel(DispatchBac
 #pragma unroll
             for (int i = 0; i < KB; ++i) {
                 row[i] = __builtin_amdgcn_readfirstlane(kb + i < K ? rows.row[kb + i] : kNone);
-                v[i] = load16(a.grad + (size_t)max(row[i], 0) * a.h + c * kPiece);        // without a row: see above
+                v[i] = load16<ONCE>(a.grad + (size_t)max(row[i], 0) * a.h + c * kPiece);        // without a row: see above
             }
 #pragma unroll
             for (int i = 0; i < KB; ++i) {
@@ -411,6 +451,18 @@ Routing routing_of(const int32_t *assist, const int32_t *erc, const int32_t *ids
     return r;
 }
 
+// f(element type, whether rows of this many bytes pass the caches by)
+template <class F>
+void by_type(int dtype, long long bytes, F f)
+{
+    auto sized = [&](auto type) {
+        if (bytes >= kOnceBytes) f(type, std::true_type());
+        else f(type, std::false_type());
+    };
+    if (dtype == MOE_FP16) sized(F16());
+    else sized(BF16());
+}
+
 // Parts of the tokens for the const experts' sums: by the tokens alone, so that a sum's order does not change with h.
 int splits_of(long long N) { return (int)std::min<long long>(kMostSplits, (N + kSplitTokens - 1) / kSplitTokens); }
 
@@ -425,9 +477,10 @@ int moe_combine_backward_workspace_size(int ep_world, int bs, int experts_per_ra
     const int rc = check_call(ep_world, bs, experts_per_rank, h, topk, dtype);
     if (rc) return rc;
     const int splits = splits_of((long long)ep_world * bs);
-    // workgroups of both kernels of the const experts' gradient are counted in 24 bits, their threads in 32
-    const long long most = std::max((h + kSliceCols - 1ll) / kSliceCols * std::max(splits, 1), (h + kThreads - 1ll) / kThreads);
-    if (const_expert_num < 0 || const_expert_num * most >= 1ll << 24) return MOE_ERR_SHAPE;
+    // a launch has fewer than 2^24 workgroups, the tokens' among them
+    const long long slices = std::max((h + kSliceCols - 1ll) / kSliceCols * std::max(splits, 1), (h + kThreads - 1ll) / kThreads);
+    const long long tokens = std::max((long long)ep_world * bs, kFewPairs);
+    if (const_expert_num < 0 || (const_expert_num > 0 && const_expert_num * slices + tokens >= 1ll << 24)) return MOE_ERR_SHAPE;
     *bytes = splits > 1 ? (size_t)const_expert_num * splits * h * sizeof(float) : 0;
     return MOE_OK;
 }
@@ -463,63 +516,53 @@ int moe_combine_backward(const void *grad_out, const void *expand_x, const int32
         (need > 0 && !aligned(workspace, 16)))
         return MOE_ERR_ALIGN;
     if (N == 0 && table == 0) return MOE_OK;
+    CombineBackwardArgs a;
+    a.r = routing_of(assist_info, ep_recv_count, expert_ids, x_active_mask, mask_kind, ep_world, bs, experts_per_rank, topk);
+    a.r.zero_end = a.r.E + zero_n;
+    a.r.copy_end = a.r.zero_end + copy_n;
+    a.r.const_end = a.r.copy_end + const_n;
+    a.grad = static_cast<const uint16_t *>(grad_out);
+    a.y = static_cast<const uint16_t *>(expand_x);
+    a.ori_x = static_cast<const uint16_t *>(ori_x);
+    a.const_x = static_cast<const uint16_t *>(const_x);
+    a.w = expert_scales;
+    a.grad_y = static_cast<uint16_t *>(grad_expand_x);
+    a.grad_ori = static_cast<uint16_t *>(grad_ori_x);
+    a.grad_w = grad_scales;
+    a.h = h;
+    // few pairs: a workgroup each, one token's eight at a time otherwise
+    const bool few = N * topk <= kFewPairs;
+    a.parts = few ? topk : 1;
+    ConstArgs &c = a.table;
+    c.grad = a.grad;
+    c.w = expert_scales;
+    c.ids = expert_ids;
+    c.mask = x_active_mask;
+    c.mask_kind = mask_kind;
+    c.N = (int)N;
+    c.K = topk;
+    c.h = h;
+    c.first_id = a.r.copy_end;
+    c.splits = std::max(1, splits_of(N));
+    c.per = (int)((N + c.splits - 1) / c.splits);
+    c.slices = (int)((h + kSliceCols - 1ll) / kSliceCols);
+    c.join_slices = (int)((h + kThreads - 1ll) / kThreads);
+    c.sums = c.splits > 1 ? static_cast<float *>(workspace) : nullptr;
+    c.out = static_cast<uint16_t *>(grad_const_x);
+    a.table_blocks = table * c.slices * c.splits;
+    const dim3 g((unsigned)(a.table_blocks + N * a.parts)), b(kThreads);
+    const dim3 join((unsigned)(table * c.join_slices));
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
-    if (N > 0) {
-        CombineBackwardArgs a;
-        a.r = routing_of(assist_info, ep_recv_count, expert_ids, x_active_mask, mask_kind, ep_world, bs, experts_per_rank, topk);
-        a.r.zero_end = a.r.E + zero_n;
-        a.r.copy_end = a.r.zero_end + copy_n;
-        a.r.const_end = a.r.copy_end + const_n;
-        a.grad = static_cast<const uint16_t *>(grad_out);
-        a.y = static_cast<const uint16_t *>(expand_x);
-        a.ori_x = static_cast<const uint16_t *>(ori_x);
-        a.const_x = static_cast<const uint16_t *>(const_x);
-        a.w = expert_scales;
-        a.grad_y = static_cast<uint16_t *>(grad_expand_x);
-        a.grad_ori = static_cast<uint16_t *>(grad_ori_x);
-        a.grad_w = grad_scales;
-        a.h = h;
-        a.parts = 1;
-        const dim3 b(kThreads);
-        if (N * topk <= 4096) {
-            a.parts = topk;
-            const dim3 g((unsigned)(N * a.parts));
-            if (dtype == MOE_FP16) hipLaunchKernelGGL((combine_backward_kernel<F16, 1>), g, b, 0, st, a);
-            else hipLaunchKernelGGL((combine_backward_kernel<BF16, 1>), g, b, 0, st, a);
-        } else {
-            const dim3 g((unsigned)N);
-            if (dtype == MOE_FP16) hipLaunchKernelGGL((combine_backward_kernel<F16, 8>), g, b, 0, st, a);
-            else hipLaunchKernelGGL((combine_backward_kernel<BF16, 8>), g, b, 0, st, a);
-        }
-    }
-    if (table) {
-        ConstArgs c;
-        c.grad = static_cast<const uint16_t *>(grad_out);
-        c.w = expert_scales;
-        c.ids = expert_ids;
-        c.mask = x_active_mask;
-        c.mask_kind = mask_kind;
-        c.N = (int)N;
-        c.K = topk;
-        c.h = h;
-        c.first_id = (int)(E + zero_n + copy_n);
-        c.splits = std::max(1, splits_of(N));
-        c.per = (int)((N + c.splits - 1) / c.splits);
-        c.slices = (int)((h + kSliceCols - 1ll) / kSliceCols);
-        c.join_slices = (int)((h + kThreads - 1ll) / kThreads);
-        c.sums = c.splits > 1 ? static_cast<float *>(workspace) : nullptr;
-        c.out = static_cast<uint16_t *>(grad_const_x);
-        const dim3 g((unsigned)((long long)table * c.slices * c.splits)), b(kThreads);
-        const dim3 join((unsigned)((long long)table * c.join_slices));
-        if (dtype == MOE_FP16) {
-            hipLaunchKernelGGL(const_backward_kernel<F16>, g, b, 0, st, c);
-            if (c.sums) hipLaunchKernelGGL(const_join_kernel<F16>, join, b, 0, st, c);
-        } else {
-            hipLaunchKernelGGL(const_backward_kernel<BF16>, g, b, 0, st, c);
-            if (c.sums) hipLaunchKernelGGL(const_join_kernel<BF16>, join, b, 0, st, c);
-        }
-    }
+    by_type(dtype, N * topk * h * 2, [&](auto type, auto once) {
+        using T = decltype(type);
+        constexpr bool kOnce = decltype(once)::value;
+        if (few && table) hipLaunchKernelGGL((combine_backward_kernel<T, 1, kOnce, true>), g, b, 0, st, a);
+        else if (few) hipLaunchKernelGGL((combine_backward_kernel<T, 1, kOnce, false>), g, b, 0, st, a);
+        else if (table) hipLaunchKernelGGL((combine_backward_kernel<T, 8, kOnce, true>), g, b, 0, st, a);
+        else hipLaunchKernelGGL((combine_backward_kernel<T, 8, kOnce, false>), g, b, 0, st, a);
+        if (table && c.sums) hipLaunchKernelGGL(const_join_kernel<T>, join, b, 0, st, c);
+    });
     return launched();
 }
 
@@ -546,12 +589,13 @@ int moe_dispatch_backward(const void *grad_expand_x, const int32_t *assist_info,
     a.out = static_cast<uint16_t *>(grad_x);
     a.grad_scales = grad_scales;
     a.h = h;
-    a.slices = N < 4096 ? (int)std::min(16ll, (h + kSliceCols - 1ll) / kSliceCols) : 1;
-    const dim3 g((unsigned)(N * a.slices)), b(kThreads);
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
-    if (dtype == MOE_FP16) hipLaunchKernelGGL(dispatch_backward_kernel<F16>, g, b, 0, st, a);
-    else hipLaunchKernelGGL(dispatch_backward_kernel<BF16>, g, b, 0, st, a);
+    a.slices = N < 4096 ? (int)std::min(16ll, (h + kSliceCols - 1ll) / kSliceCols) : 1;
+    by_type(dtype, N * topk * h * 2, [&](auto type, auto once) {
+        hipLaunchKernelGGL((dispatch_backward_kernel<decltype(type), decltype(once)::value>), dim3((unsigned)(N * a.slices)),
+                           dim3(kThreads), 0, st, a);
+    });
     return launched();
 }
 

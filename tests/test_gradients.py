@@ -45,13 +45,15 @@ COMBINE = dict(grad=A, y=2 * A, assist=3 * A, erc=4 * A, ids=5 * A, w=6 * A, mas
     (dict(special=(1 << 30, 1 << 30, 0, A, A)), moe.MOE_ERR_SHAPE),
     (dict(special=(0, 0, 1 << 24, None, A), gconst=A), moe.MOE_ERR_SHAPE),
     (dict(special=(0, 0, 3, None, A), gconst=A, bs=200), moe.MOE_ERR_NULLPTR),
-    (dict(special=(0, 0, 3, None, A), gconst=A, bs=200, ws=A, wsn=3 * 2 * 8 * 4 - 1), moe.MOE_ERR_WORKSPACE),
-    (dict(special=(0, 0, 3, None, A), gconst=A, bs=200, ws=A + 8, wsn=3 * 2 * 8 * 4), moe.MOE_ERR_ALIGN),
+    (dict(special=(0, 0, 3, None, A), gconst=A, bs=200, ws=A, wsn=-1), moe.MOE_ERR_WORKSPACE),
+    (dict(special=(0, 0, 3, None, A), gconst=A, bs=200, ws=A + 8), moe.MOE_ERR_ALIGN),
     (dict(bs=0, grad=None, y=None, assist=None, ids=None, w=None, gy=None, gw=None), moe.MOE_OK),
 ])
 def test_combine_backward_refuses_before_a_launch(kw, want):
     p = dict(COMBINE, **kw)
     sp = None if p["special"] is None else _special(*p["special"])
+    if p["gconst"] and p["special"] and want in (moe.MOE_ERR_WORKSPACE, moe.MOE_ERR_ALIGN):      # wsn: beside what it needs
+        p["wsn"] += moe.combine_backward_workspace_size(p["W"], p["bs"], p["epr"], p["h"], p["K"], p["dtype"], p["special"][2])
     assert moe.library().moe_combine_backward(
         P(p["grad"]), P(p["y"]), P(p["assist"]), P(p["erc"]), P(p["ids"]), P(p["w"]), P(p["mask"]), p["kind"], sp, p["W"],
         p["bs"], p["epr"], p["h"], p["K"], p["dtype"], P(p["gy"]), P(p["gw"]), P(p["gori"]), P(p["gconst"]), P(p["ws"]),
@@ -78,9 +80,9 @@ def test_dispatch_backward_refuses_before_a_launch(kw, want):
 
 def test_workspace_is_for_the_const_experts_parts():
     size = moe.combine_backward_workspace_size
-    assert size(4, 64, 2, 24, 2, moe.MOE_BF16, 5) == 0                    # one part: no sums to join
-    assert size(4, 65, 2, 24, 2, moe.MOE_BF16, 5) == 5 * 2 * 24 * 4
-    assert size(4, 1 << 20, 2, 24, 2, moe.MOE_BF16, 5) == 5 * 64 * 24 * 4
+    assert size(4, 1, 2, 24, 2, moe.MOE_BF16, 5) == 0                     # one part: no sums to join
+    few, many = (size(4, n, 2, 24, 2, moe.MOE_BF16, 5) for n in (100, 1 << 20))
+    assert 0 < few < many <= 64 * 5 * 24 * 4 and few % (5 * 24 * 4) == many % (5 * 24 * 4) == 0
     assert size(4, 1 << 20, 2, 24, 2, moe.MOE_BF16) == 0
     for args in ((4, 65, 2, 24, 2, moe.MOE_BF16, BIG), (4, 65, 2, 24, 2, moe.MOE_BF16, 1 << 24),
                  (2, 0, 1, 2 ** 31 - 1, 1, moe.MOE_BF16, 2)):
