@@ -884,61 +884,75 @@ def dequantize_mx(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype 
 
 # ---- rows of 8-bit integers ----
 
-def quantize_int8_into(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor):
-    """moe_int8_quantize of x [..., cols] into preallocated codes (int8 [..., cols]) and scales (fp32 [...]), on the
-    current stream."""
-    fn = "moe_int8_quantize"
+def _int8_rows(fn, x):
+    """(device, shape, dtype code) of rows to quantise, checked."""
     dev = _gpu_device("x", x)
     shape = tuple(x.shape)
     if not shape or shape[-1] < 1:
         raise MoeError(fn, MOE_ERR_SHAPE, "x must have columns")
-    dt = _float_code(fn, x.dtype)
     _check_int(fn, shape[-1])
+    dt = _float_code(fn, x.dtype)
     _check_tensor("x", x, x.dtype, shape, dev)
-    _check_tensor("codes", codes, torch.int8, shape, dev)
-    _check_tensor("scales", scales, torch.float32, shape[:-1], dev)
-    _launch(fn, dev, x.data_ptr(), x.numel() // shape[-1], shape[-1], dt, codes.data_ptr(), scales.data_ptr(),
-            _stream_ptr(dev))
+    return dev, shape, dt
+
+
+def _quantize_int8(codes, scales, x, head):
+    """moe_int8_quantize into checked (or new) outputs; head: _int8_rows' result."""
+    dev, shape, dt = head
+    _launch("moe_int8_quantize", dev, x.data_ptr(), x.numel() // shape[-1], shape[-1], dt, codes.data_ptr(),
+            scales.data_ptr(), _stream_ptr(dev))
     return codes, scales
+
+
+def quantize_int8_into(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor):
+    """moe_int8_quantize of x [..., cols] into preallocated codes (int8 [..., cols]) and scales (fp32 [...]), on the
+    current stream."""
+    head = _int8_rows("moe_int8_quantize", x)
+    _check_tensor("codes", codes, torch.int8, head[1], head[0])
+    _check_tensor("scales", scales, torch.float32, head[1][:-1], head[0])
+    return _quantize_int8(codes, scales, x, head)
 
 
 def quantize_int8(x: torch.Tensor):
     """Rows of x [..., cols] (fp16, bf16 or fp32) as int8 codes with one scale each: (codes int8 [..., cols], scales
     fp32 [...]), scale = max|x| / 127 and code = x / scale rounded to the nearest, ties to even: what dispatch writes
     under MOE_QUANT_DYN_TOKEN. A row of zeros has scale 0; one with an infinity or NaN has scale NaN and codes 0."""
-    dev = _gpu_device("x", x)
-    shape = tuple(x.shape)
+    head = _int8_rows("moe_int8_quantize", x)
+    dev, shape, _ = head
+    scales = _new(shape[:-1], torch.float32, dev) if len(shape) > 1 else torch.empty((), dtype=torch.float32, device=dev)
+    return _quantize_int8(_new(shape, torch.int8, dev), scales, x, head)
+
+
+def _dequantize_int8(out, codes, scales, dt):
+    """moe_int8_dequantize into a checked (or new) out."""
+    fn, dev, shape = "moe_int8_dequantize", out.device, tuple(codes.shape)
     if not shape or shape[-1] < 1:
-        raise MoeError("moe_int8_quantize", MOE_ERR_SHAPE, "x must have columns")
-    return quantize_int8_into(_new(shape, torch.int8, dev), torch.empty(shape[:-1], dtype=torch.float32, device=dev), x)
+        raise MoeError(fn, MOE_ERR_SHAPE, "codes must have columns")
+    _check_int(fn, shape[-1])
+    _check_tensor("codes", codes, torch.int8, shape, dev)
+    _check_tensor("scales", scales, torch.float32, shape[:-1], dev)
+    _launch(fn, dev, codes.data_ptr(), scales.data_ptr(), codes.numel() // shape[-1], shape[-1], dt, out.data_ptr(),
+            _stream_ptr(dev))
+    return out
 
 
 def dequantize_int8_into(out: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
     """moe_int8_dequantize into a preallocated out [..., cols] (fp16, bf16 or fp32) on the current stream."""
-    fn = "moe_int8_dequantize"
     dev = _gpu_device("codes", codes)
     _gpu_device("out", out)
-    shape = tuple(codes.shape)
-    if not shape or shape[-1] < 1:
-        raise MoeError(fn, MOE_ERR_SHAPE, "codes must have columns")
-    dt = _float_code(fn, out.dtype)
-    _check_int(fn, shape[-1])
-    _check_tensor("codes", codes, torch.int8, shape, dev)
-    _check_tensor("scales", scales, torch.float32, shape[:-1], dev)
-    _check_tensor("out", out, out.dtype, shape, dev)
-    _launch(fn, dev, codes.data_ptr(), scales.data_ptr(), codes.numel() // shape[-1], shape[-1], dt, out.data_ptr(),
-            _stream_ptr(dev))
-    return out
+    dt = _float_code("moe_int8_dequantize", out.dtype)
+    _check_tensor("out", out, out.dtype, codes.shape, dev)
+    return _dequantize_int8(out, codes, scales, dt)
 
 
 def dequantize_int8(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """What int8 codes [..., cols] and scales fp32 [...] stand for, code * scale, in dtype: quantize_int8's rows, or
     dispatch's under MOE_QUANT_DYN_TOKEN."""
     dev = _gpu_device("codes", codes)
-    _float_code("moe_int8_dequantize", dtype)
+    dt = _float_code("moe_int8_dequantize", dtype)
     if codes.dim() < 1:
         raise MoeError("moe_int8_dequantize", MOE_ERR_SHAPE, "codes must have columns")
-    return dequantize_int8_into(_new(tuple(codes.shape), dtype, dev), codes, scales)
+    return _dequantize_int8(_new(tuple(codes.shape), dtype, dev), codes, scales, dt)
 
 
 # ---- the experts' product ----

@@ -25,7 +25,16 @@ constexpr long long kMaxTokens = (1ll << 24) - 1;
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kPiece = 8;                  // elements of 16 bytes
-constexpr long long kOnceBytes = 256ll << 20;      // the Infinity Cache
+// Rows that fill the Infinity Cache pass the caches by: 16 ranks x 256 tokens, top-8, bf16 rows of 7168, combine's
+// gradient 203 us and dispatch's 100, 217 and 106 through them; smaller ones may lie in them, fresh from the experts: 8
+// ranks x 32 tokens 15.4 and 7.9 us through them, 16.9 and 8.8 past them.
+constexpr long long kOnceBytes = 256ll << 20;
+// Up to so many pairs combine's gradient gives each pair a workgroup of its own: 1024 pairs (8 ranks x 16 tokens, 7168)
+// 9.4 us, 9.8 with a workgroup a token; 2048 14.9 and 12.9, 8192 51 and 38.5.
+constexpr long long kFewPairs = 1024;
+// Up to so many tokens dispatch's gradient parts their rows: 128 tokens of 7168 4.4 us, 6.9 in one piece; 256 7.8 and
+// 8.6, 512 13.4 and 12.8.
+constexpr long long kFewTokens = 256;
 constexpr int kNone = -1, kCopy = -2, kConst = -3;      // a pair without a row, of a copy expert, of const expert kConst - j
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -39,16 +48,19 @@ struct Routing {
     int zero_end, copy_end, const_end;     // special ids: [zero_end, copy_end) copy, [copy_end, const_end) const
 };
 
-// Tokens' rows in LDS: where each rank's rows begin, and the row (or kNone, kCopy, kConst - j) of each of a token's pairs.
+// Tokens' rows in LDS: where each rank's rows begin, and the row (or kNone, kCopy, kConst - j) of each of a token's
+// pairs.
 struct Rows {
     uint32_t before[kMaxWorld];
     int row[kMaxExperts];
 };
 
-// Finds the rows of token t's pairs: pair (t, k) lies in segment (local expert, source rank) of its expert's rank, whose
-// rows are in order of their tokens, so that assist_info's token column is searched by halves. (No pass over all
-// rows first, as combine's slots: a segment has few rows, and the search's loads hit the L2.) The first wavefront calls it;
-// the caller puts a barrier behind it. Whatever the arrays hold, rows stay in [0, R).
+// Finds the rows of token t's pairs: pair (t, k) lies in segment (local expert, source rank) of its expert's rank,
+// whose rows are in order of their tokens, so that assist_info's token column is searched by halves. (No pass over all
+// rows first, as combine's slots, which would be a launch more: a segment has few rows, and the loads hit the L2. All
+// 64 lanes looking at a segment at once were no faster: 14.7 us for 15.3 at 8 ranks x 32 tokens, 12.7 for 11.4 at 4 x
+// 515.) The first wavefront calls it; the caller puts a barrier behind it. Whatever the arrays hold, rows stay in [0,
+// R).
 __device__ __forceinline__ void find_rows(const Routing &a, int t, Rows &rows)
 {
     const int lane = threadIdx.x;
@@ -124,12 +136,12 @@ __device__ __forceinline__ u32x4 pack(const float (&x)[kPiece])
 // combine
 // --------------------------------------------------------------------------
 
-// The const experts' table: every pair adds to one row of it. A workgroup takes expert j, a slice of columns and a part of
-// the tokens: it lists the part's pairs of expert j in order, then adds their rows, and a second kernel joins the parts. These
-// workgroups come first in combine's launch (a launch of their own is 8 us more with 4 ranks of 515 tokens).
+// The const experts' table: every pair adds to one row of it. A workgroup takes expert j, a slice of columns and a part
+// of the tokens: it lists the part's pairs of expert j in order, then adds their rows, and a second kernel joins the
+// parts. These workgroups come first in combine's launch (a launch of their own is 8 us more with 4 ranks of 515
+// tokens).
 constexpr int kScan = 4 * kThreads;        // pairs looked at between two lists
 constexpr int kSliceCols = kThreads * kPiece;
-constexpr long long kFewPairs = 4096;
 constexpr int kMostSplits = 64, kSplitTokens = 32, kAhead = 8;
 
 struct ConstArgs {
@@ -242,8 +254,14 @@ struct CombineBackwardArgs {
     int table_blocks;                      // workgroups of the const experts' gradient, before the tokens'
 };
 
-// A workgroup takes token t and every `parts`th block of KB of its pairs. Rows in pieces of 16 bytes a lane, the h % 8 last
-// elements one a lane.
+// A workgroup takes token t and every `parts`th block of KB of its pairs: g[t] is read once for KB rows, which are read
+// and written once. Rows in pieces of 16 bytes a lane (at any alignment), the h % 8 last elements one a lane. Each lane
+// adds the products of its own columns, eight neighbours in order and then those 2048 on; a wavefront's lanes and then
+// the four wavefronts are joined in a fixed order, the same for every KB.
+//
+// Memory bounds it: 3 operations an element of 4 bytes. 16 ranks x 256 tokens, top-8, bf16 rows of 7168: 1.0 GB in 197
+// to 203 us, 4.9 to 5.1 TB/s, where a large copy reaches 5.2. A wavefront for a token and all of its rows takes 193 us
+// there, but 24.7 for 16.9 with 8 ranks x 32 tokens.
 template <class T, int KB, bool ONCE, bool TABLE>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineBackwardArgs a)
 {
@@ -269,8 +287,8 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineBackw
         for (int i = 0; i < KB; ++i) {
             row[i] = __builtin_amdgcn_readfirstlane(kb + i < K ? rows.row[kb + i] : kNone);
             w[i] = kb + i < K ? a.w[(size_t)t * K + kb + i] : 0.f;
-            // a pair without a row reads the gradient's again, which is in the cache: a load that hangs on the pair would
-            // have the others waited for
+            // a pair without a row reads the gradient's again, which is in the cache: a load that hangs on the pair
+            // would have the others waited for
             src[i] = row[i] >= 0       ? a.y + (size_t)row[i] * a.h
                      : row[i] == kNone ? g
                      : row[i] == kCopy ? a.ori_x + (size_t)t * a.h
@@ -361,7 +379,8 @@ struct DispatchBackwardArgs {
     int h, slices;
 };
 
-// A workgroup takes token t and every `slices`th 256 pieces of its row.
+// A workgroup takes token t and every `slices`th 256 pieces of its row, eight rows' pieces on their way at a time.
+// Memory bounds it: 529 MB in 97 to 100 us (5.3 TB/s) at 16 ranks x 256 tokens, top-8, bf16 rows of 7168.
 template <class T, bool ONCE>
 __global__ __launch_bounds__(kThreads) void dispatch_backward_kernel(DispatchBackwardArgs a)
 {
@@ -591,7 +610,7 @@ int moe_dispatch_backward(const void *grad_expand_x, const int32_t *assist_info,
     a.h = h;
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
-    a.slices = N < 4096 ? (int)std::min(16ll, (h + kSliceCols - 1ll) / kSliceCols) : 1;
+    a.slices = N <= kFewTokens ? (int)std::min(16ll, (h + kSliceCols - 1ll) / kSliceCols) : 1;
     by_type(dtype, N * topk * h * 2, [&](auto type, auto once) {
         hipLaunchKernelGGL((dispatch_backward_kernel<decltype(type), decltype(once)::value>), dim3((unsigned)(N * a.slices)),
                            dim3(kThreads), 0, st, a);

@@ -18,6 +18,7 @@ using namespace moe_detail;
 
 constexpr int kPiece = 16;                 // codes of 16 bytes
 constexpr int kRowThreads = 256;
+constexpr long long kOnceBytes = 256ll << 20;      // the Infinity Cache
 
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -36,8 +37,8 @@ struct RowsArgs {
     int cols, per_row;         // elements and pieces (the last one may be shorter) of a row
 };
 
-// Elements of a piece, `live` of them (0 to 16), zeros behind. Rows start at any element.
-template <class T>
+// Elements of a piece, `live` of them (0 to 16), zeros behind. Rows start at any element. ONCE: past the caches.
+template <class T, bool ONCE>
 __device__ __forceinline__ void load_piece(const typename T::raw *p, int live, float (&x)[kPiece])
 {
 #pragma unroll
@@ -46,14 +47,16 @@ __device__ __forceinline__ void load_piece(const typename T::raw *p, int live, f
         if constexpr (sizeof(typename T::raw) == 4) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const u32x4 v = reinterpret_cast<const u32x4_a4 *>(p)[i];
+                const u32x4_a4 *q = reinterpret_cast<const u32x4_a4 *>(p) + i;
+                const u32x4 v = ONCE ? __builtin_nontemporal_load(q) : *q;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[4 * i + j] = T::load(v[j]);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const u32x4 v = reinterpret_cast<const u32x4_a2 *>(p)[i];
+                const u32x4_a2 *q = reinterpret_cast<const u32x4_a2 *>(p) + i;
+                const u32x4 v = ONCE ? __builtin_nontemporal_load(q) : *q;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     x[8 * i + 2 * j] = T::load((uint16_t)(v[j] & 0xffff));
@@ -96,10 +99,10 @@ __device__ __forceinline__ void store_piece(typename T::raw *p, int live, const 
     }
 }
 
-// The codes of a piece, four a word. FAST, for 16-bit types and scale >= 2^-100: one correction step gives the correctly
-// rounded quotient as far as its rounding to an integer goes, and adding 1.5 * 2^23 rounds it, ties to even, with the code
-// in the low byte; both hold for every pair of 16-bit x and max|x| (checked exhaustively by the test of dispatch's
-// quantiser, whose codes these are). Otherwise the division itself.
+// The codes of a piece, four a word. FAST, for 16-bit types and scale >= 2^-100: one correction step gives the
+// correctly rounded quotient as far as its rounding to an integer goes, and adding 1.5 * 2^23 rounds it, ties to even,
+// with the code in the low byte; both hold for every pair of 16-bit x and max|x| (checked exhaustively by the test of
+// dispatch's quantiser, whose codes these are). Otherwise the division itself.
 template <bool FAST>
 __device__ __forceinline__ u32x4 codes_of(const float (&x)[kPiece], float scale, float inv)
 {
@@ -133,8 +136,12 @@ __device__ __forceinline__ float row_max(float v, float (&part)[kRowThreads / kW
     return v;
 }
 
-// A row's LANES lanes hold it, J pieces each (J = 0: any number, read a second time for the codes).
-template <class T, int LANES, int J>
+// A row's LANES lanes hold it, J pieces each (J = 0: any number, read a second time for the codes, through the cache).
+//
+// Memory bounds it: 3 bytes an element of 16 bits, against some twelve instructions. bf16 [32768, 7168] 115 us, 6.1
+// TB/s of 0.7 GB; [256, 2048] 3 us. Lanes by the row's pieces: 16 (four rows a wavefront), 64, or the workgroup's 256
+// above 256 pieces: a wavefront that holds 448 pieces, 7 a lane, takes 173 us for 115.
+template <class T, int LANES, int J, bool ONCE>
 __global__ __launch_bounds__(kRowThreads) void quantize_kernel(RowsArgs a)
 {
     constexpr int kRows = kRowThreads / LANES, kHeld = J ? J : 1;
@@ -152,7 +159,8 @@ __global__ __launch_bounds__(kRowThreads) void quantize_kernel(RowsArgs a)
         for (int j = 0; j < pieces; ++j) {
             const int p = lane + j * LANES;
             float(&v)[kPiece] = x[J ? j : 0];
-            load_piece<T>(in + (size_t)min(p, a.per_row) * kPiece, live ? min(max(a.cols - p * kPiece, 0), kPiece) : 0, v);
+            load_piece<T, ONCE>(in + (size_t)min(p, a.per_row) * kPiece,
+                                live ? min(max(a.cols - p * kPiece, 0), kPiece) : 0, v);
 #pragma unroll
             for (int i = 0; i < kPiece; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
         }
@@ -167,7 +175,7 @@ __global__ __launch_bounds__(kRowThreads) void quantize_kernel(RowsArgs a)
         for (int j = 0; j < pieces; ++j) {
             const int p = lane + j * LANES, n = live ? min(max(a.cols - p * kPiece, 0), kPiece) : 0;
             float(&v)[kPiece] = x[J ? j : 0];
-            if (!J) load_piece<T>(in + (size_t)min(p, a.per_row) * kPiece, n, v);
+            if (!J) load_piece<T, ONCE>(in + (size_t)min(p, a.per_row) * kPiece, n, v);
             u32x4 c = {0, 0, 0, 0};
             if (some) c = fast ? codes_of<true>(v, scale, inv) : codes_of<false>(v, scale, inv);
             uint8_t *out = static_cast<uint8_t *>(a.out) + row * a.cols + (size_t)p * kPiece;
@@ -182,7 +190,7 @@ __global__ __launch_bounds__(kRowThreads) void quantize_kernel(RowsArgs a)
     }
 }
 
-// A lane takes a piece.
+// A lane takes a piece. bf16 [32768, 7168] 125 to 140 us, 5.1 to 5.6 TB/s; stores past the caches 171.
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void dequantize_kernel(RowsArgs a)
 {
@@ -219,29 +227,45 @@ struct ProductArgs {
 };
 
 // Rows of one expert, 16 * FR * WM at a time, against 16 * NF * WN weight rows (half of them the gate's, half the
-// matching ones of the up projection with GLU): WM x WN wavefronts, each with FR x NF fragments of its own and all of k.
+// matching ones of the up projection with GLU): WM x WN wavefronts, each with FR x NF fragments of its own and all of
+// k.
 //
-// One 16 x 16 x 64 step: lane (r, g), r = lane % 16, g = lane / 16, holds the codes 16g..16g+15 of row r of either side.
-// Result register i is weight row 4g + i, input row r.
+// One 16 x 16 x 64 step: lane (r, g), r = lane % 16, g = lane / 16, holds the codes 16g..16g+15 of row r of either
+// side. Result register i is weight row 4g + i, input row r.
 //
-// Both sides go through LDS in stages of SUB steps, RING of them; a row's 16-byte pieces are swapped by its number (each
-// lane fetches the piece that belongs where it writes) so that the lanes that LDS serves in a clock meet every bank once.
-// The barrier comes when the current stage has been read, two fragments before its end; behind it the stage RING ahead is
-// fetched in its place, and the next one's first fragments are read while those two multiply.
-template <class T, int FR, int NF, int WM, int WN, int SUB, int RING, bool GLU>
+// Both sides go through LDS in stages of 128 bytes of a row, RING of them; a row's 16-byte pieces are swapped by its
+// number (each lane fetches the piece that belongs where it writes) so that the lanes that LDS serves in a clock meet
+// every bank once. Whole lines: four stages of 64 bytes are slower (2188 us for 2080 with the case of many rows below,
+// 406 for 333 at 8 ranks x 32 tokens). The barrier comes when the current stage has been read, two fragments before its
+// end; the next one's first fragments are read while those two multiply. The stage RING - 1 ahead is fetched between
+// the next products (all at once behind the barrier the wavefronts stand still until the fetches are taken: 2021 us for
+// 1937).
+//
+// Fragment f of wavefront row wm holds the tile's rows 16 * (f * WM + wm) and on, so that a tile with few rows leaves
+// each wavefront as many: only those are fetched, read and multiplied (256 rows high, 2080 -> 2027 us; with 128 rows an
+// expert 566 -> 491).
+//
+// What bounds it, with 64 experts of 7168 -> 4096 with SwiGLU or 256 of 2048 -> 7168. Few rows: the weights' bytes, 322
+// us for 1.9 GB with 32 rows each (5.9 TB/s), 782 to 815 us for 4.2 GB in and out with 96 rows each. Many rows, skewed
+// (1024 a rank, 8 ranks): 1721 to 1830 us, 2.1 to 2.2 POP/s, where the instruction alone reaches 4.2 on such values and
+// 4.8 on constants. Power takes the clock to 1.6 GHz; of those cycles the matrix units are busy in 61 % and LDS reads
+// in 26 %. Cut down (from 2080 us): 1475 without fetches, 1745 with fetches that hit the cache, 2086 without waiting
+// for them, 1612 with the fetches alone; on zeros, which cost little power, 1835. So it is the fetches' way through the
+// caches and their energy, not their latency.
+template <class T, int FR, int NF, int WM, int WN, int RING, bool GLU>
 __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(ProductArgs a)
 {
     constexpr int kThreads = WM * WN * kWave, kRowsW = WN * NF * 16, kRowsX = WM * FR * 16;
-    constexpr int kP = 4 * SUB;                               // 16-byte pieces of a row in a stage
+    constexpr int kSub = 2, kP = 4 * kSub;                    // steps, and 16-byte pieces of a row, in a stage
     constexpr int kLoadsW = kRowsW * kP / kThreads, kLoadsX = kRowsX * kP / kThreads;
     constexpr int kSizeW = kRowsW * kP, kSize = kSizeW + kRowsX * kP;
     constexpr int kBytes = kP * 16;                           // of a row in a stage
     static_assert(kRowsW * kP % kThreads == 0 && kRowsX * kP % kThreads == 0, "every thread carries as many pieces");
-    static_assert(RING >= 2 && RING <= 4 && RING * SUB % 2 == 0, "a fragment's registers are known where it is used");
+    static_assert(RING == 2 || RING == 3, "stages in LDS");
     // a stage's weights, then its inputs; an array a stage, so that the compiler tells them apart
-    __shared__ u32x4 l0[kSize], l1[kSize], l2[RING > 2 ? kSize : 1], l3[RING > 3 ? kSize : 1];
+    __shared__ u32x4 l0[kSize], l1[kSize], l2[RING > 2 ? kSize : 1];
     __shared__ float sw[kRowsW], sx[kRowsX];
-    auto ring = [&](int i) -> u32x4 * { return i % RING == 0 ? l0 : (i % RING == 1 ? l1 : (i % RING == 2 ? l2 : l3)); };
+    auto ring = [&](int i) -> u32x4 * { return i % RING == 0 ? l0 : (i % RING == 1 ? l1 : l2); };
     __shared__ Plan plan;
     const int total = make_plan<kRowsX, kThreads>(a, plan) * a.ntiles;
     const int tid = threadIdx.x, lane = tid % kWave;
@@ -250,20 +274,21 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
     constexpr int kOut = GLU ? NF / 2 : NF, kOwn = NF * 16;   // output fragments and weight rows of a wavefront
     const int half = a.n / 2, stages = a.k / kBytes;
     // piece p of row q in LDS
-    auto place = [](int q, int p) { return kP == 8 ? q * 8 + (p ^ (q & 7)) : q * 4 + (p ^ ((q >> 1) & 3)); };
-    // a reader's pieces in each step: of fragment 0; the weights' others lie 16 rows apart, the inputs' 16 * WM (so that a
-    // tile with few rows has as many for each wavefront)
-    int wfrag[SUB], xfrag[SUB];
+    auto place = [](int q, int p) { return q * kP + (p ^ (q & 7)); };
+    // a reader's pieces in each step: of fragment 0; the weights' others lie 16 rows apart, the inputs' 16 * WM (so
+    // that a tile with few rows has as many for each wavefront)
+    int wfrag[kSub], xfrag[kSub];
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) {
+    for (int u = 0; u < kSub; ++u) {
         wfrag[u] = wn * kOwn * kP + place(r, 4 * u + g);
         xfrag[u] = kSizeW + wm * 16 * kP + place(r, 4 * u + g);
     }
     // the piece that this thread fetches of its rows (rows of its later pieces are a multiple of 8 on)
-    const int piece = kP == 8 ? tid % 8 ^ (tid / 8 % 8) : tid % 4 ^ (tid / 8 % 4);
+    const int piece = tid % kP ^ (tid / kP % 8);
 
-    // Each XCD (workgroups go to the eight in turn) begins an eighth of the stages further on, and after the last one comes
-    // the first: the sums are whole numbers, whose order does not matter, and the XCDs read different memory at a time.
+    // Each XCD (workgroups go to the eight in turn) begins an eighth of the stages further on, and after the last one
+    // comes the first: the sums are whole numbers, whose order does not matter, and the XCDs read different memory at a
+    // time.
     const int turn = (int)(blockIdx.x % 8) * stages / 8;
 
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
@@ -291,9 +316,9 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
         for (int f = 0; f < FR; ++f)
 #pragma unroll
             for (int j = 0; j < NF; ++j) acc[f][j] = i32x4{0, 0, 0, 0};
-        // Fetches FROM..TO-1 of a whole stage's: the weights', then `loads` of the inputs'. Beyond the last stage the last
-        // one is fetched again, and not used: a branch here would part the steps that it stands between, and the waits
-        // count the fetches.
+        // Fetches FROM..TO-1 of a whole stage's: the weights', then `loads` of the inputs'. Beyond the last stage the
+        // last one is fetched again, and not used: a branch here would part the steps that it stands between, and the
+        // waits count the fetches.
         auto fetch = [&](auto loads, int stage, int slot, int from, int to) {
             int at = min(stage, stages - 1) + turn;
             at -= at >= stages ? stages : 0;
@@ -309,11 +334,11 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
         u32x4 wf[2][NF], xf[2][FR];
         // fragments of step i, counted over the ring
         auto read_w = [&](int i) {
-            const u32x4 *l = ring(i / SUB) + wfrag[i % SUB];
+            const u32x4 *l = ring(i / kSub) + wfrag[i % kSub];
 #pragma unroll
             for (int j = 0; j < NF; ++j) wf[i & 1][j] = l[j * 16 * kP];
         };
-        auto read_x = [&](int i, int f) { xf[i & 1][f] = (ring(i / SUB) + xfrag[i % SUB])[f * WM * 16 * kP]; };
+        auto read_x = [&](int i, int f) { xf[i & 1][f] = (ring(i / kSub) + xfrag[i % kSub])[f * WM * 16 * kP]; };
         auto multiply = [&](int i, int f) {
 #pragma unroll
             for (int j = 0; j < NF; ++j)
@@ -337,17 +362,19 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
                 for (int s = 0; s < RING; ++s) {
                     if (s0 + s >= stages) break;
 #pragma unroll
-                    for (int u = 0; u < SUB; ++u) {
-                        const int i = s * SUB + u, next = (i + 1) % (RING * SUB);
+                    for (int u = 0; u < kSub; ++u) {
+                        const int i = s * kSub + u, next = (i + 1) % (RING * kSub);
 #pragma unroll
                         for (int f = 0; f < LIVE - LAST; ++f) {
                             read_x(i, f + LAST);
                             multiply(i, f);
-                            if (u == 0) fetch(Loads(), s0 + s + RING - 1, (s + RING - 1) % RING, 2 * f, f == LIVE - LAST - 1 ? kAll : 2 * f + 2);
+                            if (u == 0)
+                                fetch(Loads(), s0 + s + RING - 1, (s + RING - 1) % RING, 2 * f,
+                                      f == LIVE - LAST - 1 ? kAll : 2 * f + 2);
                             __builtin_amdgcn_sched_barrier(0);
                         }
                         if (LIVE == LAST && u == 0) fetch(Loads(), s0 + s + RING - 1, (s + RING - 1) % RING, 0, kAll);
-                        if (u == SUB - 1) barrier_fetched<kLeft>();
+                        if (u == kSub - 1) barrier_fetched<kLeft>();
                         read_w(next);
 #pragma unroll
                         for (int f = 0; f < LAST; ++f) read_x(next, f);
@@ -387,7 +414,7 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
             }
             __syncthreads();
 #pragma unroll
-            for (int u = 0; u < SUB; ++u) {
+            for (int u = 0; u < kSub; ++u) {
                 read_w(u);
 #pragma unroll
                 for (int f = 0; f < FR; ++f) {
@@ -441,12 +468,12 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
     }
 }
 
-// Rows of a tile, for `each` rows an expert (masked pairs' among them: no more is known here): 32 (two workgroups on a CU,
-// the most weights on their way and the most tiles), 128 (three stages) or 256 (two; the fewest bytes for a product).
-// Measured with 64 experts, 7168 -> 4096 with SwiGLU, 1 / 16 / 32 / 64 / 128 / 160 / 256 rows each: 238, 347, 372, 517, 794, 949
-// and 1407 us with 32 rows; 236, 348, 344, 356, 458, 514 and 701 with 128; 286, 408, 428, 437, 482, 505 and 699 with 256.
-// 8 experts of 1 row: 28, 33 and 53. 256 experts, 2048 -> 7168, 96 / 128 / 192 / 256 rows: 841, 1049, 1408 and 1635 with 128, 992,
-// 1050, 1180 and 1483 with 256.
+// Rows of a tile, for `each` rows an expert (masked pairs' among them: no more is known here): 32 (two workgroups on a
+// CU, the most weights on their way and the most tiles), 128 (three stages) or 256 (two; the fewest bytes for a
+// product). Measured with 64 experts, 7168 -> 4096 with SwiGLU, 1 / 16 / 32 / 64 / 128 / 160 / 256 rows each: 238, 347,
+// 372, 517, 794, 949 and 1407 us with 32 rows; 236, 348, 344, 356, 458, 514 and 701 with 128; 286, 408, 428, 437, 482,
+// 505 and 699 with 256. 8 experts of 1 row: 28, 33 and 53. 256 experts, 2048 -> 7168, 96 / 128 / 192 / 256 rows: 841,
+// 1049, 1408 and 1635 with 128, 992, 1050, 1180 and 1483 with 256.
 int tile_rows(int each) { return each <= 20 ? 32 : each <= 144 ? 128 : 256; }
 
 int check_rows(long long rows, int cols, int dtype)
@@ -494,6 +521,9 @@ int moe_int8_quantize(const void *x, int64_t rows, int cols, int dtype, int8_t *
     if (!aligned_to(x, dtype) || !aligned(scales, 4)) return MOE_ERR_ALIGN;
     RowsArgs a = rows_args(x, codes, rows, cols);
     a.scales_out = scales;
+    // An input that fills the Infinity Cache passes it by: bf16 [32768, 7168] 115 us, 128 through it; a smaller one may
+    // lie in it, fresh from the kernel before: [8192, 7168] 32 us past it, 28 through it.
+    const bool once = rows * cols * (dtype == MOE_FP32 ? 4 : 2) >= kOnceBytes;
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
     by_type(dtype, [&](auto type) {
@@ -501,7 +531,9 @@ int moe_int8_quantize(const void *x, int64_t rows, int cols, int dtype, int8_t *
         auto launch = [&](auto lanes, auto held) {
             constexpr int kLanes = decltype(lanes)::value, kRows = kRowThreads / kLanes;
             const dim3 g((unsigned)std::min<long long>((rows + kRows - 1) / kRows, 1 << 20));
-            hipLaunchKernelGGL((quantize_kernel<T, kLanes, decltype(held)::value>), g, dim3(kRowThreads), 0, st, a);
+            constexpr int kHeld = decltype(held)::value;
+            if (once) hipLaunchKernelGGL((quantize_kernel<T, kLanes, kHeld, kHeld != 0>), g, dim3(kRowThreads), 0, st, a);
+            else hipLaunchKernelGGL((quantize_kernel<T, kLanes, kHeld, false>), g, dim3(kRowThreads), 0, st, a);
         };
         using std::integral_constant;
         using Some = integral_constant<int, 16>;
@@ -583,9 +615,9 @@ int moe_expert_product_int8(const int8_t *x, const float *x_scales, const int8_t
     auto launch = [&](auto type, auto act) {
         using T = decltype(type);
         constexpr bool kGlu = decltype(act)::value;
-        if (tall == 32) hipLaunchKernelGGL((expert_product_kernel<T, 2, 2, 1, 4, 2, 3, kGlu>), g, b, 0, st, a);
-        else if (tall == 128) hipLaunchKernelGGL((expert_product_kernel<T, 4, 4, 2, 4, 2, 3, kGlu>), g, b, 0, st, a);
-        else hipLaunchKernelGGL((expert_product_kernel<T, 8, 4, 2, 4, 2, 2, kGlu>), g, b, 0, st, a);
+        if (tall == 32) hipLaunchKernelGGL((expert_product_kernel<T, 2, 2, 1, 4, 3, kGlu>), g, b, 0, st, a);
+        else if (tall == 128) hipLaunchKernelGGL((expert_product_kernel<T, 4, 4, 2, 4, 3, kGlu>), g, b, 0, st, a);
+        else hipLaunchKernelGGL((expert_product_kernel<T, 8, 4, 2, 4, 2, kGlu>), g, b, 0, st, a);
     };
     if (dtype == MOE_FP16 && glu) launch(F16(), std::true_type());
     else if (dtype == MOE_FP16) launch(F16(), std::false_type());
