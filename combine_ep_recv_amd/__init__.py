@@ -14,11 +14,17 @@ or ``__graft_entry__.build()``).
 
 Around them: ``gate`` makes expert_ids and expert_scales from a router's logits
 (``gate_backward`` its gradient), and ``quantize_mx`` / ``expert_product`` run
-the experts on microscaled rows and 4-bit weights:
+the experts on microscaled rows and 4-bit weights, ``quantize_int8`` /
+``expert_product`` on int8 rows and weights:
 
     expert_ids, expert_scales = gate(logits, topk)
     rows, row_scales, assist_info, ep_recv_count = dispatch(..., quant_mode=MOE_QUANT_MX)
     y = expert_product(rows, row_scales, weights, weight_scales, ep_recv_count)
+
+``combine_backward`` and ``dispatch_backward`` are the gradients of the two calls:
+
+    grad_rows, grad_scales = combine_backward(grad_out, expand_x, ...)
+    grad_x = dispatch_backward(grad_expand_x, ...)
 """
 from __future__ import annotations
 

@@ -1,6 +1,7 @@
 /*
- * moe_ep.h -- MoE token dispatch and combine on one MI355X (gfx950), with the gate
- * that routes the tokens and the experts' product on microscaled rows.
+ * moe_ep.h -- MoE token dispatch and combine on one MI355X (gfx950) and their
+ * gradients, with the gate that routes the tokens and the experts' products on
+ * microscaled and int8 rows.
  *
  * C ABI. Every tensor argument is a plain DEVICE pointer to row-major,
  * densely packed memory that the caller allocated and owns; sizes are plain
@@ -67,7 +68,8 @@ enum moe_status {
     MOE_ERR_MASK = 9       /* unknown mask kind, or a mask pointer that does not match it */
 };
 
-/* Token element types. MOE_FP32 is taken by the gate and by microscaled quantisation, not by dispatch or combine. */
+/* Token element types. MOE_FP32 is taken by the gate and by the quantisation of rows, not by dispatch or combine;
+ * MOE_INT32 by dispatch and combine alone. */
 enum moe_dtype { MOE_INT32 = 0, MOE_FP16 = 1, MOE_BF16 = 2, MOE_FP32 = 3 };
 
 /* Quantisation modes; the numbering follows quantMode of
