@@ -549,6 +549,38 @@ def _check_routing(assist_info, ep_recv_count, expert_ids, N, K, ep_world, exper
     _check_tensor("expert_ids", expert_ids, torch.int32, (N, K), device)
 
 
+def _combine_backward(head, grad_expand_x, grad_scales, grad_out, expand_x, assist_info, ep_recv_count, expert_ids,
+                      expert_scales, ep_world, experts_per_rank, workspace, x_active_mask, zero_experts, copy_experts,
+                      ori_x, grad_ori_x, const_experts, const_x, grad_const_x):
+    """moe_combine_backward on outputs that have been checked (or made); head: _row_call's result."""
+    fn = "moe_combine_backward"
+    dev, N, K, h, dt = head
+    dtype = expand_x.dtype
+    _check_routing(assist_info, ep_recv_count, expert_ids, N, K, ep_world, experts_per_rank, dev)
+    _check_tensor("expand_x", expand_x, dtype, (N * K, h), dev)
+    _check_tensor("grad_out", grad_out, dtype, (N, h), dev)
+    _check_tensor("expert_scales", expert_scales, torch.float32, (N, K), dev)
+    mp, mk = (None, MOE_MASK_NONE) if x_active_mask is None else _mask_args(x_active_mask, N, K, dev)
+    special = None
+    if zero_experts or copy_experts or const_experts:
+        _check_int(fn, zero_experts | copy_experts | const_experts)
+        for name, count, t, shape in (("ori_x", copy_experts, ori_x, (N, h)),
+                                      ("const_x", const_experts, const_x, (const_experts, h))):
+            if count and t is None:
+                raise MoeError(fn, MOE_ERR_NULLPTR, "%s is needed: it was combine's" % name)
+            if count:
+                _check_tensor(name, t, dtype, shape, dev)
+        special = _special(zero_experts, copy_experts, ori_x, const_experts, const_x)
+    if workspace is not None:
+        _check_tensor("workspace", workspace, torch.uint8, (workspace.numel(),), dev)
+    elif grad_const_x is not None:
+        workspace = combine_backward_workspace(ep_world, N // ep_world, experts_per_rank, h, K, dtype, const_experts, dev)
+    _launch(fn, dev, grad_out.data_ptr(), expand_x.data_ptr(), assist_info.data_ptr(), ep_recv_count.data_ptr(),
+            expert_ids.data_ptr(), expert_scales.data_ptr(), mp, mk, special, ep_world, N // ep_world, experts_per_rank, h,
+            K, dt, grad_expand_x.data_ptr(), grad_scales.data_ptr(), _address(grad_ori_x), _address(grad_const_x),
+            _address(workspace), 0 if workspace is None else workspace.numel(), _stream_ptr(dev))
+
+
 def combine_backward_into(grad_expand_x: torch.Tensor, grad_scales: torch.Tensor, grad_out: torch.Tensor,
                           expand_x: torch.Tensor, assist_info: torch.Tensor, ep_recv_count: torch.Tensor,
                           expert_ids: torch.Tensor, expert_scales: torch.Tensor, ep_world: int, experts_per_rank: int,
@@ -558,27 +590,13 @@ def combine_backward_into(grad_expand_x: torch.Tensor, grad_scales: torch.Tensor
                           const_x: Optional[torch.Tensor] = None, grad_const_x: Optional[torch.Tensor] = None):
     """moe_combine_backward into preallocated grad_expand_x [rows, h] (rows behind the last counted one are left as
     they were), grad_scales fp32 [N, topk] and, when given, grad_ori_x [N, h] and grad_const_x [const_experts, h], on
-    the current stream. See combine_backward for the rest."""
+    the current stream. workspace: combine_backward_workspace's, needed (and otherwise made) for grad_const_x. See
+    combine_backward for the rest."""
     fn = "moe_combine_backward"
-    dev, N, K, h, dt = _row_call(fn, expand_x, expert_ids, ep_world, experts_per_rank)
-    _check_routing(assist_info, ep_recv_count, expert_ids, N, K, ep_world, experts_per_rank, dev)
-    _check_tensor("expand_x", expand_x, expand_x.dtype, (N * K, h), dev)
-    _check_tensor("grad_out", grad_out, expand_x.dtype, (N, h), dev)
-    _check_tensor("expert_scales", expert_scales, torch.float32, (N, K), dev)
+    head = _row_call(fn, expand_x, expert_ids, ep_world, experts_per_rank)
+    dev, N, K, h, _ = head
     _check_tensor("grad_expand_x", grad_expand_x, expand_x.dtype, (N * K, h), dev)
     _check_tensor("grad_scales", grad_scales, torch.float32, (N, K), dev)
-    mp, mk = _mask_args(x_active_mask, N, K, dev)
-    special = None
-    if zero_experts or copy_experts or const_experts:
-        zero_experts, copy_experts, const_experts = int(zero_experts), int(copy_experts), int(const_experts)
-        _check_int(fn, zero_experts | copy_experts | const_experts)
-        for name, count, t, shape in (("ori_x", copy_experts, ori_x, (N, h)),
-                                      ("const_x", const_experts, const_x, (const_experts, h))):
-            if count and t is None:
-                raise MoeError(fn, MOE_ERR_NULLPTR, "%s is needed: it was combine's" % name)
-            if count:
-                _check_tensor(name, t, expand_x.dtype, shape, dev)
-        special = _special(zero_experts, copy_experts, ori_x, const_experts, const_x)
     for name, count, t, shape in (("grad_ori_x", copy_experts, grad_ori_x, (N, h)),
                                   ("grad_const_x", const_experts, grad_const_x, (const_experts, h))):
         if t is None:
@@ -586,15 +604,9 @@ def combine_backward_into(grad_expand_x: torch.Tensor, grad_scales: torch.Tensor
         if not count:
             raise MoeError(fn, MOE_ERR_NULLPTR, "%s without such experts" % name)
         _check_tensor(name, t, expand_x.dtype, shape, dev)
-    if grad_const_x is not None and workspace is None:
-        workspace = combine_backward_workspace(ep_world, N // ep_world, experts_per_rank, h, K, expand_x.dtype,
-                                               const_experts, dev)
-    elif workspace is not None:
-        _check_tensor("workspace", workspace, torch.uint8, (workspace.numel(),), dev)
-    _launch(fn, dev, grad_out.data_ptr(), expand_x.data_ptr(), assist_info.data_ptr(), ep_recv_count.data_ptr(),
-            expert_ids.data_ptr(), expert_scales.data_ptr(), mp, mk, special, ep_world, N // ep_world, experts_per_rank, h,
-            K, dt, grad_expand_x.data_ptr(), grad_scales.data_ptr(), _address(grad_ori_x), _address(grad_const_x),
-            _address(workspace), 0 if workspace is None else workspace.numel(), _stream_ptr(dev))
+    _combine_backward(head, grad_expand_x, grad_scales, grad_out, expand_x, assist_info, ep_recv_count, expert_ids,
+                      expert_scales, ep_world, experts_per_rank, workspace, x_active_mask, int(zero_experts),
+                      int(copy_experts), ori_x, grad_ori_x, int(const_experts), const_x, grad_const_x)
     return grad_expand_x, grad_scales
 
 
@@ -611,16 +623,33 @@ def combine_backward(grad_out: torch.Tensor, expand_x: torch.Tensor, assist_info
     behind the last counted one uninitialised; grad_scales[t, k] is the product of the pair's row (ori_x[t], const_x[j])
     with grad_out[t], and 0 for a zero expert's or an inactive pair: gate_backward takes it.
     """
-    _gpu_device("expand_x", expand_x)
-    _gpu_device("expert_ids", expert_ids)
-    dev = expand_x.device
-    made = (torch.empty_like(expand_x), _new(tuple(expert_ids.shape), torch.float32, dev))
-    ori = torch.empty_like(ori_x) if copy_experts and ori_x is not None else None
-    const = torch.empty_like(const_x) if const_experts and const_x is not None else None
-    combine_backward_into(*made, grad_out, expand_x, assist_info, ep_recv_count, expert_ids, expert_scales, ep_world,
-                          experts_per_rank, None, x_active_mask, zero_experts, copy_experts, ori_x, ori, const_experts,
-                          const_x, const)
+    head = _row_call("moe_combine_backward", expand_x, expert_ids, ep_world, experts_per_rank)
+    dev, N, K, h, _ = head
+    made = (_new((N * K, h), expand_x.dtype, dev), _new((N, K), torch.float32, dev))
+    zero_experts, copy_experts, const_experts = int(zero_experts), int(copy_experts), int(const_experts)
+    ori = _new((N, h), expand_x.dtype, dev) if copy_experts > 0 and ori_x is not None else None
+    const = torch.empty_like(const_x) if const_experts > 0 and isinstance(const_x, torch.Tensor) else None
+    _combine_backward(head, *made, grad_out, expand_x, assist_info, ep_recv_count, expert_ids, expert_scales, ep_world,
+                      experts_per_rank, None, x_active_mask, zero_experts, copy_experts, ori_x, ori, const_experts, const_x,
+                      const)
     return made + tuple(t for t in (ori, const) if t is not None)
+
+
+def _dispatch_backward(head, grad_x, grad_expand_x, assist_info, ep_recv_count, expert_ids, ep_world, experts_per_rank,
+                       x_active_mask, add, grad_expand_scales, grad_scales):
+    """moe_dispatch_backward on outputs that have been checked (or made); head: _row_call's result."""
+    fn = "moe_dispatch_backward"
+    dev, N, K, h, dt = head
+    _check_routing(assist_info, ep_recv_count, expert_ids, N, K, ep_world, experts_per_rank, dev)
+    _check_tensor("grad_expand_x", grad_expand_x, grad_expand_x.dtype, (N * K, h), dev)
+    if add is not None:
+        _check_tensor("add", add, grad_expand_x.dtype, (N, h), dev)
+    if grad_expand_scales is not None:
+        _check_tensor("grad_expand_scales", grad_expand_scales, torch.float32, (N * K,), dev)
+    mp, mk = (None, MOE_MASK_NONE) if x_active_mask is None else _mask_args(x_active_mask, N, K, dev)
+    _launch(fn, dev, grad_expand_x.data_ptr(), assist_info.data_ptr(), ep_recv_count.data_ptr(), expert_ids.data_ptr(),
+            _address(grad_expand_scales), _address(add), mp, mk, ep_world, N // ep_world, experts_per_rank, h, K, dt,
+            grad_x.data_ptr(), _address(grad_scales), _stream_ptr(dev))
 
 
 def dispatch_backward_into(grad_x: torch.Tensor, grad_expand_x: torch.Tensor, assist_info: torch.Tensor,
@@ -631,22 +660,15 @@ def dispatch_backward_into(grad_x: torch.Tensor, grad_expand_x: torch.Tensor, as
     """moe_dispatch_backward into a preallocated grad_x [N, h] (which may be add itself) and, with grad_expand_scales,
     grad_scales fp32 [N, topk], on the current stream. See dispatch_backward for the rest."""
     fn = "moe_dispatch_backward"
-    dev, N, K, h, dt = _row_call(fn, grad_expand_x, expert_ids, ep_world, experts_per_rank)
-    _check_routing(assist_info, ep_recv_count, expert_ids, N, K, ep_world, experts_per_rank, dev)
-    dtype = grad_expand_x.dtype
-    _check_tensor("grad_expand_x", grad_expand_x, dtype, (N * K, h), dev)
-    _check_tensor("grad_x", grad_x, dtype, (N, h), dev)
-    if add is not None:
-        _check_tensor("add", add, dtype, (N, h), dev)
+    head = _row_call(fn, grad_expand_x, expert_ids, ep_world, experts_per_rank)
+    dev, N, K, h, _ = head
+    _check_tensor("grad_x", grad_x, grad_expand_x.dtype, (N, h), dev)
     if (grad_expand_scales is None) != (grad_scales is None):
         raise MoeError(fn, MOE_ERR_NULLPTR, "grad_expand_scales and grad_scales go together")
     if grad_scales is not None:
-        _check_tensor("grad_expand_scales", grad_expand_scales, torch.float32, (N * K,), dev)
         _check_tensor("grad_scales", grad_scales, torch.float32, (N, K), dev)
-    mp, mk = _mask_args(x_active_mask, N, K, dev)
-    _launch(fn, dev, grad_expand_x.data_ptr(), assist_info.data_ptr(), ep_recv_count.data_ptr(), expert_ids.data_ptr(),
-            _address(grad_expand_scales), _address(add), mp, mk, ep_world, N // ep_world, experts_per_rank, h, K, dt,
-            grad_x.data_ptr(), _address(grad_scales), _stream_ptr(dev))
+    _dispatch_backward(head, grad_x, grad_expand_x, assist_info, ep_recv_count, expert_ids, ep_world, experts_per_rank,
+                       x_active_mask, add, grad_expand_scales, grad_scales)
     return grad_x
 
 
@@ -659,15 +681,12 @@ def dispatch_backward(grad_expand_x: torch.Tensor, assist_info: torch.Tensor, ep
     [N, h] is what else flows back to the tokens, combine_backward's grad_ori_x among it. With grad_expand_scales
     fp32 [rows], the gradient of dispatch's expand_scales, returns (grad_x, grad_scales fp32 [N, topk]), else
     grad_x [N, h]. Pairs of special experts and inactive ones have no row and get 0."""
-    _gpu_device("grad_expand_x", grad_expand_x)
-    _gpu_device("expert_ids", expert_ids)
-    if grad_expand_x.dim() != 2 or expert_ids.dim() != 2:
-        raise MoeError("moe_dispatch_backward", MOE_ERR_SHAPE, "grad_expand_x and expert_ids must be 2-D")
-    dev, (N, K) = grad_expand_x.device, expert_ids.shape
-    out = _new((N, grad_expand_x.shape[1]), grad_expand_x.dtype, dev)
+    head = _row_call("moe_dispatch_backward", grad_expand_x, expert_ids, ep_world, experts_per_rank)
+    dev, N, K, h, _ = head
+    out = _new((N, h), grad_expand_x.dtype, dev)
     scales = _new((N, K), torch.float32, dev) if grad_expand_scales is not None else None
-    dispatch_backward_into(out, grad_expand_x, assist_info, ep_recv_count, expert_ids, ep_world, experts_per_rank,
-                           x_active_mask, add, grad_expand_scales, scales)
+    _dispatch_backward(head, out, grad_expand_x, assist_info, ep_recv_count, expert_ids, ep_world, experts_per_rank,
+                       x_active_mask, add, grad_expand_scales, scales)
     return out if scales is None else (out, scales)
 
 

@@ -164,6 +164,20 @@ def test_dispatch_backward_rejects_before_the_call(rec, field, value):  # noqa: 
     assert rec.calls == []
 
 
+@pytest.mark.parametrize("kw", [dict(const_experts=BIG, const_x=torch.zeros(1, H).bfloat16()), dict(const_experts=2),
+                                dict(const_experts=2, const_x=torch.zeros(1, H).bfloat16()), dict(copy_experts=1),
+                                dict(copy_experts=1, ori_x=torch.zeros(N_, H)), dict(const_experts=1, const_x=3),
+                                dict(const_experts=2, const_x=torch.zeros(H, 2).bfloat16().t()), dict(zero_experts=-1),
+                                dict(expand_x=torch.zeros(N_ * K_, H, dtype=torch.int32)), dict(ep_world=4)], ids=str)
+def test_combine_backward_refuses_before_it_makes_room(rec, kw):  # noqa: F811
+    a = _combine_args()
+    del a["grad_expand_x"], a["grad_scales"]
+    a.update(kw)
+    with pytest.raises(moe.MoeError):
+        moe.combine_backward(**a)
+    assert rec.calls == []
+
+
 def test_gradients_of_cpu_tensors_are_rejected():
     with pytest.raises(moe.MoeError):
         moe.combine_backward_into(**_combine_args())
@@ -214,6 +228,10 @@ SHAPES = [
     (768, 2, 1, 3, 24, (0, 0, 0), "pair", 0.0), (70, 9, 14, 70, 48, (3, 3, 3), "pair", 0.0),
     (2, 4, 512, 200, 32, (0, 0, 0), "pair", 0.0), (2, 9, 512, 1000, 16, (1, 1, 1), None, 0.0),
     (4, 5, 2, 2, 24, (0, 1, 1), "none", 0.0), (4, 5, 2, 2, 24, (1, 1, 1), "no token", 0.0),
+    (4, 9000, 2, 3, 20, (1, 1, 2), "pair", 0.0),         # parts of the tokens that are listed in several pieces
+    (2, 40000, 1, 1, 9, (0, 0, 1), None, -9.0),          # a const expert with nearly every pair: full lists
+    (4, 2100, 2, 4, 4099, (0, 1, 1), "token", 0.0),      # rows that fill the Infinity Cache, at odd offsets
+    (2, 1, 2, 2, 200003, (0, 1, 1), None, 0.0),
 ]
 TYPES = [torch.bfloat16, torch.float16]
 
@@ -565,3 +583,31 @@ def test_a_training_step_of_the_layer():
     dot = (f * (X.detach().abs() * G.double().abs()).sum(1)[:, None]).max(1).values[:, None]
     assert ((gl.cpu().double() - L.grad).abs() <= 2 * (1 + K) * (chain(h) + 40) * u * dot).all()
     assert A < N * K and (gl != 0).any()
+
+
+@pytest.mark.gpu
+def test_gradients_of_rows_beyond_4_gib():
+    """300000 rows of 14336 bytes: tokens whose rows lie on both sides of the 4 GiB line, the first and the last ones."""
+    W, bs, epr, K, h = 2, 18750, 4, 8, 7168
+    N = W * bs
+    g = torch.Generator(DEV).manual_seed(61)
+    ids = torch.rand(N, W * epr, generator=g, device=DEV).argsort(dim=1)[:, :K].int().contiguous()   # every expert
+    w = torch.randn(N, K, generator=g, device=DEV)
+    x = torch.randn(N, h, generator=g, device=DEV, dtype=torch.bfloat16)
+    y, _, assist, counts = moe.dispatch(x, ids, W, epr)
+    assert y.numel() * 2 > 1 << 32
+    gy, gw = moe.combine_backward(x, y, assist, counts, ids, w, W, epr)
+    gx = moe.dispatch_backward(y, assist, counts, ids, W, epr)
+    row = torch.empty(N * K, dtype=torch.int64, device=DEV)
+    a = assist.long()
+    row[(a[:, 0] * bs + a[:, 1]) * K + a[:, 2]] = torch.arange(N * K, device=DEV)
+    row = row.view(N, K)
+    line = (1 << 32) // (2 * h)
+    near = a[line - 20:line + 20, 0] * bs + a[line - 20:line + 20, 1]
+    for t in torch.cat((torch.tensor([0, 1, bs - 1, bs, N - 1], device=DEV), near)).tolist():
+        assert torch.equal(gy[row[t]], (w[t][:, None] * x[t].float()).bfloat16())
+        # dispatch's rows are the token: the weights' gradients are its square, the tokens' eight times itself
+        size = x[t].double().square().sum()
+        assert ((gw[t].double() - size).abs() <= 1.01 * chain(h) * 2.0 ** -24 * size).all()
+        assert torch.equal(gx[t], x[t] * 8)
+    torch.cuda.empty_cache()
