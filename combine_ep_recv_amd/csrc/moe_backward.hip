@@ -22,9 +22,13 @@ namespace {
 using namespace moe_detail;
 
 constexpr long long kMaxTokens = (1ll << 24) - 1;
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
 constexpr int kPiece = 8;                  // elements of 16 bytes
+// Threads of a workgroup, by the columns alone, so that a sum's order goes by them alone: one wavefront up to so many,
+// four above. 8 ranks x 1024 tokens, 512 columns: combine's gradient 27.0 us, dispatch's 17.9, with four 46.6 and 23.0;
+// 16 x 256, 1024 columns 23.7 and 15.1, 29.7 and 16.6; 4 x 515, 2048 columns 20.6 and 13.5, 22.5 and 15.2; 16 x 256,
+// 7168 columns 193 and 104, 203 and 100, but 8 x 32 24.7 and 9.5, 16.9 and 8.8.
+constexpr int kNarrow = 64, kWide = 256, kNarrowCols = 2048;
+int threads_of(int h) { return h <= kNarrowCols ? kNarrow : kWide; }
 // Rows that fill the Infinity Cache pass the caches by: 16 ranks x 256 tokens, top-8, bf16 rows of 7168, combine's
 // gradient 203 us and dispatch's 100, 217 and 106 through them; smaller ones may lie in them, fresh from the experts: 8
 // ranks x 32 tokens 15.4 and 7.9 us through them, 16.9 and 8.8 past them.
@@ -140,8 +144,6 @@ __device__ __forceinline__ u32x4 pack(const float (&x)[kPiece])
 // of the tokens: it lists the part's pairs of expert j in order, then adds their rows, and a second kernel joins the
 // parts. These workgroups come first in combine's launch (a launch of their own is 8 us more with 4 ranks of 515
 // tokens).
-constexpr int kScan = 4 * kThreads;        // pairs looked at between two lists
-constexpr int kSliceCols = kThreads * kPiece;
 constexpr int kMostSplits = 64, kSplitTokens = 32, kAhead = 8;
 
 struct ConstArgs {
@@ -154,20 +156,22 @@ struct ConstArgs {
     int mask_kind, N, K, h, first_id, slices, splits, per, join_slices;
 };
 
+template <int THREADS>
 struct ConstList {
-    int pair[kScan];
-    int count[4][kWaves];
+    int pair[4 * THREADS];                 // of as many looked at between two lists
+    int count[4][THREADS / kWave];
 };
 
-template <class T>
-__device__ __forceinline__ void const_backward(const ConstArgs &a, int block, ConstList &found)
+template <class T, int THREADS>
+__device__ __forceinline__ void const_backward(const ConstArgs &a, int block, ConstList<THREADS> &found)
 {
+    constexpr int kWaves = THREADS / kWave, kScan = 4 * THREADS;
     int(&list)[kScan] = found.pair;
     int(&count)[4][kWaves] = found.count;
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const int j = block / (a.slices * a.splits), q = block - j * (a.slices * a.splits);
     const int split = q / a.slices;
-    const long long at = (long long)(q - split * a.slices) * kSliceCols + tid * kPiece;
+    const long long at = (long long)(q - split * a.slices) * (THREADS * kPiece) + tid * kPiece;
     const int id = a.first_id + j;
     // columns of this lane, the last eight where it has fewer (those of its neighbour among them, which both store)
     const int live = at >= a.h ? 0 : min(a.h, kPiece);
@@ -181,7 +185,7 @@ __device__ __forceinline__ void const_backward(const ConstArgs &a, int block, Co
         bool mine[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const long long p = base + u * kThreads + tid;
+            const long long p = base + u * THREADS + tid;
             mine[u] = p < to && a.ids[p] == id;
             if (mine[u] && a.mask_kind != MOE_MASK_NONE)
                 mine[u] = a.mask[a.mask_kind == MOE_MASK_TOKEN ? p / a.K : p] != 0;
@@ -198,7 +202,7 @@ __device__ __forceinline__ void const_backward(const ConstArgs &a, int block, Co
                 if (i < wave) at += count[u][i];
                 total += count[u][i];
             }
-            if (mine[u]) list[at + __popcll(hit[u] & ((1ull << lane) - 1))] = (int)(base + u * kThreads + tid);
+            if (mine[u]) list[at + __popcll(hit[u] & ((1ull << lane) - 1))] = (int)(base + u * THREADS + tid);
         }
         __syncthreads();
         // kAhead rows on their way at a time; the list's last pair stands in for those past its end
@@ -256,21 +260,21 @@ struct CombineBackwardArgs {
 
 // A workgroup takes token t and every `parts`th block of KB of its pairs: g[t] is read once for KB rows, which are read
 // and written once. Rows in pieces of 16 bytes a lane (at any alignment), the h % 8 last elements one a lane. Each lane
-// adds the products of its own columns, eight neighbours in order and then those 2048 on; a wavefront's lanes and then
-// the four wavefronts are joined in a fixed order, the same for every KB.
+// adds the products of its own columns, eight neighbours in order and then those 8 * THREADS on; a wavefront's lanes
+// and then the wavefronts are joined in a fixed order, the same for every KB.
 //
 // Memory bounds it: 3 operations an element of 4 bytes. 16 ranks x 256 tokens, top-8, bf16 rows of 7168: 1.0 GB in 197
-// to 203 us, 4.9 to 5.1 TB/s, where a large copy reaches 5.2. A wavefront for a token and all of its rows takes 193 us
-// there, but 24.7 for 16.9 with 8 ranks x 32 tokens.
-template <class T, int KB, bool ONCE, bool TABLE>
-__global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineBackwardArgs a)
+// to 203 us, 4.9 to 5.1 TB/s, where a large copy reaches 5.2.
+template <class T, int KB, bool ONCE, bool TABLE, int THREADS>
+__global__ __launch_bounds__(THREADS) void combine_backward_kernel(CombineBackwardArgs a)
 {
+    constexpr int kWaves = THREADS / kWave;
     __shared__ Rows rows;
     __shared__ float part[kWaves][KB];
     int block = blockIdx.x;
     if constexpr (TABLE) {
-        __shared__ ConstList found;
-        if (block < a.table_blocks) return const_backward<T>(a.table, block, found);
+        __shared__ ConstList<THREADS> found;
+        if (block < a.table_blocks) return const_backward<T, THREADS>(a.table, block, found);
         block -= a.table_blocks;
     }
     const int t = block / a.parts, first = block - t * a.parts;
@@ -295,7 +299,7 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineBackw
                                        : a.const_x + (size_t)(kConst - row[i]) * a.h;
             acc[i] = 0.f;
         }
-        for (int c = tid; c < pieces; c += kThreads) {
+        for (int c = tid; c < pieces; c += THREADS) {
             u32x4 v[KB];
             const u32x4 gv = *reinterpret_cast<const u32x4_a2 *>(g + c * kPiece);
 #pragma unroll
@@ -343,7 +347,7 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineBackw
             if (rows.row[k] == kCopy) w += a.w[(size_t)t * K + k];
         w = wave_sum(w);
         uint16_t *o = a.grad_ori + (size_t)t * a.h;
-        for (int c = tid; c < pieces; c += kThreads) {
+        for (int c = tid; c < pieces; c += THREADS) {
             float x[kPiece];
             unpack<T>(*reinterpret_cast<const u32x4_a2 *>(g + c * kPiece), x);
 #pragma unroll
@@ -355,10 +359,10 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(CombineBackw
 }
 
 template <class T>
-__global__ __launch_bounds__(kThreads) void const_join_kernel(ConstArgs a)
+__global__ __launch_bounds__(kWide) void const_join_kernel(ConstArgs a)
 {
     const int j = blockIdx.x / a.join_slices;
-    const long long col = (long long)(blockIdx.x - j * a.join_slices) * kThreads + threadIdx.x;
+    const long long col = (long long)(blockIdx.x - j * a.join_slices) * kWide + threadIdx.x;
     if (col >= a.h) return;
     float v = 0.f;
 #pragma unroll 8
@@ -379,10 +383,10 @@ struct DispatchBackwardArgs {
     int h, slices;
 };
 
-// A workgroup takes token t and every `slices`th 256 pieces of its row, eight rows' pieces on their way at a time.
+// A workgroup takes token t and every `slices`th THREADS pieces of its row, eight rows' pieces on their way at a time.
 // Memory bounds it: 529 MB in 97 to 100 us (5.3 TB/s) at 16 ranks x 256 tokens, top-8, bf16 rows of 7168.
-template <class T, bool ONCE>
-__global__ __launch_bounds__(kThreads) void dispatch_backward_kernel(DispatchBackwardArgs a)
+template <class T, bool ONCE, int THREADS>
+__global__ __launch_bounds__(THREADS) void dispatch_backward_kernel(DispatchBackwardArgs a)
 {
     __shared__ Rows rows;
     const int t = blockIdx.x / a.slices, slice = blockIdx.x - t * a.slices;
@@ -390,7 +394,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_backward_kernel(DispatchBac
     if (tid < kWave) find_rows(a.r, t, rows);
     __syncthreads();
     constexpr int KB = 8;
-    for (int c = slice * kThreads + tid; c < pieces; c += a.slices * kThreads) {
+    for (int c = slice * THREADS + tid; c < pieces; c += a.slices * THREADS) {
         float acc[kPiece];
         u32x4 v[KB];
         if (a.add) {
@@ -425,7 +429,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_backward_kernel(DispatchBac
         a.out[(size_t)t * a.h + rest] = T::store(v);
     }
     if (slice == 0 && a.grad_scales)
-        for (int k = tid; k < K; k += kThreads)
+        for (int k = tid; k < K; k += THREADS)
             a.grad_scales[(size_t)t * K + k] = rows.row[k] >= 0 ? a.grad_scales_in[rows.row[k]] : 0.f;
 }
 
@@ -470,13 +474,18 @@ Routing routing_of(const int32_t *assist, const int32_t *erc, const int32_t *ids
     return r;
 }
 
-// f(element type, whether rows of this many bytes pass the caches by)
+// f(element type, whether rows of this many bytes pass the caches by, threads of a workgroup for h columns)
 template <class F>
-void by_type(int dtype, long long bytes, F f)
+void by_type(int dtype, long long bytes, int h, F f)
 {
     auto sized = [&](auto type) {
-        if (bytes >= kOnceBytes) f(type, std::true_type());
-        else f(type, std::false_type());
+        const bool once = bytes >= kOnceBytes, narrow = threads_of(h) == kNarrow;
+        using Narrow = std::integral_constant<int, kNarrow>;
+        using Wide = std::integral_constant<int, kWide>;
+        if (once && narrow) f(type, std::true_type(), Narrow());
+        else if (once) f(type, std::true_type(), Wide());
+        else if (narrow) f(type, std::false_type(), Narrow());
+        else f(type, std::false_type(), Wide());
     };
     if (dtype == MOE_FP16) sized(F16());
     else sized(BF16());
@@ -497,7 +506,8 @@ int moe_combine_backward_workspace_size(int ep_world, int bs, int experts_per_ra
     if (rc) return rc;
     const int splits = splits_of((long long)ep_world * bs);
     // a launch has fewer than 2^24 workgroups, the tokens' among them
-    const long long slices = std::max((h + kSliceCols - 1ll) / kSliceCols * std::max(splits, 1), (h + kThreads - 1ll) / kThreads);
+    const long long cols = threads_of(h) * kPiece;
+    const long long slices = std::max((h + cols - 1) / cols * std::max(splits, 1), (h + kWide - 1ll) / kWide);
     const long long tokens = std::max((long long)ep_world * bs, kFewPairs);
     if (const_expert_num < 0 || (const_expert_num > 0 && const_expert_num * slices + tokens >= 1ll << 24)) return MOE_ERR_SHAPE;
     *bytes = splits > 1 ? (size_t)const_expert_num * splits * h * sizeof(float) : 0;
@@ -564,23 +574,26 @@ int moe_combine_backward(const void *grad_out, const void *expand_x, const int32
     c.first_id = a.r.copy_end;
     c.splits = std::max(1, splits_of(N));
     c.per = (int)((N + c.splits - 1) / c.splits);
-    c.slices = (int)((h + kSliceCols - 1ll) / kSliceCols);
-    c.join_slices = (int)((h + kThreads - 1ll) / kThreads);
+    const long long cols = threads_of(h) * kPiece;          // of a workgroup at a time
+    c.slices = (int)((h + cols - 1) / cols);
+    c.join_slices = (int)((h + kWide - 1ll) / kWide);
     c.sums = c.splits > 1 ? static_cast<float *>(workspace) : nullptr;
     c.out = static_cast<uint16_t *>(grad_const_x);
     a.table_blocks = table * c.slices * c.splits;
-    const dim3 g((unsigned)(a.table_blocks + N * a.parts)), b(kThreads);
+    const dim3 g((unsigned)(a.table_blocks + N * a.parts));
     const dim3 join((unsigned)(table * c.join_slices));
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
-    by_type(dtype, N * topk * h * 2, [&](auto type, auto once) {
+    by_type(dtype, N * topk * h * 2, h, [&](auto type, auto once, auto threads) {
         using T = decltype(type);
         constexpr bool kOnce = decltype(once)::value;
-        if (few && table) hipLaunchKernelGGL((combine_backward_kernel<T, 1, kOnce, true>), g, b, 0, st, a);
-        else if (few) hipLaunchKernelGGL((combine_backward_kernel<T, 1, kOnce, false>), g, b, 0, st, a);
-        else if (table) hipLaunchKernelGGL((combine_backward_kernel<T, 8, kOnce, true>), g, b, 0, st, a);
-        else hipLaunchKernelGGL((combine_backward_kernel<T, 8, kOnce, false>), g, b, 0, st, a);
-        if (table && c.sums) hipLaunchKernelGGL(const_join_kernel<T>, join, b, 0, st, c);
+        constexpr int kT = decltype(threads)::value;
+        const dim3 b(kT);
+        if (few && table) hipLaunchKernelGGL((combine_backward_kernel<T, 1, kOnce, true, kT>), g, b, 0, st, a);
+        else if (few) hipLaunchKernelGGL((combine_backward_kernel<T, 1, kOnce, false, kT>), g, b, 0, st, a);
+        else if (table) hipLaunchKernelGGL((combine_backward_kernel<T, 8, kOnce, true, kT>), g, b, 0, st, a);
+        else hipLaunchKernelGGL((combine_backward_kernel<T, 8, kOnce, false, kT>), g, b, 0, st, a);
+        if (table && c.sums) hipLaunchKernelGGL(const_join_kernel<T>, join, dim3(kWide), 0, st, c);
     });
     return launched();
 }
@@ -610,10 +623,12 @@ int moe_dispatch_backward(const void *grad_expand_x, const int32_t *assist_info,
     a.h = h;
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
-    a.slices = N <= kFewTokens ? (int)std::min(16ll, (h + kSliceCols - 1ll) / kSliceCols) : 1;
-    by_type(dtype, N * topk * h * 2, [&](auto type, auto once) {
-        hipLaunchKernelGGL((dispatch_backward_kernel<decltype(type), decltype(once)::value>), dim3((unsigned)(N * a.slices)),
-                           dim3(kThreads), 0, st, a);
+    const long long cols = threads_of(h) * kPiece;
+    a.slices = N <= kFewTokens ? (int)std::min(16ll, (h + cols - 1) / cols) : 1;
+    by_type(dtype, N * topk * h * 2, h, [&](auto type, auto once, auto threads) {
+        constexpr int kT = decltype(threads)::value;
+        hipLaunchKernelGGL((dispatch_backward_kernel<decltype(type), decltype(once)::value, kT>),
+                           dim3((unsigned)(N * a.slices)), dim3(kT), 0, st, a);
     });
     return launched();
 }
