@@ -261,11 +261,11 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
     constexpr int kSizeW = kRowsW * kP, kSize = kSizeW + kRowsX * kP;
     constexpr int kBytes = kP * 16;                           // of a row in a stage
     static_assert(kRowsW * kP % kThreads == 0 && kRowsX * kP % kThreads == 0, "every thread carries as many pieces");
-    static_assert(RING == 2 || RING == 3, "stages in LDS");
+    static_assert(RING >= 2 && RING <= 4, "stages in LDS");
     // a stage's weights, then its inputs; an array a stage, so that the compiler tells them apart
-    __shared__ u32x4 l0[kSize], l1[kSize], l2[RING > 2 ? kSize : 1];
+    __shared__ u32x4 l0[kSize], l1[kSize], l2[RING > 2 ? kSize : 1], l3[RING > 3 ? kSize : 1];
     __shared__ float sw[kRowsW], sx[kRowsX];
-    auto ring = [&](int i) -> u32x4 * { return i % RING == 0 ? l0 : (i % RING == 1 ? l1 : l2); };
+    auto ring = [&](int i) -> u32x4 * { return i % RING == 0 ? l0 : (i % RING == 1 ? l1 : (i % RING == 2 ? l2 : l3)); };
     __shared__ Plan plan;
     const int total = make_plan<kRowsX, kThreads>(a, plan) * a.ntiles;
     const int tid = threadIdx.x, lane = tid % kWave;
@@ -468,13 +468,44 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
     }
 }
 
-// Rows of a tile, for `each` rows an expert (masked pairs' among them: no more is known here): 32 (two workgroups on a
-// CU, the most weights on their way and the most tiles), 128 (three stages) or 256 (two; the fewest bytes for a
-// product). Measured with 64 experts, 7168 -> 4096 with SwiGLU, 1 / 16 / 32 / 64 / 128 / 160 / 256 rows each: 238, 347,
-// 372, 517, 794, 949 and 1407 us with 32 rows; 236, 348, 344, 356, 458, 514 and 701 with 128; 286, 408, 428, 437, 482,
-// 505 and 699 with 256. 8 experts of 1 row: 28, 33 and 53. 256 experts, 2048 -> 7168, 96 / 128 / 192 / 256 rows: 841,
-// 1049, 1408 and 1635 with 128, 992, 1050, 1180 and 1483 with 256.
-int tile_rows(int each) { return each <= 20 ? 32 : each <= 144 ? 128 : 256; }
+// Shapes of a tile: its rows and weight rows, the workgroups that run at once (two on a CU of the smallest), and what a
+// round of 256 such tiles costs, in eighths of 128 x 256. The large ones do most on what they fetch, the small ones
+// fill the card where there are few, and pad few rows.
+struct TileShape {
+    int rows, weights, threads, groups, cost;
+};
+constexpr TileShape kShapes[] = {{128, 256, 512, 256, 8}, {256, 256, 512, 256, 12}, {128, 128, 512, 256, 7},
+                                 {32, 128, 256, 512, 4}};
+
+// The shape whose rounds cost least, the first of several, were the rows even over the experts (masked pairs' among
+// them: no more is known here; an expert's last tile is half full). Measured over 2 to 64 experts of 4 to 1000 rows, k
+// 1152 to 7168 and n 400 to 4096, the choice costs 4 % over the best of seven shapes in the mean (a choice by an expert's
+// rows alone, 24 %). In us, for 256 x 256, 128 x 256, 128 x 128 and 32 x 128:
+//    2 experts,   4 rows each, 7168 -> 4096:    50   30   22   21
+//    2 experts, 250 rows each, 5376 -> 400:     50   30   19   13
+//    8 experts, 250 rows each, 1152 -> 1600:    19   14   12   24
+//   16 experts,  60 rows each, 7168 -> 4096:   108   91   90  119
+//   16 experts, 250 rows each, 7168 -> 4096:   207  172  183  332
+//   64 experts,   4 rows each, 7168 -> 4096:   368  308  309  306
+//   64 experts, 250 rows each, 1152 -> 1600:    63   74   76  152
+//   64 experts, 1000 rows each, 7168 -> 4096: 1828 2022 2393 4179
+int shape_of(int experts, int rows, int out_columns, bool glu)
+{
+    const long long hit = std::max(1, std::min(experts, rows)), each = rows / hit;
+    int best = 0;
+    long long least = LLONG_MAX;
+    for (int i = 0; i < (int)(sizeof kShapes / sizeof *kShapes); ++i) {
+        const TileShape &s = kShapes[i];
+        const int cols = s.weights / (glu ? 2 : 1);
+        const long long high = hit * std::max<long long>(2 * s.rows, 2 * each + s.rows) / (2 * s.rows);
+        const long long tiles = high * ((out_columns + cols - 1ll) / cols), cost = (tiles + 255) / 256 * s.cost;
+        if (cost < least) {
+            least = cost;
+            best = i;
+        }
+    }
+    return best;
+}
 
 int check_rows(long long rows, int cols, int dtype)
 {
@@ -589,13 +620,12 @@ int moe_expert_product_int8(const int8_t *x, const float *x_scales, const int8_t
     a.k = k;
     a.n = n;
     a.fo = glu ? n / 2 : n;
-    const int each = rows / a.E;                // rows of an expert, were they even
-    // rows and columns of a tile, and workgroups at a time
-    const int tall = tile_rows(each);
-    const int cols = (tall == 32 ? 128 : 256) / (glu ? 2 : 1), groups = tall == 32 ? 512 : 256;
-    a.ntiles = (a.fo + cols - 1) / cols;
+    const int shape = shape_of(a.E, rows, a.fo, glu);
+    const TileShape &tile = kShapes[shape];
+    const int cols = tile.weights / (glu ? 2 : 1), groups = tile.groups;
+    a.ntiles = (int)((a.fo + cols - 1ll) / cols);
     // a tile starts at every expert's first row, so at most this many
-    const long long mtiles = rows / tall + std::min(a.E, rows);
+    const long long mtiles = rows / tile.rows + std::min(a.E, rows);
     // rows and tiles are counted past the last one by up to a tile's height and a stride of the grid
     if (rows > INT_MAX - 256 || mtiles * a.ntiles > INT_MAX - groups) return MOE_ERR_SHAPE;
     if (rows == 0) return MOE_OK;
@@ -609,15 +639,16 @@ int moe_expert_product_int8(const int8_t *x, const float *x_scales, const int8_t
     a.ws = weight_scales;
     a.erc = ep_recv_count;
     a.out = out;
-    const dim3 g((unsigned)std::min<long long>(mtiles * a.ntiles, groups)), b(tall == 32 ? 256 : 512);
+    const dim3 g((unsigned)std::min<long long>(mtiles * a.ntiles, groups)), b(tile.threads);
     hipStream_t st = static_cast<hipStream_t>(stream);
     (void)hipGetLastError();
     auto launch = [&](auto type, auto act) {
         using T = decltype(type);
         constexpr bool kGlu = decltype(act)::value;
-        if (tall == 32) hipLaunchKernelGGL((expert_product_kernel<T, 2, 2, 1, 4, 3, kGlu>), g, b, 0, st, a);
-        else if (tall == 128) hipLaunchKernelGGL((expert_product_kernel<T, 4, 4, 2, 4, 3, kGlu>), g, b, 0, st, a);
-        else hipLaunchKernelGGL((expert_product_kernel<T, 8, 4, 2, 4, 2, kGlu>), g, b, 0, st, a);
+        if (shape == 0) hipLaunchKernelGGL((expert_product_kernel<T, 4, 4, 2, 4, 3, kGlu>), g, b, 0, st, a);
+        else if (shape == 1) hipLaunchKernelGGL((expert_product_kernel<T, 8, 4, 2, 4, 2, kGlu>), g, b, 0, st, a);
+        else if (shape == 2) hipLaunchKernelGGL((expert_product_kernel<T, 4, 2, 2, 4, 4, kGlu>), g, b, 0, st, a);
+        else hipLaunchKernelGGL((expert_product_kernel<T, 2, 2, 1, 4, 3, kGlu>), g, b, 0, st, a);
     };
     if (dtype == MOE_FP16 && glu) launch(F16(), std::true_type());
     else if (dtype == MOE_FP16) launch(F16(), std::false_type());

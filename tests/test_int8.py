@@ -261,8 +261,9 @@ def check(per_expert, W, k, n, act=NONE, dtype=torch.bfloat16, seed=0, spare=0, 
     x, xs, w, ws, counts = args = draw(per_expert, W, k, n, seed, spare, scaled, full)
     fo = n // 2 if act == SWIGLU else n
     out = torch.full((x.shape[0], fo), 7.0, dtype=dtype, device=DEV)
-    moe.expert_product_into(out, *on_gpu(args), activation=act)
-    got, f, row = out.cpu().double(), torch.finfo(dtype), 0
+    x, xs, w, ws, counts = args = on_gpu(args)
+    moe.expert_product_into(out, *args, activation=act)
+    got, f, row = out.double(), torch.finfo(dtype), 0
     for e, c in enumerate(per_expert):
         if c == 0:
             continue
@@ -296,6 +297,23 @@ def check(per_expert, W, k, n, act=NONE, dtype=torch.bfloat16, seed=0, spare=0, 
 @pytest.mark.parametrize("per_expert", [[20, 1], [100, 60], [300, 180]], ids=str)
 def test_int8_product_shapes(per_expert, act, k, n):
     check(per_expert, 2, k, n, act, seed=k + n)
+
+
+# Rows and columns by which a call takes each shape of a tile (rows x weight rows), with last tiles of every number of
+# fragments, and lengths of no, one, two, ... seven whole stages and a rest.
+TILES = {"256x256": ([2078, 2148, 2228, 2000], 4096), "128x256": ([100, 40, 128, 64, 65, 1, 0, 200, 129, 100, 96, 33] + [100] * 4, 7168),
+         "128x128": ([1000, 929, 1090, 0], 800), "32x128": ([31, 33, 64, 1], 1000)}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", [NONE, SWIGLU])
+@pytest.mark.parametrize("k", [48, 128, 272, 384, 640, 768, 1008])
+@pytest.mark.parametrize("tile", list(TILES))
+def test_int8_product_in_every_shape_of_a_tile(tile, k, act):
+    per_expert, n = TILES[tile]
+    check(per_expert, 2, k, n, act, seed=k, spare=5)
+    if k == 272:
+        check(per_expert, 2, k, n - 118, act, torch.float16, seed=1)      # a last tile of few columns
 
 
 @pytest.mark.gpu
@@ -341,9 +359,9 @@ def test_int8_product_of_the_longest_rows_at_the_largest_sum(rows):
 
 @pytest.mark.gpu
 def test_int8_product_rows_do_not_depend_on_each_other():
-    """An expert's rows by themselves and among many: all three heights of a tile give the same bits. Scales that are not
-    finite stay in their row or column."""
-    per, W, k, n = [30, 700, 5], 3, 656, 130
+    """An expert's rows by themselves and among many: all shapes of a tile give the same bits. Scales that are not finite
+    stay in their row or column."""
+    per, W, k, n = [30, 2500, 5], 3, 656, 4096
     x, xs, w, ws, counts = draw(per, W, k, n, 11)
     bad = xs.clone()
     bad[3], bad[100] = float("nan"), float("inf")
@@ -351,28 +369,28 @@ def test_int8_product_rows_do_not_depend_on_each_other():
     wbad[1, 7] = float("nan")
     for act in (NONE, SWIGLU):
         whole = moe.expert_product(*on_gpu((x, xs, w, ws, counts)), act)
-        for rows in ([30, 0, 0], [0, 40, 0], [0, 300, 0], [0, 700, 0], [0, 0, 5]):
+        for rows in ([30, 0, 0], [0, 40, 0], [0, 300, 0], [0, 1200, 0], [0, 2500, 0], [0, 0, 5]):
             e = int(np.argmax(rows))
             first = sum(per[:e])
             part = slice(first, first + rows[e])
             alone = moe.expert_product(*on_gpu((x[part].contiguous(), xs[part].contiguous(), w, ws, counts_for(rows, W, 1))), act)
             assert torch.equal(alone, whole[part]), (act, rows)
         got = moe.expert_product(*on_gpu((x, bad, w, wbad, counts)), act)
-        fine = torch.ones(735, whole.shape[1], dtype=torch.bool, device=DEV)
-        fine[3], fine[100], fine[30:730, 7] = False, False, False
-        assert torch.equal(got[fine], whole[fine]) and got[3].isnan().all() and got[30:730, 7].isnan().all()
+        fine = torch.ones(2535, whole.shape[1], dtype=torch.bool, device=DEV)
+        fine[3], fine[100], fine[30:2530, 7] = False, False, False
+        assert torch.equal(got[fine], whole[fine]) and got[3].isnan().all() and got[30:2530, 7].isnan().all()
         assert not torch.isfinite(got[100]).any() or act == SWIGLU
 
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("bad", ["negative", "descending", "huge"])
 def test_int8_product_stays_in_bounds_on_counts_it_should_not_get(bad):
-    for per in ([30, 70, 1, 20], [300, 700, 0, 20]):
-        x, xs, w, ws, counts = draw(per, 2, 160, 48, 3)
+    for per, n in [([30, 70, 1, 20], 48), *TILES.values()]:
+        x, xs, w, ws, counts = draw(per, 2, 160, n, 3)
         counts = {"negative": -counts, "descending": counts.flip(1).contiguous(),
                   "huge": torch.full_like(counts, 2 ** 31 - 1)}[bad]
         rows = x.shape[0]
-        whole = torch.full((rows + 64, 48), 7.0, dtype=torch.bfloat16, device=DEV)
+        whole = torch.full((rows + 64, n), 7.0, dtype=torch.bfloat16, device=DEV)
         moe.expert_product_into(whole[32:32 + rows], *on_gpu((x, xs, w, ws, counts)))
         assert (whole[:32] == 7.0).all() and (whole[32 + rows:] == 7.0).all()
 
