@@ -342,19 +342,25 @@ __global__ __launch_bounds__(THREADS) void combine_backward_kernel(CombineBackwa
         __syncthreads();
     }
     if (a.grad_ori && first == 0) {
+        // a token without copy pairs gets 0 whatever its gradient holds
         float w = 0.f;
+        bool mine = false;
         for (int k = lane; k < K; k += kWave)
-            if (rows.row[k] == kCopy) w += a.w[(size_t)t * K + k];
+            if (rows.row[k] == kCopy) {
+                w += a.w[(size_t)t * K + k];
+                mine = true;
+            }
         w = wave_sum(w);
+        const bool some = __builtin_amdgcn_ballot_w64(mine) != 0;
         uint16_t *o = a.grad_ori + (size_t)t * a.h;
         for (int c = tid; c < pieces; c += THREADS) {
             float x[kPiece];
             unpack<T>(*reinterpret_cast<const u32x4_a2 *>(g + c * kPiece), x);
 #pragma unroll
-            for (int j = 0; j < kPiece; ++j) x[j] = product(w, x[j]);
+            for (int j = 0; j < kPiece; ++j) x[j] = some ? product(w, x[j]) : 0.f;
             store16(o + c * kPiece, pack<T>(x));
         }
-        if (tid < tail) o[rest] = T::store(product(w, T::load(g[rest])));
+        if (tid < tail) o[rest] = T::store(some ? product(w, T::load(g[rest])) : 0.f);
     }
 }
 

@@ -338,7 +338,7 @@ int moe_combine_backward_workspace_size(int ep_world, int bs, int experts_per_ra
  *   grad_scales[t, k]        = sum over the columns of expand_x[row(t, k)] * g[t]; for a copy expert's pair of
  *                              ori_x[t] * g[t], for const expert j's of const_x[j] * g[t]; 0 for a zero expert's and for an
  *                              inactive pair, whatever their weights hold
- *   grad_ori_x[t]            = (sum over t's copy pairs of expert_scales[t, k]) * g[t]
+ *   grad_ori_x[t]            = (sum over t's copy pairs of expert_scales[t, k]) * g[t], 0 without copy pairs, whatever g[t] holds
  *   grad_const_x[j]          = sum over const expert j's pairs of expert_scales[t, k] * g[t]
  * fp32 throughout, each result rounded once. Where the combined rows were quantised on the way, the gradient is that of the
  * values that they stood for.

@@ -391,6 +391,33 @@ def test_values_in_places_that_do_not_count():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bs", [6, 400], ids=["workgroup a pair", "workgroup a token"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")], ids=str)
+@pytest.mark.parametrize("mask", ["pair", "token"])
+def test_a_padded_tokens_gradient_reaches_no_token_nor_const_expert(bs, bad, mask):
+    """What x_out's gradient holds at a token without active pairs (padding) flows back to nothing: neither its own
+    grad_ori_x nor the const experts' table, and dispatch's gradient adds 0."""
+    W, epr, K, h = 2, 2, 3, 77
+    N, E, special = W * bs, W * epr, (1, 1, 2)
+    ids, m, row, on = route(W, bs, epr, K, sum(special), mask, 12)
+    assist, counts = dispatched(ids, m, row, W, epr, sum(special))
+    v = inputs(ids, h, special, torch.bfloat16, 13)
+    clean, copy = v["g"].to(DEV), on & (ids == E + 1)
+    idle, d = ~on.any(1), {k: t.to(DEV) for k, t in v.items()}
+    assert idle.any() and copy.any() and (on.any(1) & ~copy.any(1)).any()
+    d["g"][idle.to(DEV)] = bad
+    kw = dict(x_active_mask=m.to(DEV), zero_experts=1, copy_experts=1, ori_x=d["x"], const_experts=2, const_x=d["cx"])
+    args = (d["y"], assist, counts, ids.to(DEV), d["w"], W, epr)
+    got, want = moe.combine_backward(d["g"], *args, **kw), moe.combine_backward(clean, *args, **kw)
+    A = int((row >= 0).sum())
+    assert torch.equal(got[0][:A], want[0][:A])
+    assert all(torch.equal(a, b) for a, b in zip(got[1:], want[1:]))
+    assert (got[2][~copy.any(1).to(DEV)] == 0).all() and torch.isfinite(got[2]).all()
+    back = [moe.dispatch_backward(r[0], assist, counts, ids.to(DEV), W, epr, m.to(DEV), r[2]) for r in (got, want)]
+    assert torch.equal(*back) and (back[0][idle.to(DEV)] == 0).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("h", [8, 61, 2056])
 def test_gradients_at_any_alignment_leave_the_neighbours_alone(h):
     W, bs, epr, K = 2, 9, 3, 4
