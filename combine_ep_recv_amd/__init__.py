@@ -178,7 +178,7 @@ def _check_tensor(name, t, dtype, shape, device):
 
 def _gpu_device(name, t):
     """The device of t, which must be a GPU tensor."""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise MoeError(name, MOE_ERR_SHAPE, "%s must be a tensor on a GPU" % name)
     return t.device
 
@@ -483,6 +483,7 @@ def _launch(name: str, device, *args):
 
 
 _FLOAT_CODES = {torch.float32: MOE_FP32, torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16}
+_HALF_CODES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16}
 
 
 def _float_code(name, dt: torch.dtype) -> int:
@@ -530,17 +531,18 @@ def combine_backward_workspace(ep_world, bs, experts_per_rank, h, topk, dtype: t
 
 def _row_call(fn, rows, expert_ids, ep_world, experts_per_rank):
     """(device, tokens, topk, h, dtype code) of a gradient call on dispatch's rows, its sizes checked."""
-    dev = _gpu_device("expert_ids", expert_ids)
-    _gpu_device("the rows", rows)
-    if rows.dim() != 2 or expert_ids.dim() != 2:
-        raise MoeError(fn, MOE_ERR_SHAPE, "the rows and expert_ids must be 2-D")
-    if rows.dtype not in (torch.float16, torch.bfloat16):
+    dev = _gpu_device("the rows", rows)
+    try:
+        (R, h), (N, K) = rows.shape, expert_ids.shape
+    except (AttributeError, ValueError):
+        raise MoeError(fn, MOE_ERR_SHAPE, "the rows and expert_ids must be 2-D tensors") from None
+    dt = _HALF_CODES.get(rows.dtype)
+    if dt is None:
         raise MoeError(fn, MOE_ERR_DTYPE, "gradients are fp16 or bf16, got %s" % rows.dtype)
-    N, K = expert_ids.shape
-    _check_int(fn, N | K | rows.shape[1] | ep_world | experts_per_rank)
-    if ep_world < 1 or N % ep_world or rows.shape[0] != N * K:
+    _check_int(fn, N | K | h | ep_world | experts_per_rank)
+    if ep_world < 1 or N % ep_world or R != N * K:
         raise MoeError(fn, MOE_ERR_SHAPE, "there must be ep_world*bs*topk rows")
-    return dev, N, K, rows.shape[1], _FLOAT_CODES[rows.dtype]
+    return dev, N, K, h, dt
 
 
 def _check_routing(assist_info, ep_recv_count, expert_ids, N, K, ep_world, experts_per_rank, device):
@@ -983,12 +985,15 @@ def dequantize_int8(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtyp
 # ---- the experts' product ----
 
 def _product_int8(out, x, x_scales, weights, weight_scales, ep_recv_count, activation):
-    """moe_expert_product_int8 of tensors on GPUs with the right numbers of dimensions."""
-    fn = "moe_expert_product_int8"
-    dev, (rows, k), (E, n), W = x.device, x.shape, weights.shape[:2], ep_recv_count.shape[0]
+    """moe_expert_product_int8 of rows x on a GPU."""
+    fn, dev = "moe_expert_product_int8", x.device
+    try:
+        (rows, k), (E, n, _), (W, _), dt = x.shape, weights.shape, ep_recv_count.shape, _HALF_CODES.get(out.dtype)
+    except (AttributeError, ValueError):
+        raise MoeError(fn, MOE_ERR_SHAPE, "x, weights and ep_recv_count must have 2, 3 and 2 dimensions") from None
     if W < 1 or E % W:
         raise MoeError(fn, MOE_ERR_SHAPE, "%d experts are not a multiple of %d ranks" % (E, W))
-    if out.dtype not in (torch.float16, torch.bfloat16):
+    if dt is None:
         raise MoeError(fn, MOE_ERR_DTYPE, "out must be fp16 or bf16, got %s" % out.dtype)
     _check_tensor("x", x, torch.int8, (rows, k), dev)
     if x_scales is not None:
@@ -999,8 +1004,7 @@ def _product_int8(out, x, x_scales, weights, weight_scales, ep_recv_count, activ
     _check_tensor("out", out, out.dtype, (rows, n // 2 if activation == MOE_ACT_SWIGLU else n), dev)
     _check_int(fn, W | E | rows | k | n | int(activation))
     _launch(fn, dev, x.data_ptr(), _address(x_scales), weights.data_ptr(), weight_scales.data_ptr(),
-            ep_recv_count.data_ptr(), W, E // W, rows, k, n, int(activation), dtype_code(out.dtype), out.data_ptr(),
-            _stream_ptr(dev))
+            ep_recv_count.data_ptr(), W, E // W, rows, k, n, int(activation), dt, out.data_ptr(), _stream_ptr(dev))
     return out
 
 
@@ -1010,14 +1014,14 @@ def expert_product_into(out: torch.Tensor, x: torch.Tensor, x_scales: Optional[t
     with MOE_ACT_SWIGLU) in fp16 or bf16, on the current stream. Rows behind the last that ep_recv_count counts are left as
     they were."""
     dev = _gpu_device("x", x)
+    if x.dtype == torch.int8:
+        return _product_int8(out, x, x_scales, weights, weight_scales, ep_recv_count, activation)
     _gpu_device("weights", weights)
     _gpu_device("ep_recv_count", ep_recv_count)
     _gpu_device("out", out)
     if x.dim() != 2 or weights.dim() != 3 or ep_recv_count.dim() != 2 or out.dim() != 2:
         raise MoeError("moe_expert_product", MOE_ERR_SHAPE,
                        "x, weights, ep_recv_count and out must have 2, 3, 2 and 2 dimensions")
-    if x.dtype == torch.int8:
-        return _product_int8(out, x, x_scales, weights, weight_scales, ep_recv_count, activation)
     element, (rows, k) = _mx_rows("x", x)
     E, n = weights.shape[:2]
     W, nb = ep_recv_count.shape[0], -(-k // MX_BLOCK)
