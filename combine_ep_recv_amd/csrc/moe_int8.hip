@@ -272,7 +272,7 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave), wm = wave / WN, wn = wave % WN;
     const int r = lane % 16, g = lane / 16;
     constexpr int kOut = GLU ? NF / 2 : NF, kOwn = NF * 16;   // output fragments and weight rows of a wavefront
-    const int half = a.n / 2, stages = a.k / kBytes;
+    const int half = a.n / 2, stages = (a.k + kBytes - 1) / kBytes;
     // piece p of row q in LDS
     auto place = [](int q, int p) { return q * kP + (p ^ (q & 7)); };
     // a reader's pieces in each step: of fragment 0; the weights' others lie 16 rows apart, the inputs' 16 * WM (so
@@ -285,6 +285,9 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
     }
     // the piece that this thread fetches of its rows (rows of its later pieces are a multiple of 8 on)
     const int piece = tid % kP ^ (tid / kP % 8);
+    // Of the inputs' last stage this thread's piece may lie behind the row: an offset past the buffer then, which brings
+    // zeros. (The weights' may too: of whatever comes there, times zeros.)
+    const uint32_t behind = (stages - 1) * kBytes + 16 * piece < a.k ? 0u : 1u << 31;
 
     // Each XCD (workgroups go to the eight in turn) begins an eighth of the stages further on, and after the last one
     // comes the first: the sums are whole numbers, whose order does not matter, and the XCDs read different memory at a
@@ -296,8 +299,8 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
         const int tile0 = t % a.ntiles * (WN * kOut * 16);
         const uint8_t *wb = a.w + (size_t)tile.expert * a.n * a.k, *xb = a.x + (size_t)tile.row * a.k;
         const __amdgpu_buffer_rsrc_t wbuf = buffer_of(wb, (uint64_t)a.n * a.k);
-        const __amdgpu_buffer_rsrc_t xbuf = buffer_of(xb, (uint64_t)(tile.end - tile.row) * a.k);
         const int last = tile.end - 1 - tile.row;             // rows past the expert's last read the last one
+        const __amdgpu_buffer_rsrc_t xbuf = buffer_of(xb, (uint64_t)(min(last, kRowsX - 1) + 1) * a.k);      // below 2^31
         // weight row of a place in the tile; columns past the last one read the last one's, and are not stored
         auto weight_row = [&](int q) -> uint32_t {
             const int c = GLU ? q / kOwn * (kOwn / 2) + q % (kOwn / 2) : q;
@@ -322,13 +325,14 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
         auto fetch = [&](auto loads, int stage, int slot, int from, int to) {
             int at = min(stage, stages - 1) + turn;
             at -= at >= stages ? stages : 0;
+            const uint32_t past = at == stages - 1 ? behind : 0u;
             u32x4 *wl = ring(slot), *xl = wl + kSizeW;
 #pragma unroll
             for (int i = from; i < to; ++i) {
                 if (i < kLoadsW)
                     fetch_lds(wbuf, wo[i], at * kBytes, wl + i * kThreads + wave * kWave);
                 else if (i - kLoadsW < decltype(loads)::value)
-                    fetch_lds(xbuf, xo[i - kLoadsW], at * kBytes, xl + (i - kLoadsW) * kThreads + wave * kWave);
+                    fetch_lds(xbuf, xo[i - kLoadsW] | past, at * kBytes, xl + (i - kLoadsW) * kThreads + wave * kWave);
             }
         };
         u32x4 wf[2][NF], xf[2][FR];
@@ -345,7 +349,7 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
                 acc[f][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, wf[i & 1][j]),
                                                                   __builtin_bit_cast(i32x4, xf[i & 1][f]), acc[f][j], 0, 0, 0);
         };
-        // Whole stages, for the first LIVE fragments of every wavefront: the others have no rows.
+        // All stages, for the first LIVE fragments of every wavefront: the others have no rows.
         auto whole = [&](auto count) {
             constexpr int LIVE = decltype(count)::value, LAST = 2;
             using Loads = std::integral_constant<int, (kLoadsX * LIVE + FR - 1) / FR>;
@@ -386,44 +390,18 @@ __global__ __launch_bounds__(WM *WN *kWave, 2) void expert_product_kernel(Produc
                 }
             }
         };
-        if (stages > 0) {
-            const int live = last / (WM * 16) + 1;            // fragments that hold rows of the expert
-            if constexpr (FR == 8) {
-                if (live > 6) whole(std::integral_constant<int, 8>());
-                else if (live > 4) whole(std::integral_constant<int, 6>());
-                else if (live > 2) whole(std::integral_constant<int, 4>());
-                else whole(std::integral_constant<int, 2>());
-            } else {
-                static_assert(FR == 2 || FR == 4, "the counts of fragments that the main loop is made for");
-                if (FR > 2 && live > 2) whole(std::integral_constant<int, FR>());
-                else whole(std::integral_constant<int, 2>());
-            }
+        const int live = last / (WM * 16) + 1;                // fragments that hold rows of the expert
+        if constexpr (FR == 8) {
+            if (live > 6) whole(std::integral_constant<int, 8>());
+            else if (live > 4) whole(std::integral_constant<int, 6>());
+            else if (live > 2) whole(std::integral_constant<int, 4>());
+            else whole(std::integral_constant<int, 2>());
+        } else {
+            static_assert(FR == 2 || FR == 4, "the counts of fragments that the main loop is made for");
+            if (FR > 2 && live > 2) whole(std::integral_constant<int, FR>());
+            else whole(std::integral_constant<int, 2>());
         }
         barrier_fetched<0>();
-        // the last k % kBytes elements, zeros behind them
-        if (stages * kBytes < a.k) {
-            const int at = stages * kBytes;
-#pragma unroll 1
-            for (int c = tid; c < kSize; c += kThreads) {
-                const bool is_w = c < kSizeW;
-                const int q = (is_w ? c : c - kSizeW) / kP, p = c % kP;
-                const uint8_t *from = is_w ? wb + (size_t)weight_row(q) * a.k : xb + (size_t)min(q, last) * a.k;
-                u32x4 v = {0, 0, 0, 0};
-                if (at + 16 * p < a.k) v = *reinterpret_cast<const u32x4 *>(from + at + 16 * p);
-                l0[(is_w ? 0 : kSizeW) + place(q, p)] = v;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int u = 0; u < kSub; ++u) {
-                read_w(u);
-#pragma unroll
-                for (int f = 0; f < FR; ++f) {
-                    read_x(u, f);
-                    multiply(u, f);
-                }
-            }
-            __syncthreads();
-        }
         // Results leave by way of LDS, 16 rows of the wavefront's columns at a time, so that neighbouring lanes store
         // neighbouring 16 bytes
         constexpr int kPitch = kOut * 32 + 16;                // bytes; 16 more than the columns, to spread the banks
