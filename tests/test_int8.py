@@ -302,7 +302,8 @@ def test_int8_product_shapes(per_expert, act, k, n):
 # Rows and columns by which a call takes each shape of a tile (rows x weight rows), with last tiles of every number of
 # fragments, and lengths of no, one, two, ... seven whole stages and a rest.
 TILES = {"256x256": ([2078, 2148, 2228, 2000], 4096), "128x256": ([100, 40, 128, 64, 65, 1, 0, 200, 129, 100, 96, 33] + [100] * 4, 7168),
-         "128x128": ([1000, 929, 1090, 0], 800), "32x128": ([31, 33, 64, 1], 1000)}
+         "128x128": ([1000, 929, 1090, 0], 800), "32x128": ([31, 33, 64, 1], 1000),         # 32x64 from k 512 on
+         "32x128 of long rows": ([31, 33, 64, 1], 4600)}
 
 
 @pytest.mark.gpu
@@ -314,6 +315,15 @@ def test_int8_product_in_every_shape_of_a_tile(tile, k, act):
     check(per_expert, 2, k, n, act, seed=k, spare=5)
     if k == 272:
         check(per_expert, 2, k, n - 118, act, torch.float16, seed=1)      # a last tile of few columns
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", [NONE, SWIGLU])
+@pytest.mark.parametrize("k", [512, 528, 656, 896, 1040, 2064, 7168])
+@pytest.mark.parametrize("per_expert", [[1, 0], [16, 17], [0, 32, 33, 3], [100, 2], [1] * 16], ids=str)
+def test_int8_product_of_few_tiles(per_expert, k, act):
+    check(per_expert, 2, k, 134, act, seed=k, spare=3)
+    check(per_expert, 2, k, 66, act, torch.float16, seed=k + 1, scaled=False)
 
 
 @pytest.mark.gpu
