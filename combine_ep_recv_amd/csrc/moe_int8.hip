@@ -253,7 +253,7 @@ struct ProductArgs {
 // for them, 1612 with the fetches alone; on zeros, which cost little power, 1835. So it is the fetches' way through the
 // caches and their energy, not their latency.
 template <class T, int FR, int NF, int WM, int WN, int RING, bool GLU>
-__global__ __launch_bounds__(WM *WN *kWave, WM *WN < 4 ? 1 : 2) void expert_product_kernel(ProductArgs a)
+__global__ __launch_bounds__(WM *WN *kWave, WM *WN < 8 ? 1 : 2) void expert_product_kernel(ProductArgs a)
 {
     constexpr int kThreads = WM * WN * kWave, kRowsW = WN * NF * 16, kRowsX = WM * FR * 16;
     constexpr int kSub = 2, kP = 4 * kSub;                    // steps, and 16-byte pieces of a row, in a stage
@@ -446,24 +446,25 @@ __global__ __launch_bounds__(WM *WN *kWave, WM *WN < 4 ? 1 : 2) void expert_prod
     }
 }
 
-// Shapes of a tile: its rows and weight rows, the workgroups that run at once (two on a CU of the small ones), and what a
+// Shapes of a tile: its rows and weight rows, the workgroups that run at once (two on a CU of the smallest), and what a
 // round of them costs, in sixteenths of 128 x 256, whole or with 256 tiles at most (one on a CU). The large ones do most
-// on what they fetch, the small ones fill the card where there are few, and pad few rows.
+// on what they fetch, the small ones fill the card where there are few, and pad few rows. (32 x 128 with four stages and
+// one workgroup on a CU: 34.5 us with two tokens of the case above, 36.7 with three stages and two.)
 struct TileShape {
     int rows, weights, threads, groups, cost, half, columns;     // columns: those of a row that it is worth while from
 };
 constexpr TileShape kShapes[] = {{128, 256, 512, 256, 16, 16, 0}, {256, 256, 512, 256, 24, 24, 0},
-                                 {128, 128, 512, 256, 12, 12, 0}, {32, 128, 256, 512, 12, 7, 0}, {32, 64, 128, 512, 10, 6, 512}};
+                                 {128, 128, 512, 256, 12, 12, 0}, {32, 128, 256, 256, 7, 7, 0}, {32, 64, 128, 512, 10, 6, 512}};
 
 // The shape whose rounds cost least, the first of several, were the rows even over the experts (masked pairs' among
-// them: no more is known here; an expert's last tile is half full). Measured over 190 drawn products of 2 to 64 experts,
-// k 144 to 7152 and n 132 to 4012, the choice costs 3 % over the best of seven shapes in the mean (the best shape for
+// them: no more is known here; an expert's last tile is half full). Measured over 204 products of 2 to 64 experts,
+// k 144 to 7168 and n 132 to 7168, the choice costs 3 % over the best of seven shapes in the mean (the best shape for
 // all of them 19 %). In us, for 256 x 256, 128 x 256, 128 x 128, 32 x 128 and 32 x 64:
-//    4 experts,   1 row each,  7168 -> 4096:    52   46   33   33   26
-//    2 experts,  14 rows each, 3760 -> 3444:    51   37   24   24   16
+//    4 experts,   1 row each,  7168 -> 4096:    75   46   33   32   26
+//    2 experts,  14 rows each, 3760 -> 3444:    56   40   24   23   15
 //    2 experts, 250 rows each, 5376 -> 400:     50   30   19   13
 //    8 experts, 250 rows each, 1152 -> 1600:    19   14   12   24
-//   16 experts,  21 rows each, 6992 -> 268:     92   70   41   41   27
+//   16 experts,  21 rows each, 6992 -> 268:     97   69   40   39   25
 //   16 experts,  60 rows each, 7168 -> 4096:   108   91   90  119
 //   16 experts, 250 rows each, 7168 -> 4096:   207  172  183  332
 //   64 experts,   4 rows each, 7168 -> 4096:   368  308  309  306
@@ -629,7 +630,7 @@ int moe_expert_product_int8(const int8_t *x, const float *x_scales, const int8_t
         if (shape == 0) hipLaunchKernelGGL((expert_product_kernel<T, 4, 4, 2, 4, 3, kGlu>), g, b, 0, st, a);
         else if (shape == 1) hipLaunchKernelGGL((expert_product_kernel<T, 8, 4, 2, 4, 2, kGlu>), g, b, 0, st, a);
         else if (shape == 2) hipLaunchKernelGGL((expert_product_kernel<T, 4, 2, 2, 4, 4, kGlu>), g, b, 0, st, a);
-        else if (shape == 3) hipLaunchKernelGGL((expert_product_kernel<T, 2, 2, 1, 4, 3, kGlu>), g, b, 0, st, a);
+        else if (shape == 3) hipLaunchKernelGGL((expert_product_kernel<T, 2, 2, 1, 4, 4, kGlu>), g, b, 0, st, a);
         else hipLaunchKernelGGL((expert_product_kernel<T, 2, 2, 1, 2, 4, kGlu>), g, b, 0, st, a);
     };
     if (dtype == MOE_FP16 && glu) launch(F16(), std::true_type());
