@@ -915,12 +915,9 @@ def _int8_rows(fn, x):
     """(device, shape, dtype code) of rows to quantise, checked."""
     dev = _gpu_device("x", x)
     shape = tuple(x.shape)
-    if not shape or shape[-1] < 1:
-        raise MoeError(fn, MOE_ERR_SHAPE, "x must have columns")
-    _check_int(fn, shape[-1])
-    dt = _float_code(fn, x.dtype)
-    _check_tensor("x", x, x.dtype, shape, dev)
-    return dev, shape, dt
+    if not shape or not 0 < shape[-1] < 1 << 31 or not x.is_contiguous():
+        raise MoeError(fn, MOE_ERR_SHAPE, "x must be contiguous, with 1 to 2^31 - 1 columns; got %s" % (shape,))
+    return dev, shape, _float_code(fn, x.dtype)
 
 
 def _quantize_int8(codes, scales, x, head):
@@ -953,9 +950,8 @@ def quantize_int8(x: torch.Tensor):
 def _dequantize_int8(out, codes, scales, dt):
     """moe_int8_dequantize into a checked (or new) out."""
     fn, dev, shape = "moe_int8_dequantize", out.device, tuple(codes.shape)
-    if not shape or shape[-1] < 1:
-        raise MoeError(fn, MOE_ERR_SHAPE, "codes must have columns")
-    _check_int(fn, shape[-1])
+    if not shape or not 0 < shape[-1] < 1 << 31:
+        raise MoeError(fn, MOE_ERR_SHAPE, "codes must have 1 to 2^31 - 1 columns")
     _check_tensor("codes", codes, torch.int8, shape, dev)
     _check_tensor("scales", scales, torch.float32, shape[:-1], dev)
     _launch(fn, dev, codes.data_ptr(), scales.data_ptr(), codes.numel() // shape[-1], shape[-1], dt, out.data_ptr(),
