@@ -145,6 +145,9 @@ __device__ __forceinline__ u32x4 pack(const float (&x)[kPiece])
 // parts. These workgroups come first in combine's launch (a launch of their own is 8 us more with 4 ranks of 515
 // tokens).
 constexpr int kMostSplits = 64, kSplitTokens = 32, kAhead = 8;
+// Tokens of a part that are added by themselves, before their sum goes to the part's: a part has up to 2^18 tokens, and
+// fp32 sums of so many like terms one after the other are off by 0.35 % (seven half steps of fp16), by 0.01 % so.
+constexpr int kBlockTokens = 1024;
 
 struct ConstArgs {
     const uint16_t *grad;
@@ -177,9 +180,11 @@ __device__ __forceinline__ void const_backward(const ConstArgs &a, int block, Co
     const int live = at >= a.h ? 0 : min(a.h, kPiece);
     const long long col = max(min(at, (long long)a.h - kPiece), 0ll);
     const long long from = (long long)split * a.per * a.K, to = min((long long)a.N, (long long)(split + 1) * a.per) * a.K;
-    float acc[kPiece];
+    float acc[kPiece], sum[kPiece];
 #pragma unroll
-    for (int i = 0; i < kPiece; ++i) acc[i] = 0.f;
+    for (int i = 0; i < kPiece; ++i) acc[i] = sum[i] = 0.f;
+    static_assert(kBlockTokens % kScan == 0, "lists end where blocks do");
+    int left = kBlockTokens * a.K;
     for (long long base = from; base < to; base += kScan) {
         uint64_t hit[4];
         bool mine[4];
@@ -237,13 +242,22 @@ __device__ __forceinline__ void const_backward(const ConstArgs &a, int block, Co
                 }
             }
         }
+        left -= kScan;
+        if (left == 0 || base + kScan >= to) {
+#pragma unroll
+            for (int c = 0; c < kPiece; ++c) {
+                sum[c] += acc[c];
+                acc[c] = 0.f;
+            }
+            left = kBlockTokens * a.K;
+        }
         __syncthreads();
     }
 #pragma unroll
     for (int c = 0; c < kPiece; ++c) {
         if (c >= live) continue;
-        if (a.sums) a.sums[((size_t)j * a.splits + split) * a.h + col + c] = acc[c];
-        else a.out[(size_t)j * a.h + col + c] = T::store(acc[c]);
+        if (a.sums) a.sums[((size_t)j * a.splits + split) * a.h + col + c] = sum[c];
+        else a.out[(size_t)j * a.h + col + c] = T::store(sum[c]);
     }
 }
 
