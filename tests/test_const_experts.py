@@ -1,5 +1,5 @@
-"""The gradient of const_x where a const expert has many pairs: sums within the bound of their longest chain, and batches so
-long that a plain fp32 sum would lose digits."""
+"""The gradient of const_x where a const expert has many pairs: lists that are made in several pieces, whose sums are
+compared exactly or with the bound of their longest chain, and batches so long that a plain fp32 sum would lose digits."""
 import pytest
 import torch
 
@@ -55,6 +55,22 @@ LONG = [
     (2, 1100, 1, 2, 2049, 2, 0.8),         # 70, in a list that is not full
     (2, 6, 2, 4, 4100, 2, 0.8),            # one part
 ]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("shape", LONG, ids=str)
+def test_every_pair_of_a_const_expert_counts_once(shape, dtype):
+    """Small whole numbers, none of them 0: their sums are exact, so a pair left out or taken twice shows."""
+    W, bs, epr, K, h, const, on = shape
+    N, E = W * bs, W * epr
+    g, ids, mask, *dispatched = route(W, bs, epr, K, const, on, 3)
+    whole = lambda *s: torch.tensor([-2, -1, 1, 2], device=DEV)[torch.randint(0, 4, s, generator=g, device=DEV)]
+    w, grad = whole(N, K).float(), whole(N, h).to(dtype)
+    got = gradient(W, bs, epr, K, h, const, dtype, ids, mask, *dispatched, w, grad)
+    share, hit = shares(ids, mask, w, E, const)
+    assert (hit.sum(0) >= on * N - 4 * N ** 0.5).all()
+    assert torch.equal(got, (share @ grad.double()).to(dtype))
 
 
 @pytest.mark.gpu
