@@ -1046,7 +1046,9 @@ def expert_product(x: torch.Tensor, x_scales: Optional[torch.Tensor], weights: t
     Either x, x_scales: microscaled rows [rows, k], from dispatch under MOE_QUANT_MX or from quantize_mx;
     weights, weight_scales: quantize_mx of [E, n, k] in E2M1. Or x int8 [rows, k] and x_scales fp32 [rows],
     from dispatch under MOE_QUANT_DYN_TOKEN or from quantize_int8 (x_scales None: 1, for dispatch's rows under
-    MOE_QUANT_STATIC); weights, weight_scales: quantize_int8 of [E, n, k], int8 and fp32 [E, n].
+    MOE_QUANT_STATIC); weights, weight_scales: quantize_int8 of [E, n, k], int8 and fp32 [E, n]. Static rows stand
+    for code / coefficient: one coefficient divides weight_scales; those of the columns, quant_scales [k] or [E, k],
+    divide the weights before these are quantised, quantize_int8(w / c[..., None, :]).
     ep_recv_count: dispatch's. Returns [rows, n], or with MOE_ACT_SWIGLU [rows, n / 2]: silu(first n / 2
     weight rows) * the others. Rows behind the last counted one are uninitialised.
     """

@@ -511,8 +511,11 @@ int moe_int8_dequantize(const int8_t *codes, const float *scales, int64_t rows, 
  * are fp32, rounded once.
  *  x              int8 [rows, k], 16-byte aligned: dispatch's expand_x under MOE_QUANT_DYN_TOKEN or MOE_QUANT_STATIC, or
  *                 moe_int8_quantize's codes
- *  x_scales       fp32 [rows], or NULL for 1 (static rows, whose coefficient goes into the weights' scales)
- *  weights        int8 [E, n, k], 16-byte aligned; weight_scales fp32 [E, n]: moe_int8_quantize of the E * n weight rows
+ *  x_scales       fp32 [rows], or NULL for 1 (MOE_QUANT_STATIC's rows)
+ *  weights        int8 [E, n, k], 16-byte aligned; weight_scales fp32 [E, n]: moe_int8_quantize of the E * n weight rows. For
+ *                 MOE_QUANT_STATIC's rows, whose codes stand for code / c: a single coefficient c divides weight_scales;
+ *                 coefficients of the columns (h, or E * h of them) differ along k and cannot leave the sum, so the weights
+ *                 are divided by them before they are quantised, w[e, i, k] / c[k] or w[e, i, k] / c[e, k]
  *  ep_recv_count  [W, S] int32: dispatch's, unchanged
  *  out            [rows, n], or [rows, n / 2] with MOE_ACT_SWIGLU, fp16 or bf16 (dtype). Rows behind the last that
  *                 ep_recv_count counts are left as they were
