@@ -351,9 +351,9 @@ int moe_combine_backward_workspace_size(int ep_world, int bs, int experts_per_ra
  *  grad_const_x   [const_expert_num, h] dtype, every element written, or NULL; NULL without const experts
  *  workspace      device scratch of at least the queried size, 16-byte aligned; NULL where that is 0
  * Outputs overlap no input. Any alignment to the elements' size is taken. Ranges as in moe_dispatch; with grad_const_x, const
- * experts times 64 times ceil(h / 512), plus the tokens (at least 4096), below 2^24 (larger ones as far as the launch
- * allows). Rows are found from ep_recv_count and the tokens in
- * assist_info, which are dispatch's, unchanged; otherwise the kernels stay in bounds and the outputs are unspecified.
+ * experts times 64 times ceil(h / 512), plus the tokens (at least 1024), below 2^24 (larger ones as far as the launch
+ * allows). Rows are found from ep_recv_count and the tokens in assist_info, which are dispatch's, unchanged; otherwise the
+ * kernels stay in bounds and the outputs are unspecified.
  * Bitwise deterministic, and the first three outputs' rows do not depend on how many tokens there are.
  */
 int moe_combine_backward(const void *grad_out, const void *expand_x, const int32_t *assist_info,
