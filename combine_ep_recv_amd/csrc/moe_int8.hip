@@ -21,7 +21,6 @@ constexpr int kRowThreads = 256;
 constexpr long long kOnceBytes = 256ll << 20;      // the Infinity Cache
 
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 // --------------------------------------------------------------------------
