@@ -139,7 +139,8 @@ __device__ __forceinline__ float row_max(float v, float (&part)[kRowThreads / kW
 //
 // Memory bounds it: 3 bytes an element of 16 bits, against some twelve instructions. bf16 [32768, 7168] 115 us, 6.1
 // TB/s of 0.7 GB; [256, 2048] 3 us. Lanes by the row's pieces: 16 (four rows a wavefront), 64, or the workgroup's 256
-// above 256 pieces: a wavefront that holds 448 pieces, 7 a lane, takes 173 us for 115.
+// above 256 pieces: a wavefront that holds 448 pieces, 7 a lane, takes 173 us for 115. fp32 rows, which are divided in full,
+// 285 us, 4.1 TB/s of 1.2 GB (weights, 256 x 4096 rows of 7168: 9.0 ms for 37.6 GB; [4096, 7168] 28 us).
 template <class T, int LANES, int J, bool ONCE>
 __global__ __launch_bounds__(kRowThreads) void quantize_kernel(RowsArgs a)
 {
@@ -249,8 +250,9 @@ struct ProductArgs {
 // (1024 a rank, 8 ranks): 1721 to 1830 us, 2.1 to 2.2 POP/s, where the instruction alone reaches 4.2 on such values and
 // 4.8 on constants. Power takes the clock to 1.6 GHz; of those cycles the matrix units are busy in 61 % and LDS reads
 // in 26 %. Cut down (from 2080 us): 1475 without fetches, 1745 with fetches that hit the cache, 2086 without waiting
-// for them, 1612 with the fetches alone; on zeros, which cost little power, 1835. So it is the fetches' way through the
-// caches and their energy, not their latency.
+// for them, 1612 with the fetches alone; on zeros, which cost little power, 1835. So of what it takes beyond the instructions'
+// own 917 us, about half is LDS reads, issue and their power (the loop without fetches), the other half the fetches' way
+// through the caches and their energy, not their latency.
 template <class T, int FR, int NF, int WM, int WN, int RING, bool GLU>
 __global__ __launch_bounds__(WM *WN *kWave, WM *WN < 8 ? 1 : 2) void expert_product_kernel(ProductArgs a)
 {
@@ -456,19 +458,20 @@ constexpr TileShape kShapes[] = {{128, 256, 512, 256, 16, 16, 0}, {256, 256, 512
                                  {128, 128, 512, 256, 12, 12, 0}, {32, 128, 256, 256, 7, 7, 0}, {32, 64, 128, 512, 10, 6, 512}};
 
 // The shape whose rounds cost least, the first of several, were the rows even over the experts (masked pairs' among
-// them: no more is known here; an expert's last tile is half full). Measured over 204 products of 2 to 64 experts,
-// k 144 to 7168 and n 132 to 7168, the choice costs 3 % over the best of seven shapes in the mean (the best shape for
-// all of them 19 %). In us, for 256 x 256, 128 x 256, 128 x 128, 32 x 128 and 32 x 64:
-//    4 experts,   1 row each,  7168 -> 4096:    75   46   33   32   26
-//    2 experts,  14 rows each, 3760 -> 3444:    56   40   24   23   15
-//    2 experts, 250 rows each, 5376 -> 400:     50   30   19   13
-//    8 experts, 250 rows each, 1152 -> 1600:    19   14   12   24
-//   16 experts,  21 rows each, 6992 -> 268:     97   69   40   39   25
-//   16 experts,  60 rows each, 7168 -> 4096:   108   91   90  119
-//   16 experts, 250 rows each, 7168 -> 4096:   207  172  183  332
-//   64 experts,   4 rows each, 7168 -> 4096:   368  308  309  306
-//   64 experts, 250 rows each, 1152 -> 1600:    63   74   76  152
-//   64 experts, 1000 rows each, 7168 -> 4096: 1828 2022 2393 4179
+// them: no more is known here; an expert's last tile is half full). Measured over 200 products of 2 to 64 experts, 1 to 1000
+// rows each, k 144 to 7168 and n 132 to 7168, half of them with SwiGLU, the choice costs 1.4 % over the best of the five in
+// the mean and 30 % at most (128 x 128 for all of them 18 % in the mean). In us, for 256 x 256, 128 x 256, 128 x 128, 32 x
+// 128 and 32 x 64, on inputs that change from pass to pass:
+//    4 experts,   1 row each,  7168 -> 4096:    75   48   37   35   28
+//    2 experts,  14 rows each, 3760 -> 3444:    55   40   24   23   15
+//    2 experts, 250 rows each, 5376 -> 400:     51   32   21   15   14
+//    8 experts, 250 rows each, 1152 -> 1600:    23   16   13   28   29
+//   16 experts,  21 rows each, 6992 -> 268:     93   66   40   39   25
+//   16 experts,  60 rows each, 7168 -> 4096:   101   87   88  116  122
+//   16 experts, 250 rows each, 7168 -> 4096:   129  138  169  386  354
+//   64 experts,   4 rows each, 7168 -> 4096:   357  312  314  310  312
+//   64 experts, 250 rows each, 1152 -> 1600:    55   68   74  164  174
+//   64 experts, 1000 rows each, 7168 -> 4096: 1685 1898 2335 4566 4210
 int shape_of(int experts, int rows, int k, int out_columns, bool glu)
 {
     const long long hit = std::max(1, std::min(experts, rows)), each = rows / hit;
