@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import combine_ep_recv_amd as moe
+import test_gradients as tg
 
 DEV = "cuda"
 U = 2.0 ** -24
@@ -112,3 +113,14 @@ def test_a_long_batch_of_like_gradients_loses_no_digits():
     room = 1.01 * (BLOCK + -(-N // PARTS // BLOCK) + PARTS) * U * ref
     assert ((got - ref).abs() <= room + torch.finfo(dtype).eps / 2 * (ref + room)).all()
     torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=str)
+def test_skewed_routing_with_pairs_of_every_special_expert(dtype):
+    W, bs, epr, K, h, special, mask, skew = shape = (2, 700, 4, 3, 264, (1, 1, 2), "pair", 0.2)
+    ids, _, _, on = tg.route(W, bs, epr, K, sum(special), mask, 5, skew)
+    hits = torch.bincount(ids[on].long(), minlength=W * epr + sum(special))
+    assert hits[0] > 500 and (hits[W * epr:] > 20).all()
+    tg.test_combine_backward(shape, dtype)
+    tg.test_dispatch_backward(shape, dtype)
